@@ -1,0 +1,610 @@
+"""What a MoE block needs around its expert MLP, as measured cases.
+
+Four operators and their gradients:
+
+* ``route``:   top-k of the router's logits with the softmax over the selected ones;
+* ``permute``: tokens sorted by expert (``side="in"``) and back with the routing
+  weights applied (``side="out"``);
+* ``linear``:  the product of expert-sorted rows with a stored weight stack, with
+  bias, activation and residual in its epilogue (one expert: a dense projection);
+* ``norm``:    the RMS norm after a block, its gate and residual scale, and the RMS
+  norm before the next block.
+
+``run`` computes them in elementary torch operations in 32 bits, or, where ``own``
+is set, through the library's entry points. ``exact`` computes them in 64 bits.
+"""
+
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+_NF4 = (-1.0, -0.6961928009986877, -0.5250730514526367, -0.39491748809814453, -0.28444138169288635,
+        -0.18477343022823334, -0.09105003625154495, 0.0, 0.07958029955625534, 0.16093020141124725,
+        0.24611230194568634, 0.33791524171829224, 0.44070982933044434, 0.5626170039176941,
+        0.7229568362236023, 1.0)
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+_FP8 = tuple((i * 2.0 ** -9 if i < 8 else (1 + (i & 7) / 8) * 2.0 ** ((i >> 3) - 7)) / 480 for i in range(128))
+_BITS = {"nf4": 4.5, "mxfp4": 4.25, "fp8": 8.5, "bf16": 16.0}  # stored bits a weight, scales included
+
+
+# ---- cases ----
+
+def _route(T, E, k, way, masked=False, **kw):
+    return dict(op="route", T=T, E=E, k=k, way=way, masked=masked, **kw)
+
+
+def _permute(T, E, k, H, side, way, dtype="bf16", skew=0.0, drop=0.0, **kw):
+    return dict(op="permute", T=T, E=E, k=k, H=H, side=side, way=way, dtype=dtype, skew=skew, drop=drop, **kw)
+
+
+def _linear(rows, E, touched, inn, out, codebook, act, way, bias=True, residual=False, y="bf16", tail=0, skew=0.0, **kw):
+    return dict(op="linear", rows=rows, E=E, touched=touched, inn=inn, out=out, codebook=codebook, act=act, way=way,
+                bias=bias, residual=residual, y=y, tail=tail, skew=skew, **kw)
+
+
+def _norm(T, H, way, dtype="bf16", block=True, post=True, gate="none", pre=True, **kw):
+    return dict(op="norm", T=T, H=H, way=way, dtype=dtype, block=block, post=post, gate=gate, pre=pre, **kw)
+
+
+def listed():
+    return [
+        # the router of a 128-expert layer while eight sequences each decode a token
+        _route(8, 128, 8, "forward", name="route, 8 tokens"),
+        # the same router over a prefill batch, with the gradient of its logits
+        _route(16384, 128, 8, "step", name="route, 16384 tokens, step"),
+        # the rows of one decode step put in expert order
+        _permute(8, 128, 8, 2048, "in", "forward", skew=1.0, name="permute, 8 tokens"),
+        # a training microbatch of a 64-expert layer into expert order, and its gradient
+        _permute(4096, 64, 8, 2048, "in", "step", name="permute, 4096 x 8, step"),
+        # expert outputs of a wide 8-expert layer back into token order with their weights, and the gradients
+        _permute(8192, 8, 2, 4096, "out", "step", name="unpermute, 8192 x 2, step"),
+        # the router's projection of a decode step: fp32 logits from a bf16 matrix
+        _linear(8, 1, 1, 2048, 128, "bf16", "none", "forward", y="fp32", name="router product, 8 rows"),
+        # the first expert product of that decode step: 64 pairs on 40 of 128 experts
+        _linear(64, 128, 40, 2048, 1536, "nf4", "silu", "forward", skew=1.0, name="expert product, 64 rows"),
+        # a dense projection of a prefill chunk, added to the residual stream
+        _linear(2048, 1, 1, 2048, 4096, "nf4", "gelu", "forward", residual=True, name="dense product, 2048 rows"),
+        # a training step through one expert product of the 64-expert layer
+        _linear(32768, 64, 64, 2048, 2048, "nf4", "silu", "step", name="expert product, 32768 rows, step"),
+        # between two blocks while one token decodes
+        _norm(1, 4096, "forward", name="norms, 1 token"),
+        # between two blocks of a training microbatch, each token with a gate of its own
+        _norm(4096, 2048, "step", gate="token", name="norms, 4096 x 2048, step"),
+        # a ragged batch with the residual stream in fp32 and a scale for each channel
+        _norm(8191, 4096, "step", dtype="fp32", gate="channel", name="norms, 8191 x 4096 fp32, step"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("route", "permute", "linear", "norm"))
+    way = rng.choice(("forward", "step"))
+    if op == "route":
+        E = _log(rng, 4, 512)
+        return _route(_log(rng, 1, 16384), E, rng.randint(1, min(E, 16)), way, masked=rng.random() < 0.3)
+    if op == "permute":
+        k, H = rng.randint(1, 8), rng.choice((64 * rng.randint(1, 64), rng.randint(33, 4095)))
+        T = _log(rng, 1, max(2, 16384 // k))
+        return _permute(T, _log(rng, 2, 256), k, H, rng.choice(("in", "out")), way, rng.choice(("bf16", "fp32")),
+                        rng.choice((0.0, 1.0)), rng.choice((0.0, 0.0, 0.3)))
+    if op == "linear":
+        inn, out = 64 * _log(rng, 1, 64), rng.choice((64 * _log(rng, 1, 48), rng.randint(17, 2049)))
+        E = rng.choice((1, _log(rng, 2, 128)))
+        rows = _log(rng, 1, 8192)
+        return _linear(rows, E, rng.randint(1, min(E, rows)), inn, out, rng.choice(("nf4", "mxfp4", "fp8", "bf16")),
+                       rng.choice(("none", "relu", "silu", "gelu", "gelu_tanh")), way, rng.random() < 0.7,
+                       rng.random() < 0.4, rng.choice(("bf16", "bf16", "fp32")),
+                       rng.choice((0, rng.randint(1, 40))), rng.choice((0.0, 1.0)))
+    H = rng.choice((64 * rng.randint(1, 64), rng.randint(33, 4095)))
+    block = rng.random() < 0.8
+    post = block and rng.random() < 0.6
+    pre = not block or rng.random() < 0.7
+    return _norm(_log(rng, 1, 8192), H, way, rng.choice(("bf16", "fp32")), block, post,
+                 rng.choice(("none", "token", "channel")) if block else "none", pre)
+
+
+# ---- inputs ----
+
+_T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def _expert_probs(E, skew, g):
+    p = 1.0 / torch.arange(1, E + 1, device=DEV, dtype=torch.float64) ** skew
+    return p[torch.randperm(E, generator=g, device=DEV)]
+
+
+def _expert_ids(c, g):
+    """Distinct experts a token (ids of one token are drawn without replacement where E allows it);
+    a dropped pair has id -1, as a pair whose expert lives on another rank has."""
+    p = _expert_probs(c["E"], c["skew"], g).log()
+    u = torch.rand(c["T"], c["E"], generator=g, device=DEV, dtype=torch.float64).clamp_(1e-12)
+    s = p - torch.log(-torch.log(u))
+    k = c["k"]
+    ids = s.argsort(dim=1, descending=True)[:, :min(k, c["E"])].to(torch.int32)
+    if k > c["E"]:
+        ids = torch.cat([ids] * -(-k // c["E"]), dim=1)[:, :k].contiguous()
+    if c["drop"]:
+        ids = torch.where(torch.rand(ids.shape, generator=g, device=DEV) < c["drop"], torch.full_like(ids, -1), ids)
+    return ids.contiguous()
+
+
+def _plan(ids, E):
+    """(offsets [E + 1], sorted pairs [P], place of each pair [T, k]): pairs by expert, in token
+    order within one; pairs of no expert come last."""
+    flat = ids.reshape(-1).to(torch.int64)
+    key = torch.where((flat >= 0) & (flat < E), flat, torch.full_like(flat, E))
+    order = torch.argsort(key, stable=True)
+    pos = torch.empty_like(order)
+    pos[order] = torch.arange(order.numel(), device=order.device)
+    counts = torch.zeros(E + 1, dtype=torch.int64, device=flat.device).scatter_add_(0, key, torch.ones_like(key))
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64, device=flat.device), counts[:E].cumsum(0)])
+    return offsets.to(torch.int32), order.to(torch.int32), pos.to(torch.int32).reshape(ids.shape)
+
+
+def prepare(case, seed):
+    c = case
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def randn(*shape, dtype=torch.float32, scale=1.0):
+        return torch.randn(*shape, generator=g, device=DEV).mul_(scale).to(dtype)
+
+    s = dict(c)
+    if c["op"] == "route":
+        s["logits"] = randn(c["T"], c["E"])
+        if c["masked"]:
+            # experts that are out of service for a token; a padding token has none at all
+            m = torch.rand(c["T"], c["E"], generator=g, device=DEV) < 0.4
+            m[torch.rand(c["T"], generator=g, device=DEV) < 0.1] = True
+            s["logits"].masked_fill_(m, -math.inf)
+        s["grad_w"] = randn(c["T"], c["k"])
+    elif c["op"] == "permute":
+        dt, P = _T[c["dtype"]], c["T"] * c["k"]
+        s["ids"] = _expert_ids(c, g)
+        s["w"] = torch.softmax(randn(c["T"], c["k"]), dim=1)
+        s["x"] = randn(c["T"], c["H"], dtype=dt) if c["side"] == "in" else None
+        s["rows"] = randn(P, c["H"], dtype=dt) if c["side"] == "out" else None
+        s["plan"] = _plan(s["ids"], c["E"]) if c["side"] == "out" else None
+        s["grad"] = randn(P if c["side"] == "in" else c["T"], c["H"], dtype=dt)
+    elif c["op"] == "linear":
+        E, inn, out, rows = c["E"], c["inn"], c["out"], c["rows"]
+        s["packed"], s["absmax"], s["scales"] = _stored(c, g)
+        s["table"] = _table(c["codebook"])
+        # every touched expert has a row, the others follow the skew
+        p = _expert_probs(c["touched"], c["skew"], g)
+        more = torch.multinomial(p, max(rows - c["touched"], 1), replacement=True, generator=g)[:rows - c["touched"]]
+        per = torch.bincount(more, minlength=c["touched"]) + 1
+        counts = torch.zeros(E, dtype=torch.int64, device=DEV)
+        counts[torch.randperm(E, generator=g, device=DEV)[:c["touched"]]] = per
+        s["live"] = counts.nonzero()[:, 0]  # the touched experts
+        s["offsets"] = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32) if E > 1 or c["tail"] else None
+        s["cap"] = int(counts.max())
+        R = rows + c["tail"]
+        s["x"] = randn(R, inn, dtype=torch.bfloat16)
+        s["bias"] = randn(E, out, scale=0.1) if c["bias"] else None
+        s["residual"] = randn(R, out, dtype=torch.bfloat16) if c["residual"] else None
+        s["grad_y"] = randn(R, out, dtype=_T[c["y"]])
+    else:
+        T, H, dt = c["T"], c["H"], _T[c["dtype"]]
+        s["x"] = randn(T, H, dtype=dt)
+        s["y"] = randn(T, H, dtype=torch.bfloat16, scale=0.5) if c["block"] else None
+        s["w_post"] = 1 + randn(H, scale=0.1) if c["post"] else None
+        s["w_pre"] = 1 + randn(H, scale=0.1) if c["pre"] else None
+        s["gate_v"] = {"none": None, "token": torch.sigmoid(randn(T)), "channel": randn(H, scale=0.3)}[c["gate"]]
+        s["scale"] = 0.7 if c["block"] else 1.0
+        s["grad_r"] = randn(T, H, dtype=dt)
+        s["grad_h"] = randn(T, H, dtype=torch.bfloat16) if c["pre"] else None
+    return s
+
+
+def _stored(c, g):
+    """A stored stack: (packed codes or values, fp32 absmax or None, E8M0 scales or None)."""
+    E, n, cb = c["E"], c["out"] * c["inn"], c["codebook"]
+    if cb == "bf16":
+        w = torch.randn(E, n, generator=g, device=DEV).mul_(0.02).to(torch.bfloat16)
+        return w.view(torch.uint8), None, None
+    nbytes = n if cb == "fp8" else n // 2
+    packed = torch.randint(0, 256, (E, nbytes), generator=g, device=DEV, dtype=torch.uint8)
+    if cb == "mxfp4":
+        return packed, None, torch.randint(118, 123, (E, n // 32), generator=g, device=DEV, dtype=torch.uint8)
+    return packed, torch.rand(E, n // 64, generator=g, device=DEV).mul_(0.04).add_(0.02), None
+
+
+def _table(cb):
+    """What each stored byte stands for, without its scale: one value (fp8) or two (4-bit codes, high nibble first)."""
+    if cb == "bf16":
+        return None
+    if cb == "fp8":
+        v = [[x] for x in _FP8 + tuple(-x for x in _FP8)]
+    else:
+        t = _NF4 if cb == "nf4" else _E2M1 + tuple(-x for x in _E2M1)
+        v = [[t[b >> 4], t[b & 15]] for b in range(256)]
+    return torch.tensor(v, device=DEV, dtype=torch.float32)
+
+
+# ---- the plain forms ----
+
+def _weights(s):
+    """[E, out, in]: the bf16 view of the stored weights, in fp32."""
+    out, inn, cb, p = s["out"], s["inn"], s["codebook"], s["packed"]
+    E = p.shape[0]
+    if cb == "bf16":
+        return p.view(torch.bfloat16).float().view(E, out, inn)
+    v = s["table"][p.to(torch.int64)].view(E, out * inn)
+    if cb == "mxfp4":
+        v = torch.ldexp(v.view(E, -1, 32), (s["scales"].to(torch.int32) - 127)[..., None])
+    else:
+        v = v.view(E, -1, 64) * s["absmax"][..., None]
+    return v.to(torch.bfloat16).float().view(E, out, inn)
+
+
+def _act(name, z):
+    """(act(z), act'(z))"""
+    if name == "none":
+        return z, torch.ones_like(z)
+    if name == "relu":
+        return z * (z > 0), (z > 0).to(z.dtype)
+    if name == "silu":
+        sg = 1 / (1 + torch.exp(-z))
+        return z * sg, sg * (1 + z * (1 - sg))
+    if name == "gelu":
+        cdf = 0.5 * (1 + torch.erf(z * math.sqrt(0.5)))
+        return z * cdf, cdf + z * torch.exp(-0.5 * z * z) * (1 / math.sqrt(2 * math.pi))
+    a, b = math.sqrt(2 / math.pi), 0.044715
+    th = torch.tanh(a * (z + b * z * z * z))
+    return 0.5 * z * (1 + th), 0.5 * (1 + th) + 0.5 * z * (1 - th * th) * a * (1 + 3 * b * z * z)
+
+
+def _plain_route(s):
+    val, idx = torch.sort(s["logits"], dim=1, descending=True, stable=True)
+    val, idx = val[:, :s["k"]], idx[:, :s["k"]]
+    z = torch.where(val == -math.inf, torch.zeros_like(val), torch.exp(val - val[:, :1]))
+    tot = z.sum(1, keepdim=True)
+    w = torch.where(tot > 0, z / tot, torch.zeros_like(z))
+    out = {"idx": idx.to(torch.int32), "w": w}
+    if s["way"] == "step":
+        gsel = w * (s["grad_w"] - (w * s["grad_w"]).sum(1, keepdim=True))
+        out["grad_logits"] = torch.zeros_like(s["logits"]).scatter_(1, idx, gsel)
+    return out
+
+
+def _plain_permute(s):
+    T, k, dt = s["T"], s["k"], s["grad"].dtype
+    offsets, order, pos = s["plan"] or _plan(s["ids"], s["E"])
+    kept = (pos < offsets[-1])[..., None]
+    place = pos.to(torch.int64)
+    if s["side"] == "in":
+        live = (torch.arange(T * k, device=DEV) < offsets[-1])[:, None]
+        rows = s["x"][order.to(torch.int64) // k]
+        out = {"rows": torch.where(live, rows, torch.zeros_like(rows)), "offsets": offsets, "sorted": order, "pos": pos}
+        if s["way"] == "step":
+            out["grad_x"] = torch.where(kept, s["grad"].float()[place], torch.zeros((), device=DEV)).sum(1).to(dt)
+        return out
+    r = torch.where(kept, s["rows"].float()[place], torch.zeros((), device=DEV))
+    out = {"y": (r * s["w"][..., None]).sum(1).to(dt)}
+    if s["way"] == "step":
+        gy = s["grad"].float()[:, None, :]
+        out["grad_w"] = (r * gy).sum(2)
+        gr = torch.where(kept, s["w"][..., None] * gy, torch.zeros((), device=DEV)).to(dt)
+        out["grad_rows"] = torch.empty_like(s["rows"]).index_copy_(0, place.reshape(-1), gr.reshape(T * k, -1))
+    return out
+
+
+def _plain_linear(s):
+    R, E, cap, off = s["x"].shape[0], s["E"], s["cap"], s["offsets"]
+    x, bias = s["x"].float(), s["bias"]
+    if off is None:
+        w = _weights(s)
+        spread, gather = (lambda v: v[None]), (lambda v: v[0])
+    else:
+        # the touched experts' weights, and their rows side by side, padded to the longest
+        live, off = s["live"], off.to(torch.int64)
+        w = _weights({**s, **{n: None if s[n] is None else s[n][live] for n in ("packed", "absmax", "scales")}})
+        bias = None if bias is None else bias[live]
+        lo, hi = off[live], off[live + 1]
+        r = torch.arange(R, device=DEV)
+        e = torch.searchsorted(hi, r, right=True).clamp_(max=live.numel() - 1)
+        col = (r - lo[e]).clamp_(max=cap - 1)
+        tail = (r >= off[-1])[:, None]
+        at = lo[:, None] + torch.arange(cap, device=DEV)
+        inside = (at < hi[:, None])[..., None]
+        at = at.clamp_(max=R - 1)
+        spread = lambda v: torch.where(inside, v[at], torch.zeros((), device=DEV))  # noqa: E731
+        gather = lambda v: torch.where(tail, torch.zeros((), device=DEV), v[e, col])  # noqa: E731
+    z = torch.bmm(spread(x), w.transpose(1, 2).contiguous())
+    if bias is not None:
+        z = z + bias[:, None, :]
+    a, da = _act(s["act"], z)
+    y = a if s["residual"] is None else a + spread(s["residual"].float())
+    out = {"y": gather(y).to(s["grad_y"].dtype)}
+    if s["way"] == "step":
+        dz = spread(s["grad_y"].float()) * da
+        out["grad_x"] = gather(torch.bmm(dz, w)).to(torch.bfloat16)
+        if bias is not None:
+            gb = dz.sum(1)
+            out["grad_bias"] = gb if off is None else gb.new_zeros(E, s["out"]).index_copy_(0, live, gb)
+    return out
+
+
+def _plain_norm(s, eps=1e-6):
+    x = s["x"].float()
+    out, rt = {}, s["x"].dtype
+    gate = None if s["gate_v"] is None else s["gate_v"].float()[:, None] if s["gate"] == "token" else s["gate_v"].float()
+    if s["y"] is None:
+        r = x
+    else:
+        y = s["y"].float()
+        if s["w_post"] is not None:
+            ry = 1 / torch.sqrt((y * y).mean(1, keepdim=True) + eps)
+            u = y * ry * s["w_post"].float()
+        else:
+            u = y
+        r = x + s["scale"] * (u if gate is None else gate * u)
+        out["r"] = r.to(rt)
+    if s["w_pre"] is not None:
+        rr = 1 / torch.sqrt((r * r).mean(1, keepdim=True) + eps)
+        out["h"] = (r * rr * s["w_pre"].float()).to(torch.bfloat16)
+    if s["way"] != "step":
+        return out
+    dr = s["grad_r"].float()
+    if s["w_pre"] is not None:
+        gh, n = s["grad_h"].float(), r * rr
+        gw = gh * s["w_pre"].float()
+        dr = dr + rr * (gw - n * (gw * n).mean(1, keepdim=True))
+        out["grad_w_pre"] = (gh * n).sum(0)
+    out["grad_x"] = dr.to(rt)
+    if s["y"] is not None:
+        if gate is not None:
+            out["grad_gate"] = (s["scale"] * dr * u).sum(1 if s["gate"] == "token" else 0)
+        du = s["scale"] * (dr if gate is None else gate * dr)
+        if s["w_post"] is not None:
+            n = y * ry
+            gw = du * s["w_post"].float()
+            out["grad_w_post"] = (du * n).sum(0)
+            du = ry * (gw - n * (gw * n).mean(1, keepdim=True))
+        out["grad_y"] = du.to(torch.bfloat16)
+    return out
+
+
+# ---- the library's entry points ----
+
+def _own_route(s):
+    import bit_quantized_mixture_nf4_amd as e4b
+    idx, w = e4b.moe_route(s["logits"], s["k"])
+    out = {"idx": idx, "w": w}
+    if s["way"] == "step":
+        out["grad_logits"] = e4b.moe_route_backward(idx, w, s["grad_w"], s["E"])
+    return out
+
+
+def _own_permute(s):
+    import bit_quantized_mixture_nf4_amd as e4b
+    if s["side"] == "in":
+        rows, perm = e4b.moe_permute(s["ids"], s["E"], s["x"])
+        out = {"rows": rows, "offsets": perm.offsets, "sorted": perm.sorted_pair, "pos": perm.pos}
+        if s["way"] == "step":
+            out["grad_x"] = e4b.moe_permute_backward(perm, s["grad"])
+        return out
+    perm = e4b.Permutation(*s["plan"])
+    out = {"y": e4b.moe_unpermute(perm, s["rows"], s["w"])}
+    if s["way"] == "step":
+        out["grad_rows"], out["grad_w"] = e4b.moe_unpermute_backward(perm, s["rows"], s["grad"], s["w"])
+    return out
+
+
+def _own_linear(s):
+    import bit_quantized_mixture_nf4_amd as e4b
+    stack = e4b.QuantStack(s["packed"], s["absmax"], s["E"], s["out"], s["inn"], s["codebook"], s["scales"])
+    step = s["way"] == "step"
+    y, pre = e4b.expert_linear(stack, s["x"], offsets=s["offsets"], bias=s["bias"], act=s["act"],
+                               residual=s["residual"], out_dtype=s["grad_y"].dtype, save=step)
+    out = {"y": y}
+    if step:
+        gx, gb = e4b.expert_linear_dgrad(stack, s["grad_y"], offsets=s["offsets"], act=s["act"], pre=pre,
+                                         grad_bias=s["bias"] is not None)
+        out["grad_x"] = gx
+        if gb is not None:
+            out["grad_bias"] = gb
+    return out
+
+
+def _own_norm(s):
+    import bit_quantized_mixture_nf4_amd as e4b
+    f = e4b.block_norm(s["x"], y=s["y"], w_post=s["w_post"], gate=s["gate_v"], scale=s["scale"], w_pre=s["w_pre"])
+    out = {}
+    if s["y"] is not None:
+        out["r"] = f.r
+    if f.h is not None:
+        out["h"] = f.h
+    if s["way"] == "step":
+        b = e4b.block_norm_backward(f, s["x"], s["grad_r"], s["grad_h"], y=s["y"], w_post=s["w_post"],
+                                    gate=s["gate_v"], scale=s["scale"], w_pre=s["w_pre"])
+        out["grad_x"] = b.grad_x
+        for name in ("grad_y", "grad_gate", "grad_w_post", "grad_w_pre"):
+            if getattr(b, name) is not None:
+                out[name] = getattr(b, name)
+    return out
+
+
+_PLAIN = {"route": _plain_route, "permute": _plain_permute, "linear": _plain_linear, "norm": _plain_norm}
+_OWN = {"route": _own_route, "permute": _own_permute, "linear": _own_linear, "norm": _own_norm}
+
+
+def run(state):
+    return (_OWN if own else _PLAIN)[state["op"]](state)
+
+
+# ---- what a pass cannot do without ----
+
+def work(case):
+    c, step = case, case["way"] == "step"
+    if c["op"] == "route":
+        n = c["T"] * c["E"] * 4 + c["T"] * c["k"] * 8
+        return {"bytes": n + (c["T"] * c["k"] * 4 + c["T"] * c["E"] * 4 if step else 0), "flops": 0}
+    if c["op"] == "permute":
+        P, b = c["T"] * c["k"], c["H"] * (2 if c["dtype"] == "bf16" else 4)
+        n = (c["T"] + P) * b + P * 8
+        if c["side"] == "in":
+            return {"bytes": n + P * 4 + (n if step else 0), "flops": P * c["H"] if step else 0}
+        # backward: grad_y in, grad_rows out; the rows are read once for both directions
+        return {"bytes": n + ((c["T"] + P) * b + P * 4 if step else 0), "flops": 2 * P * c["H"] * (3 if step else 1)}
+    if c["op"] == "linear":
+        R, b = c["rows"] + c["tail"], 2 if c["y"] == "bf16" else 4
+        n = c["touched"] * c["out"] * c["inn"] * _BITS[c["codebook"]] / 8 + R * (c["inn"] * 2 + c["out"] * b)
+        n += (c["touched"] * c["out"] * 4 if c["bias"] else 0) + (R * c["out"] * 2 if c["residual"] else 0)
+        if step:
+            n += R * (c["out"] * b + c["inn"] * 2) + (c["E"] * c["out"] * 4 if c["bias"] else 0)
+        return {"bytes": n, "flops": 2 * c["rows"] * c["inn"] * c["out"] * (2 if step else 1)}
+    TH, b = c["T"] * c["H"], 2 if c["dtype"] == "bf16" else 4
+    n = TH * (b + (2 + b if c["block"] else 0) + (2 if c["pre"] else 0))
+    if step:
+        n += TH * (2 * b + (2 if c["block"] else 0) + (2 if c["pre"] else 0))
+    return {"bytes": n + 4 * c["H"] * (c["post"] + c["pre"]), "flops": TH * (30 if step else 10)}
+
+
+# ---- the definitions in 64 bits ----
+
+def _weight64(s, e):
+    """[out, in] of expert `e` in 64 bits: code value times block scale rounded to fp32, then to bf16."""
+    p, cb = s["packed"][e], s["codebook"]
+    if cb == "bf16":
+        return p.view(torch.bfloat16).double().view(s["out"], s["inn"])
+    q = p.long() if cb == "fp8" else torch.stack([p.long() // 16, p.long() % 16], dim=1).reshape(-1)
+    sign, low = (128, 127) if cb == "fp8" else (8, 7)
+    if cb == "nf4":
+        v = torch.tensor(_NF4, dtype=torch.float64, device=DEV)[q]
+    else:
+        # the table entries are fp32 values
+        mag = torch.tensor(_FP8 if cb == "fp8" else _E2M1, dtype=torch.float64, device=DEV).float().double()
+        v = torch.where(q >= sign, -mag[q & low], mag[q & low])
+    block = 32 if cb == "mxfp4" else 64
+    scale = torch.exp2(s["scales"][e].double() - 127) if cb == "mxfp4" else s["absmax"][e].double()
+    v = (v.view(-1, block) * scale[:, None]).float().bfloat16().double()
+    return v.view(s["out"], s["inn"])
+
+
+def _places64(ids, E):
+    """The place of each pair, by counting: the pairs of lower experts, and the earlier ones of its own."""
+    flat = torch.where((ids >= 0) & (ids < E), ids, torch.full_like(ids, E)).reshape(-1).long()
+    hot = torch.nn.functional.one_hot(flat, E + 1)
+    before = (hot.cumsum(0) - hot).gather(1, flat[:, None])[:, 0]
+    first = hot.sum(0).cumsum(0) - hot.sum(0)
+    return (first[flat] + before).view(ids.shape)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    f64 = torch.float64
+    if s["op"] == "route":
+        lg = s["logits"].to(f64).cpu()
+        T, E, k = s["T"], s["E"], s["k"]
+        idx = torch.from_numpy(np.argsort(-lg.numpy(), axis=1, kind="stable")[:, :k].copy())
+        v = lg.gather(1, idx)
+        top = v[:, :1]
+        dead = top == -math.inf
+        w = torch.softmax(torch.where(dead, torch.zeros_like(v), v), dim=1).masked_fill(dead, 0.0)
+        out = {"idx": None, "w": w}
+        if s["way"] == "step":
+            gw = s["grad_w"].to(f64).cpu()
+            jac = torch.diag_embed(w) - w[:, :, None] * w[:, None, :]
+            out["grad_logits"] = torch.zeros_like(lg).scatter_(1, idx, (jac @ gw[..., None])[..., 0])
+        return out
+    if s["op"] == "permute":
+        T, k, E = s["T"], s["k"], s["E"]
+        ids = s["ids"]
+        good = (ids >= 0) & (ids < E)
+        if s["side"] == "in":
+            pos = _places64(ids, E)
+            rows = torch.zeros(T * k, s["H"], dtype=f64, device=DEV)
+            for j in range(k):
+                rows[pos[good[:, j], j]] = s["x"][good[:, j]].to(f64)
+            out = {"rows": rows, "offsets": None, "sorted": None, "pos": None}
+            if s["way"] == "step":
+                gx = torch.zeros(T, s["H"], dtype=f64, device=DEV)
+                for j in range(k):
+                    gx += s["grad"].to(f64)[pos[:, j]] * good[:, j, None]
+                out["grad_x"] = gx
+            return out
+        pos = _places64(ids, E)
+        y = torch.zeros(T, s["H"], dtype=f64, device=DEV)
+        gw = torch.zeros(T, k, dtype=f64, device=DEV)
+        gr = torch.zeros(T * k, s["H"], dtype=f64, device=DEV)
+        w, gy, rows = s["w"].to(f64), s["grad"].to(f64), s["rows"].to(f64)
+        for j in range(k):
+            m = good[:, j]
+            at = pos[m, j]
+            y[m] += w[m, j, None] * rows[at]
+            gw[m, j] = (rows[at] * gy[m]).sum(1)
+            gr[at] = w[m, j, None] * gy[m]
+        return {"y": y, "grad_w": gw, "grad_rows": gr} if s["way"] == "step" else {"y": y}
+    if s["op"] == "linear":
+        R, E = s["x"].shape[0], s["E"]
+        off = [0, R] if s["offsets"] is None else s["offsets"].tolist()
+        y = torch.zeros(R, s["out"], dtype=f64, device=DEV)
+        gx = torch.zeros(R, s["inn"], dtype=f64, device=DEV)
+        gb = torch.zeros(E, s["out"], dtype=f64, device=DEV)
+        for e in range(E):
+            a, b = off[e], off[e + 1]
+            if a == b:
+                continue
+            w = _weight64(s, e)
+            z = s["x"][a:b].to(f64) @ w.T
+            if s["bias"] is not None:
+                z += s["bias"][e].to(f64)
+            with torch.enable_grad():
+                zz = z.clone().requires_grad_(True)
+                act = _act64(s["act"], zz)
+                dz, = torch.autograd.grad(act, zz, s["grad_y"][a:b].to(f64))
+            y[a:b] = act.detach()
+            if s["residual"] is not None:
+                y[a:b] += s["residual"][a:b].to(f64)
+            gx[a:b] = dz @ w
+            gb[e] = dz.sum(0)
+        out = {"y": y}
+        if s["way"] == "step":
+            out["grad_x"] = gx
+            if s["bias"] is not None:
+                out["grad_bias"] = gb
+        return out
+    return _exact_norm(s)
+
+
+def _act64(name, z):
+    f = torch.nn.functional
+    return {"none": lambda: z * 1.0, "relu": lambda: f.relu(z), "silu": lambda: f.silu(z), "gelu": lambda: f.gelu(z),
+            "gelu_tanh": lambda: f.gelu(z, approximate="tanh")}[name]()
+
+
+def _exact_norm(s, eps=1e-6):
+    """The two norms by differentiation in 64 bits."""
+    f64 = torch.float64
+    leaf = {n: s[n].to(f64).requires_grad_(True) for n in ("x", "y", "w_post", "w_pre", "gate_v") if s[n] is not None}
+
+    def rms(v, w):
+        return v * torch.rsqrt(v.square().mean(-1, keepdim=True) + eps) * w
+
+    out = {}
+    with torch.enable_grad():
+        r = leaf["x"] * 1.0
+        if s["y"] is not None:
+            u = rms(leaf["y"], leaf["w_post"]) if s["w_post"] is not None else leaf["y"]
+            if s["gate"] != "none":
+                u = u * (leaf["gate_v"][:, None] if s["gate"] == "token" else leaf["gate_v"])
+            r = r + s["scale"] * u
+            out["r"] = r.detach()
+        loss = (r * s["grad_r"].to(f64)).sum()
+        if s["w_pre"] is not None:
+            h = rms(r, leaf["w_pre"])
+            out["h"] = h.detach()
+            loss = loss + (h * s["grad_h"].to(f64)).sum()
+        if s["way"] == "step":
+            names = list(leaf)
+            grads = torch.autograd.grad(loss, [leaf[n] for n in names])
+            out |= {"grad_gate" if n == "gate_v" else "grad_" + n: v for n, v in zip(names, grads)}
+    return out
