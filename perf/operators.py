@@ -416,7 +416,8 @@ def _own_linear(s):
 
 def _own_norm(s):
     import bit_quantized_mixture_nf4_amd as e4b
-    f = e4b.block_norm(s["x"], y=s["y"], w_post=s["w_post"], gate=s["gate_v"], scale=s["scale"], w_pre=s["w_pre"])
+    gates = {} if s["gate_v"] is None else {"gate_" + s["gate"]: s["gate_v"]}
+    f = e4b.block_norm(s["x"], y=s["y"], w_post=s["w_post"], scale=s["scale"], w_pre=s["w_pre"], **gates)
     out = {}
     if s["y"] is not None:
         out["r"] = f.r
@@ -424,7 +425,7 @@ def _own_norm(s):
         out["h"] = f.h
     if s["way"] == "step":
         b = e4b.block_norm_backward(f, s["x"], s["grad_r"], s["grad_h"], y=s["y"], w_post=s["w_post"],
-                                    gate=s["gate_v"], scale=s["scale"], w_pre=s["w_pre"])
+                                    scale=s["scale"], w_pre=s["w_pre"], **gates)
         out["grad_x"] = b.grad_x
         for name in ("grad_y", "grad_gate", "grad_w_post", "grad_w_pre"):
             if getattr(b, name) is not None:
