@@ -54,6 +54,22 @@ __all__ = [
     "saved_bytes",
     "perm_layout",
     "check_expert_ids",
+    "moe_route",
+    "moe_route_backward",
+    "Permutation",
+    "moe_permute",
+    "moe_permute_backward",
+    "moe_unpermute",
+    "moe_unpermute_backward",
+    "expert_linear",
+    "expert_linear_dgrad",
+    "expert_linear_workspace_bytes",
+    "expert_linear_dgrad_workspace_bytes",
+    "BlockNorm",
+    "BlockNormGrads",
+    "block_norm",
+    "block_norm_backward",
+    "block_norm_workspace_bytes",
     "E4bError",
 ]
 
@@ -500,3 +516,23 @@ class LayerPrefetcher:
             raise RuntimeError(f"layer {l} is not the acquired layer")
         _, s = self.queue.pop(0)
         self.free[s].record(torch.cuda.current_stream())
+
+
+from .block import (  # noqa: E402,F401  (block.py uses the helpers above)
+    BlockNorm,
+    BlockNormGrads,
+    Permutation,
+    block_norm,
+    block_norm_backward,
+    block_norm_workspace_bytes,
+    expert_linear,
+    expert_linear_dgrad,
+    expert_linear_dgrad_workspace_bytes,
+    expert_linear_workspace_bytes,
+    moe_permute,
+    moe_permute_backward,
+    moe_route,
+    moe_route_backward,
+    moe_unpermute,
+    moe_unpermute_backward,
+)

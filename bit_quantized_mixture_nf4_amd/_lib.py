@@ -21,9 +21,12 @@ E4B_ERR_WORKSPACE = 6
 E4B_ERR_ALIGN = 7
 E4B_ERR_PATH = 8
 E4B_ERR_HIP = 9
+E4B_ERR_ACT = 10
 
 E4B_CB_NF4, E4B_CB_FP4, E4B_CB_BF16, E4B_CB_MXFP4, E4B_CB_INT8, E4B_CB_FP8 = 0, 1, 2, 3, 4, 5
 E4B_F32, E4B_BF16 = 0, 1
+E4B_ACT_NONE, E4B_ACT_RELU, E4B_ACT_SILU, E4B_ACT_GELU, E4B_ACT_GELU_TANH = 0, 1, 2, 3, 4
+E4B_GATE_NONE, E4B_GATE_TOKEN, E4B_GATE_CHANNEL = 0, 1, 2
 E4B_PATH_AUTO, E4B_PATH_GROUPED, E4B_PATH_DECODE, E4B_PATH_MX8 = 0, 1, 2, 3
 
 # every function declared in include/e4b.h
@@ -45,6 +48,18 @@ EXPORTS = (
     "e4b_moe_dgrad_timed",
     "e4b_moe_perm_layout",
     "e4b_moe_forward_noalloc",
+    "e4b_route",
+    "e4b_route_backward",
+    "e4b_permute",
+    "e4b_unpermute",
+    "e4b_unpermute_backward",
+    "e4b_expert_linear",
+    "e4b_expert_linear_workspace_bytes",
+    "e4b_expert_linear_dgrad",
+    "e4b_expert_linear_dgrad_workspace_bytes",
+    "e4b_block_norm",
+    "e4b_block_norm_backward",
+    "e4b_block_norm_workspace_bytes",
 )
 
 # bytes of the per-GPU array that e4b_moe_forward_noalloc uses as its workspace
@@ -94,6 +109,20 @@ class E4bLora(ctypes.Structure):
     ]
 
 
+class E4bNorm(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("gate_kind", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("w_post", ctypes.c_void_p),
+        ("w_pre", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+    ]
+
+
 class E4bKernelEvents(ctypes.Structure):
     """e4b_kernel_events: start / stop hipEvent_t per kernel id (NULL: not timed)."""
 
@@ -126,6 +155,7 @@ def load():
         )
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+    no = ctypes.POINTER(E4bNorm)
     st, lay, lo = ctypes.POINTER(E4bStack), ctypes.POINTER(E4bLayer), ctypes.POINTER(E4bLora)
     sigs = {
         "e4b_quantize_nf4": (i32, [vp, i64, i64, i64, i32, i32, vp, vp, vp]),
@@ -147,6 +177,19 @@ def load():
         "e4b_moe_dgrad_timed": (
             i32, [lay, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, ctypes.POINTER(E4bKernelEvents)]),
         "e4b_moe_perm_layout": (i32, [lay, i64, i32, ctypes.POINTER(E4bPermLayout)]),
+        "e4b_route": (i32, [vp, i64, i64, i32, vp, vp, vp]),
+        "e4b_route_backward": (i32, [vp, vp, vp, i64, i64, i32, vp, vp]),
+        "e4b_permute": (i32, [i64, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "e4b_unpermute": (i32, [i64, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp]),
+        "e4b_unpermute_backward": (i32, [i64, i32, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "e4b_expert_linear": (i32, [st, i64, vp, vp, vp, i32, vp, i32, vp, vp, vp, sz, vp]),
+        "e4b_expert_linear_workspace_bytes": (sz, [st, i64]),
+        "e4b_expert_linear_dgrad": (i32, [st, i64, vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, sz, vp]),
+        "e4b_expert_linear_dgrad_workspace_bytes": (sz, [st, i64, i32]),
+        "e4b_block_norm": (i32, [no, vp, vp, vp, vp, vp, vp, vp]),
+        "e4b_block_norm_backward": (
+            i32, [no, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "e4b_block_norm_workspace_bytes": (sz, [no]),
         "e4b_moe_forward_noalloc": (i32, [lay, i64, i32, vp, vp, vp, vp, vp, vp, i32, vp]),
     }
     for name, (res, args) in sigs.items():

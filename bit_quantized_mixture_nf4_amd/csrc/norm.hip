@@ -1,0 +1,389 @@
+// norm.hip -- the norm after a block, its gate and residual scale, and the
+// norm before the next block, in one pass over the rows, and their gradients
+// in another.
+//
+// Row by row, with N(v) = v / sqrt(mean(v^2) + eps), s the residual scale and
+// g a gate per token or per channel (1 without one):
+//   u = N(y) w_post (or y)     r = x + s g u     h = N(r) w_pre
+// Gradients, with a = s g du/dN-side factors and n = N(r), m = N(y):
+//   c = grad_h w_pre                      grad_w_pre  = sum_t grad_h n
+//   dr = grad_r + rstd_r (c - n mean(c n))          = grad_x
+//   du = s g dr                           grad_w_post = sum_t du m
+//   grad_y = rstd_y (b - m mean(b m)), b = du w_post   (or du)
+//   grad_g = s sum(dr u) over the row (token gate) or over t (channel gate)
+// A row is held in registers by TPR threads, VEC C elements each, so every
+// tensor is read once and written once: HBM bounds both kernels. Statistics,
+// sums and h's and the gradients' arithmetic are fp32; h comes from the
+// unrounded r. r is not stored for the backward: it is rebuilt from x, y and
+// rstd_y, which are read anyway.
+#include "kernels.h"
+#include "plan_block.h"
+#include "rowvec.h"
+
+namespace e4b {
+
+namespace {
+
+constexpr int kNormThreads = 512;
+
+// Sum of N values over each group of TPR threads (whole waves), the same on
+// every thread. `red` holds N floats per wave and is free again on return.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) red[wave][i] = v[i];
+    __syncthreads();
+    constexpr int kW = TPR / 64;
+    const int w0 = wave / kW * kW;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kW; ++q) v[i] += red[w0 + q][i];
+    }
+    __syncthreads();
+  }
+}
+
+// One group of TPR threads per row; piece c of a thread is the VEC elements
+// from (c TPR + thread) VEC on, so a wave's accesses are consecutive.
+template <typename X, int TPR, int VEC, int C>
+__global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
+  __shared__ float red[kNormThreads / 64][1];
+  constexpr int R = kNormThreads / TPR;
+  const int th = threadIdx.x % TPR;
+  const int64_t t = int64_t(blockIdx.x) * R + threadIdx.x / TPR;
+  const bool on = t < a.T;
+  const int64_t row = on ? t * a.H : 0;
+  float x[C][VEC], y[C][VEC];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int h = (c * TPR + th) * VEC;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) x[c][q] = y[c][q] = 0.0f;
+    if (on && h < a.H) {
+      load_row<VEC>(static_cast<const X *>(a.x) + row + h, x[c]);
+      if (a.y) load_row<VEC>(static_cast<const bf16_t *>(a.y) + row + h, y[c]);
+    }
+  }
+  const float inv = 1.0f / float(a.H);
+  if (a.y) {
+    float f = a.scale;
+    if (a.w_post) {
+      float ss[1] = {0.0f};
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) ss[0] += y[c][q] * y[c][q];
+      row_sums<TPR, 1>(ss, red);
+      const float rs = 1.0f / sqrtf(ss[0] * inv + a.eps);
+      if (on && th == 0) a.rstd_y[t] = rs;
+      f *= rs;
+    }
+    if (a.gate_token && on) f *= a.gate_token[t];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + th) * VEC;
+      if (!on || h >= a.H) continue;
+      float w[VEC], g[VEC];
+      if (a.w_post) load_row<VEC>(a.w_post + h, w);
+      if (a.gate_channel) load_row<VEC>(a.gate_channel + h, g);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        float u = f * y[c][q];
+        if (a.w_post) u *= w[q];
+        if (a.gate_channel) u *= g[q];
+        x[c][q] += u;
+      }
+      store_row<VEC>(static_cast<X *>(a.r) + row + h, x[c]);
+    }
+  }
+  if (a.w_pre) {
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) ss[0] += x[c][q] * x[c][q];
+    row_sums<TPR, 1>(ss, red);
+    const float rs = 1.0f / sqrtf(ss[0] * inv + a.eps);
+    if (on && th == 0) a.rstd_r[t] = rs;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + th) * VEC;
+      if (!on || h >= a.H) continue;
+      float w[VEC];
+      load_row<VEC>(a.w_pre + h, w);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) w[q] = x[c][q] * rs * w[q];
+      store_row<VEC>(static_cast<bf16_t *>(a.h) + row + h, w);
+    }
+  }
+}
+
+// The backward. The three row sums it needs are taken at once: with
+// v = the factor of dr in the gate / post-norm products (u for a token gate,
+// else s g u), dr = grad_r + rstd_r (c - n m1) gives
+//   sum dr v = sum (grad_r + rstd_r c) v - rstd_r m1 sum n v,   m1 = mean(c n).
+// A workgroup walks rows blockIdx.x R, + gridDim.x R, ...: each thread keeps its
+// columns' share of the weight (and channel gate) gradients in registers, the
+// workgroup adds its groups' shares through LDS and writes one partial row;
+// norm_cols_kernel adds those in order. The grid depends on T alone, so results
+// are the same on every run.
+template <typename X, int TPR, int VEC, int C>
+__global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormArgs a) {
+  constexpr int R = kNormThreads / TPR, kE = VEC * C;
+  __shared__ float red[kNormThreads / 64][3];
+  __shared__ float cols[R * TPR * kE];
+  const int th = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const float inv = 1.0f / float(a.H);
+  float s_pre[C][VEC], s_post[C][VEC], s_gate[C][VEC];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) s_pre[c][q] = s_post[c][q] = s_gate[c][q] = 0.0f;
+
+  for (int64_t t0 = int64_t(blockIdx.x) * R; t0 < a.T; t0 += int64_t(gridDim.x) * R) {
+    const int64_t t = t0 + grp;
+    const bool on = t < a.T;
+    const int64_t row = on ? t * a.H : 0;
+    float x[C][VEC], y[C][VEC], dr[C][VEC], gh[C][VEC];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + th) * VEC;
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) x[c][q] = y[c][q] = dr[c][q] = gh[c][q] = 0.0f;
+      if (on && h < a.H) {
+        if (a.w_pre) load_row<VEC>(static_cast<const X *>(a.x) + row + h, x[c]);
+        if (a.y) load_row<VEC>(static_cast<const bf16_t *>(a.y) + row + h, y[c]);
+        if (a.grad_r) load_row<VEC>(static_cast<const X *>(a.grad_r) + row + h, dr[c]);
+        if (a.w_pre) load_row<VEC>(static_cast<const bf16_t *>(a.grad_h) + row + h, gh[c]);
+      }
+    }
+    const float rs_y = a.w_post && on ? a.rstd_y[t] : 1.0f;
+    const float rs_r = a.w_pre && on ? a.rstd_r[t] : 0.0f;
+    const float gt = a.gate_token && on ? a.gate_token[t] : 1.0f;
+    // y becomes m = N(y) (or y); x becomes n = N(r); dr becomes grad_r + rstd_r c
+    float sums[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + th) * VEC;
+      if (!on || h >= a.H) continue;
+      float wp[VEC], wq[VEC], gc[VEC];
+      if (a.w_post) load_row<VEC>(a.w_post + h, wp);
+      if (a.w_pre) load_row<VEC>(a.w_pre + h, wq);
+      if (a.gate_channel) load_row<VEC>(a.gate_channel + h, gc);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        const float m = y[c][q] * rs_y;
+        y[c][q] = m;
+        float v = a.w_post ? m * wp[q] : m;  // u
+        if (a.gate_channel) v *= gc[q];
+        if (a.w_pre) {
+          const float n = (x[c][q] + a.scale * gt * v) * rs_r;
+          const float cc = gh[c][q] * wq[q];
+          x[c][q] = n;
+          sums[0] += cc * n;
+          sums[2] += n * v;
+          dr[c][q] += rs_r * cc;
+          s_pre[c][q] += gh[c][q] * n;
+        }
+        sums[1] += dr[c][q] * v;
+      }
+    }
+    row_sums<TPR, 3>(sums, red);
+    const float m1 = rs_r * sums[0] * inv;         // times n: what dr loses
+    const float dv = sums[1] - m1 * sums[2];       // sum over the row of dr v
+    if (a.gate_token && a.grad_gate && on && th == 0) a.grad_gate[t] = a.scale * dv;
+    const float sg = a.scale * gt;
+    // mean of b m: b m = s g_t g_h w_post dr m = s g_t (dr v)
+    const float m2 = a.w_post ? sg * dv * inv : 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * TPR + th) * VEC;
+      if (!on || h >= a.H) continue;
+      if (a.w_pre) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) dr[c][q] -= m1 * x[c][q];
+      }
+      store_row<VEC>(static_cast<X *>(a.grad_x) + row + h, dr[c]);
+      if (a.y) {
+        float wp[VEC], gc[VEC], o[VEC];
+        if (a.w_post) load_row<VEC>(a.w_post + h, wp);
+        if (a.gate_channel) load_row<VEC>(a.gate_channel + h, gc);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          const float m = y[c][q];
+          float du = sg * dr[c][q];
+          if (a.gate_channel) {
+            s_gate[c][q] += a.scale * dr[c][q] * (a.w_post ? m * wp[q] : m);
+            du *= gc[q];
+          }
+          if (a.w_post) {
+            s_post[c][q] += du * m;
+            o[q] = rs_y * (du * wp[q] - m * m2);
+          } else {
+            o[q] = du;
+          }
+        }
+        store_row<VEC>(static_cast<bf16_t *>(a.grad_y) + row + h, o);
+      }
+    }
+  }
+  // this workgroup's share of the column sums
+  auto put = [&](const float(&s)[C][VEC], float *out) {
+    if (!out) return;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) cols[grp * (TPR * kE) + (c * TPR + th) * VEC + q] = s[c][q];
+    __syncthreads();
+    for (int h = threadIdx.x; h < a.H; h += kNormThreads) {
+      float v = 0.0f;
+      for (int r = 0; r < R; ++r) v += cols[r * (TPR * kE) + h];
+      out[int64_t(blockIdx.x) * a.H + h] = v;
+    }
+  };
+  put(s_pre, a.part_pre);
+  put(s_post, a.part_post);
+  put(s_gate, a.part_gate);
+}
+
+// out[h] = sum over the n partial rows, 16 interleaved runs added in a fixed order.
+__global__ __launch_bounds__(1024) void norm_cols_kernel(const float *__restrict__ p0, const float *__restrict__ p1,
+                                                         const float *__restrict__ p2, float *__restrict__ o0,
+                                                         float *__restrict__ o1, float *__restrict__ o2, int n, int H) {
+  __shared__ float s[16][64];
+  const float *p = blockIdx.y == 0 ? p0 : blockIdx.y == 1 ? p1 : p2;
+  float *o = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+  if (!o) return;
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6;
+  const int h = blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (h < H)
+    for (int i = run; i < n; i += 16) v += p[int64_t(i) * H + h];
+  s[run][lane] = v;
+  __syncthreads();
+  if (run == 0 && h < H) {
+    for (int r = 1; r < 16; ++r) v += s[r][lane];
+    o[h] = v;
+  }
+}
+
+template <typename X, int TPR, int VEC, int C>
+hipError_t run(const NormArgs &a, bool backward, hipStream_t s) {
+  constexpr int R = kNormThreads / TPR;
+  const int64_t blocks = (a.T + R - 1) / R;
+  if (!backward)
+    hipLaunchKernelGGL((norm_fwd_kernel<X, TPR, VEC, C>), dim3(uint32_t(blocks)), dim3(kNormThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<X, TPR, VEC, C>), dim3(uint32_t(a.groups)), dim3(kNormThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename X>
+hipError_t by_length(const NormArgs &a, bool backward, hipStream_t s) {
+  const int H = a.H;
+  if (H % 8 == 0) {
+    if (H <= 512) return run<X, 64, 8, 1>(a, backward, s);
+    if (H <= 1024) return run<X, 64, 8, 2>(a, backward, s);
+    if (H <= 2048) return run<X, 64, 8, 4>(a, backward, s);
+    if (H <= 4096) return run<X, 128, 8, 4>(a, backward, s);
+    if (H <= 8192) return run<X, 256, 8, 4>(a, backward, s);
+    return run<X, 512, 8, 4>(a, backward, s);
+  }
+  if (H <= 512) return run<X, 64, 1, 8>(a, backward, s);
+  if (H <= 2048) return run<X, 64, 1, 32>(a, backward, s);
+  if (H <= 4096) return run<X, 128, 1, 32>(a, backward, s);
+  if (H <= 8192) return run<X, 256, 1, 32>(a, backward, s);
+  return run<X, 512, 1, 32>(a, backward, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s) {
+  return a.f32 ? by_length<float>(a, false, s) : by_length<bf16_t>(a, false, s);
+}
+
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s) {
+  if (a.T) {
+    const hipError_t e = a.f32 ? by_length<float>(a, true, s) : by_length<bf16_t>(a, true, s);
+    if (e != hipSuccess) return e;
+  }
+  float *gate = a.gate_channel ? a.grad_gate : nullptr;
+  if (!a.grad_w_pre && !a.grad_w_post && !gate) return hipSuccess;
+  hipLaunchKernelGGL(norm_cols_kernel, dim3(uint32_t((a.H + 63) / 64), 3), dim3(1024), 0, s, a.part_pre, a.part_post,
+                     a.part_gate, a.grad_w_pre, a.grad_w_post, gate, a.T ? a.groups : 0, a.H);
+  return hipGetLastError();
+}
+
+}  // namespace e4b
+
+using namespace e4b;
+
+extern "C" e4b_status e4b_block_norm(const e4b_norm *n, const void *x, const void *y, void *r, void *h, float *rstd_y,
+                                     float *rstd_r, hipStream_t stream) {
+  NormArgs a{};
+  const e4b_status st = plan_norm(n, y != nullptr || (n && n->T == 0), &a);
+  if (st != E4B_OK || a.T == 0) return st;
+  if (!x || (y && !r) || (a.w_post && !rstd_y) || (a.w_pre && (!h || !rstd_r))) return E4B_ERR_NULL;
+  for (const void *p : {x, y, static_cast<const void *>(r), static_cast<const void *>(h),
+                        static_cast<const void *>(rstd_y), static_cast<const void *>(rstd_r)})
+    if (!aligned16(p)) return E4B_ERR_ALIGN;
+  a.x = x;
+  a.y = y;
+  a.r = r;
+  a.h = h;
+  a.rstd_y = rstd_y;
+  a.rstd_r = rstd_r;
+  return launch_norm_fwd(a, stream) == hipSuccess ? E4B_OK : E4B_ERR_HIP;
+}
+
+extern "C" e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, const void *y, const float *rstd_y,
+                                              const float *rstd_r, const void *grad_r, const void *grad_h,
+                                              void *grad_x, void *grad_y, float *grad_gate, float *grad_w_post,
+                                              float *grad_w_pre, void *ws, size_t ws_bytes, hipStream_t stream) {
+  NormArgs a{};
+  const e4b_status st = plan_norm(n, y != nullptr || (n && n->T == 0), &a);
+  if (st != E4B_OK) return st;
+  // T = 0 still writes the (zero) column gradients
+  if (a.T && (!x || !grad_x || (y && !grad_y) || (a.w_post && !rstd_y) || (a.w_pre && (!rstd_r || !grad_h)) ||
+              (!a.w_pre && !grad_r)))
+    return E4B_ERR_NULL;
+  const bool g = a.gate_token || a.gate_channel;
+  if ((grad_gate && !g) || (grad_w_post && !a.w_post) || (grad_w_pre && !a.w_pre)) return E4B_ERR_NULL;
+  if (a.T && !ws) return E4B_ERR_NULL;
+  if (a.T && ws_bytes < norm_ws_bytes(a)) return E4B_ERR_WORKSPACE;
+  for (const void *p :
+       {x, y, static_cast<const void *>(rstd_y), static_cast<const void *>(rstd_r), grad_r, grad_h,
+        static_cast<const void *>(grad_x), static_cast<const void *>(grad_y), static_cast<const void *>(grad_gate),
+        static_cast<const void *>(grad_w_post), static_cast<const void *>(grad_w_pre), static_cast<const void *>(ws)})
+    if (!aligned16(p)) return E4B_ERR_ALIGN;
+  a.x = x;
+  a.y = y;
+  a.rstd_y = const_cast<float *>(rstd_y);
+  a.rstd_r = const_cast<float *>(rstd_r);
+  a.grad_r = grad_r;
+  a.grad_h = grad_h;
+  a.grad_x = grad_x;
+  a.grad_y = grad_y;
+  a.grad_gate = grad_gate;
+  a.grad_w_post = grad_w_post;
+  a.grad_w_pre = grad_w_pre;
+  float *w = static_cast<float *>(ws);
+  const int64_t each = int64_t(a.groups) * a.H;
+  a.part_pre = grad_w_pre ? w : nullptr;
+  a.part_post = grad_w_post ? w + each : nullptr;
+  a.part_gate = grad_gate && a.gate_channel ? w + 2 * each : nullptr;
+  return launch_norm_bwd(a, stream) == hipSuccess ? E4B_OK : E4B_ERR_HIP;
+}
+
+extern "C" size_t e4b_block_norm_workspace_bytes(const e4b_norm *n) {
+  NormArgs a{};
+  return plan_norm(n, true, &a) == E4B_OK ? norm_ws_bytes(a) : 0;
+}

@@ -241,6 +241,7 @@ extern "C" const char *e4b_status_string(e4b_status s) {
     case E4B_ERR_WORKSPACE: return "workspace missing or too small";
     case E4B_ERR_ALIGN: return "device buffer not 16-byte aligned";
     case E4B_ERR_PATH: return "invalid path (decode path needs a gated 4-bit layer (NF4, FP4, MXFP4), T <= 8, saved == NULL and max(H, I) <= 16384)";
+    case E4B_ERR_ACT: return "unknown activation";
     case E4B_ERR_HIP: return "HIP kernel launch failed";
   }
   return "unknown status";

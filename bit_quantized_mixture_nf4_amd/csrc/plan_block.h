@@ -1,0 +1,72 @@
+// plan_block.h -- host-side checks and plans of the operators around the
+// experts (routing, expert order, block norms, stored-weight products). Like
+// plan.h, this makes no HIP call.
+#pragma once
+
+#include "plan.h"
+
+namespace e4b {
+
+// ---- expert order (order.hip) ----
+struct OrderArgs {
+  int64_t T;
+  int32_t k, E, H, f32;
+  const void *x;  // gather: tokens; the way back: expert rows
+  const void *gy;
+  void *rows;  // gather: expert rows; the way back: tokens (its gradient: expert rows)
+  const int32_t *offsets, *pos;
+  const float *w;
+  float *gw;
+};
+// T >= 0, 1 <= top_k <= 32, 1 <= E <= 1024, 1 <= H < 2^24, T top_k < 2^29.
+e4b_status plan_order(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype, OrderArgs *a);
+
+// ---- block norms (norm.hip) ----
+constexpr int kNormMaxH = 16384;  // a row is held by one workgroup's registers
+struct NormArgs {
+  int64_t T;
+  int32_t H, f32, groups;
+  float eps, scale;
+  const float *w_post, *w_pre, *gate_token, *gate_channel;
+  const void *x, *y;
+  void *r, *h;
+  float *rstd_y, *rstd_r;
+  const void *grad_r, *grad_h;
+  void *grad_x, *grad_y;
+  float *grad_gate, *grad_w_post, *grad_w_pre;
+  float *part_pre, *part_post, *part_gate;  // [groups, H] each
+};
+// The descriptor's checks; groups = the backward's workgroups (one row of
+// column sums each).
+// (An empty batch has no y to show for its gate.)
+e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a);
+inline size_t norm_ws_bytes(const NormArgs &a) { return size_t(a.groups) * size_t(a.H) * 3 * sizeof(float) + 16; }
+
+// ---- stored-weight products (linear.hip) ----
+constexpr int kLinearM = 128;  // rows per tile
+struct LinearPlan {
+  int64_t rows, m_bound;  // m_bound: row tiles of kLinearM rows, at most
+  int64_t ldz;            // row length of dz: out in whole K-steps
+  size_t off_tile_offsets, off_tile_map, off_dz, off_part, off_pre;
+  size_t fwd_bytes, bwd_bytes, bwd_recompute_bytes;
+};
+struct LinearArgs {
+  const uint16_t *A;  // bf16 rows
+  int64_t lda;
+  const uint8_t *packed, *scales;
+  const float *absmax;
+  int32_t E, out, in, cb;
+  const int32_t *tile_offsets;
+  const int4 *tile_map;
+  const float *bias;         // [E, out] or null
+  const uint16_t *residual;  // [rows, out] bf16 or null
+  void *y;                   // [rows, out] bf16 / fp32; dgrad: grad_x [rows, in] bf16
+  float *pre;                // [rows, out] or null
+  int32_t act, y_f32;
+};
+e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t dtype, LinearPlan *p);
+
+// ---- routing (route.hip) ----
+e4b_status check_route(int64_t T, int64_t E, int32_t top_k);
+
+}  // namespace e4b

@@ -11,6 +11,7 @@
 //      (expert offset + chunk base + rank among equal ids, lanes in pair order).
 #include "device.h"
 #include "kernels.h"
+#include "plan_block.h"
 #include "route_dev.h"
 
 namespace e4b {
@@ -24,6 +25,56 @@ __global__ __launch_bounds__(256) void route_kernel(const float *__restrict__ lo
   const int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
   route_token(logits, t, E, k, lane, idx, wts, nullptr, s_route[threadIdx.x >> 6]);
+}
+
+// The router as an operator of its own: the selection and weights of
+// route_kernel, for logits that may also be -inf (an expert out of service
+// for this token). Such an expert gets weight 0 when it has to fill a slot; a
+// row that is -inf throughout selects experts 0 .. k - 1 with weights 0.
+__global__ __launch_bounds__(256) void route_masked_kernel(const float *__restrict__ logits, int64_t T, int E, int k,
+                                                           int32_t *__restrict__ idx, float *__restrict__ wts) {
+  __shared__ RouteLds s_route[4];
+  const int lane = threadIdx.x & 63;
+  const int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  float best = -INFINITY;
+  for (int e = lane; e < E; e += 64) best = fmaxf(best, logits[t * E + e]);
+  route_token(logits, t, E, k, lane, idx, wts, nullptr, s_route[threadIdx.x >> 6]);
+  if (__ballot(best > -INFINITY) == 0 && lane < k) wts[t * k + lane] = 0.0f;
+}
+
+// Gradient of the logits through w = softmax(selected logits), the selection
+// held fixed: dl[idx_j] = w_j (g_j - sum_i w_i g_i), 0 for every other expert.
+// One wave per token; lane j holds slot j, then the lanes walk the row. The
+// k values sit in registers and reach the row's lanes by readlane, so the
+// whole row is written once: the floor is its 4 E bytes per token.
+__global__ __launch_bounds__(256) void route_bwd_kernel(const int32_t *__restrict__ idx, const float *__restrict__ wts,
+                                                        const float *__restrict__ gw, int64_t T, int E, int k,
+                                                        float *__restrict__ gl) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  int32_t id = -1;
+  float w = 0.0f, g = 0.0f;
+  if (lane < k) {
+    id = idx[t * k + lane];
+    w = wts[t * k + lane];
+    g = gw[t * k + lane];
+  }
+  float dot = w * g;
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
+  const float d = w * (g - dot);
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    float v = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int32_t ij = __builtin_amdgcn_readlane(id, j);
+      const float dj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), j));
+      v += ij == e ? dj : 0.0f;
+    }
+    if (e < E) gl[t * E + e] = v;
+  }
 }
 
 // hist[e * nchunks + c] = number of pairs of chunk c routed to expert e.
@@ -220,3 +271,29 @@ hipError_t launch_permute(const MoePlan &p, const int32_t *idx, char *ws, const 
 }
 
 }  // namespace e4b
+
+using namespace e4b;
+
+extern "C" e4b_status e4b_route(const float *logits, int64_t T, int64_t E, int32_t top_k, int32_t *topk_idx,
+                                float *topk_w, hipStream_t stream) {
+  const e4b_status st = check_route(T, E, top_k);
+  if (st != E4B_OK || T == 0) return st;
+  if (!logits || !topk_idx || !topk_w) return E4B_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(topk_w)) return E4B_ERR_ALIGN;
+  hipLaunchKernelGGL(route_masked_kernel, dim3(uint32_t((T + 3) / 4)), dim3(256), 0, stream, logits, T, int(E),
+                     int(top_k), topk_idx, topk_w);
+  return hipGetLastError() == hipSuccess ? E4B_OK : E4B_ERR_HIP;
+}
+
+extern "C" e4b_status e4b_route_backward(const int32_t *topk_idx, const float *topk_w, const float *grad_topk_w,
+                                         int64_t T, int64_t E, int32_t top_k, float *grad_logits,
+                                         hipStream_t stream) {
+  const e4b_status st = check_route(T, E, top_k);
+  if (st != E4B_OK || T == 0) return st;
+  if (!topk_idx || !topk_w || !grad_topk_w || !grad_logits) return E4B_ERR_NULL;
+  if (!aligned16(topk_idx) || !aligned16(topk_w) || !aligned16(grad_topk_w) || !aligned16(grad_logits))
+    return E4B_ERR_ALIGN;
+  hipLaunchKernelGGL(route_bwd_kernel, dim3(uint32_t((T + 3) / 4)), dim3(256), 0, stream, topk_idx, topk_w,
+                     grad_topk_w, T, int(E), int(top_k), grad_logits);
+  return hipGetLastError() == hipSuccess ? E4B_OK : E4B_ERR_HIP;
+}

@@ -63,7 +63,8 @@ typedef enum {
   E4B_ERR_WORKSPACE = 6, /* workspace NULL or smaller than e4b_moe_workspace_bytes() */
   E4B_ERR_ALIGN = 7,     /* a device buffer is not 16-byte aligned */
   E4B_ERR_PATH = 8,      /* unknown path, or the decode path was asked for but does not apply (a BF16, INT8 or FP8 layer, T > 8, saved != NULL, or max(H, I) above 16384) */
-  E4B_ERR_HIP = 9        /* a kernel launch failed (hipGetLastError after the launch) */
+  E4B_ERR_HIP = 9,       /* a kernel launch failed (hipGetLastError after the launch) */
+  E4B_ERR_ACT = 10       /* unknown activation (e4b_act) */
 } e4b_status;
 
 /* MXFP4 = the MX storage the [0.31.1] project page names for gpt-oss experts
@@ -409,6 +410,177 @@ typedef struct {
 } e4b_perm_layout;
 e4b_status e4b_moe_perm_layout(const e4b_moe_layer *L, int64_t T, int32_t top_k,
                                e4b_perm_layout *out);
+
+/* ---- The block around the experts ----
+ *
+ * What a MoE block needs next to its expert MLP: the router with the gradient
+ * of its logits, tokens into expert order and back, the product of expert rows
+ * with a stored stack and an epilogue, and the norms before and after a block.
+ * [sdist] Experts4bit.forward takes its routing from outside the module and
+ * scales and adds the experts' rows inside it; these calls are for callers who
+ * need the pieces (a router that trains, experts with biases or another
+ * activation, experts on another rank, dense projections over the same storage
+ * modes). They follow the conventions above. All sums, statistics and
+ * epilogues are fp32; results are the same on every run. */
+
+/* The router: topk_idx / topk_w exactly as e4b_moe_forward makes them from
+ * logits (the top_k largest, descending, ties to the lower id, and the softmax
+ * over them). A logit may be -inf (an expert out of service for that token):
+ * it gets weight 0 when it has to fill a slot, and a row that is -inf
+ * throughout selects experts 0 .. top_k - 1 with weights 0. NaN and +inf are
+ * not checked: such a row's ids and weights are meaningless.
+ *   logits   : device fp32 [T, E]
+ *   topk_idx : device int32 [T, top_k]  (written)
+ *   topk_w   : device fp32  [T, top_k]  (written)
+ * Errors: NULL, SHAPE (E outside [1, 1024], top_k outside [1, min(E, 32)], T < 0
+ * or too large), ALIGN, HIP. */
+e4b_status e4b_route(const float *logits, int64_t T, int64_t E, int32_t top_k, int32_t *topk_idx,
+                     float *topk_w, hipStream_t stream);
+
+/* Gradient of the logits, the selection held fixed (it takes grad_topk_w where
+ * e4b_moe_dgrad leaves it): grad_logits[t, idx_j] = w_j (g_j - sum_i w_i g_i),
+ * 0 for every other expert. An id given twice adds up; an id outside [0, E)
+ * gets no gradient.
+ *   topk_idx, topk_w : device [T, top_k], as e4b_route wrote them
+ *   grad_topk_w      : device fp32 [T, top_k]
+ *   grad_logits      : device fp32 [T, E] (written whole)
+ * Errors: as e4b_route. */
+e4b_status e4b_route_backward(const int32_t *topk_idx, const float *topk_w, const float *grad_topk_w,
+                              int64_t T, int64_t E, int32_t top_k, float *grad_logits,
+                              hipStream_t stream);
+
+/* Tokens into expert order: the routed pairs p = t top_k + j by expert id,
+ * stable, and each pair's row. A pair whose id lies outside [0, E) goes to no
+ * expert (one of another rank, a padding token): such pairs come last, from
+ * offsets[E] on, and their rows are zeros.
+ *   topk_idx    : device int32 [T, top_k]; top_k in [1, 32], also above E
+ *   x, rows     : device [T, H], [T top_k, H] (written), bf16 or fp32 (dtype);
+ *                 both NULL: only the order is made
+ *   offsets     : device int32 [E + 1]      (written; offsets[E] = pairs with an expert)
+ *   sorted_pair : device int32 [T top_k]    (written: pair at each place)
+ *   pos_of_pair : device int32 [T, top_k]   (written: place of each pair)
+ * T = 0 writes offsets only. Errors: NULL, SHAPE (E outside [1, 1024], H outside
+ * [1, 2^24), T top_k >= 2^29), DTYPE, ALIGN, HIP. */
+e4b_status e4b_permute(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype,
+                       const int32_t *topk_idx, const void *x, void *rows, int32_t *offsets,
+                       int32_t *sorted_pair, int32_t *pos_of_pair, hipStream_t stream);
+
+/* And back: y[t] = sum_j topk_w[t, j] rows[pos_of_pair[t, j]], in slot order;
+ * pairs without an expert add nothing, whatever their rows hold. topk_w NULL:
+ * the plain sum, which is the gradient of x in e4b_permute (rows = grad_rows).
+ * A place outside [0, offsets[E]) is read as a pair without an expert.
+ *   rows : device [T top_k, H];  y : device [T, H] (written)
+ * Errors: as e4b_permute. */
+e4b_status e4b_unpermute(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype,
+                         const int32_t *offsets, const int32_t *pos_of_pair, const float *topk_w,
+                         const void *rows, void *y, hipStream_t stream);
+
+/* Gradients of e4b_unpermute: grad_rows[pos(t, j)] = topk_w[t, j] grad_y[t] (zeros
+ * for a pair without an expert) and grad_topk_w[t, j] = rows[pos(t, j)] . grad_y[t]
+ * (0 for one). grad_topk_w may be NULL; rows is read only for it.
+ * Errors: as e4b_permute. */
+e4b_status e4b_unpermute_backward(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype,
+                                  const int32_t *offsets, const int32_t *pos_of_pair,
+                                  const float *topk_w, const void *rows, const void *grad_y,
+                                  void *grad_rows, float *grad_topk_w, hipStream_t stream);
+
+/* Activations of e4b_expert_linear: none, max(z, 0), z sigmoid(z), z Phi(z), and
+ * GELU's tanh form. */
+typedef enum {
+  E4B_ACT_NONE = 0,
+  E4B_ACT_RELU = 1,
+  E4B_ACT_SILU = 2,
+  E4B_ACT_GELU = 3,
+  E4B_ACT_GELU_TANH = 4
+} e4b_act;
+
+/* Product of expert-sorted rows with a stored stack: for a row r of expert e
+ * (offsets[e] <= r < offsets[e + 1]),
+ *   z = W[e] x_r + bias[e],   y_r = act(z) + residual_r
+ * with W the bf16 view of the stack (any storage mode) and fp32 accumulation.
+ * E = 1 with offsets NULL is a dense projection of every row. Rows from
+ * offsets[E] on belong to no expert: y and pre are zeros there.
+ *   st       : any out >= 1; in % 64 == 0; E <= 1024
+ *   offsets  : device int32 [E + 1], ascending from 0 (as e4b_permute writes them), or
+ *              NULL for E = 1. Values are not checked on the host; the kernels
+ *              clamp them, so that no list leads out of a buffer.
+ *   x_bf16   : device bf16 [rows, in]
+ *   bias     : device fp32 [E, out] or NULL
+ *   residual : device bf16 [rows, out] or NULL
+ *   y        : device [rows, out], bf16 or fp32 (y_dtype)  (written)
+ *   pre      : device fp32 [rows, out] or NULL: z, for the gradient  (written)
+ *   ws       : device workspace of e4b_expert_linear_workspace_bytes()
+ * Errors: NULL, SHAPE, BLOCKSIZE, CODEBOOK, ACT, DTYPE, WORKSPACE, ALIGN, HIP. */
+e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const int32_t *offsets,
+                             const void *x_bf16, const float *bias, int32_t act,
+                             const void *residual_bf16, int32_t y_dtype, void *y, float *pre,
+                             void *ws, size_t ws_bytes, hipStream_t stream);
+size_t e4b_expert_linear_workspace_bytes(const e4b_stack *st, int64_t rows);
+
+/* Its gradient, the stack frozen: dz = grad_y act'(z), rounded to bf16 as the
+ * product's operand;
+ *   grad_x = W[e]^T dz,   grad_bias[e] = sum over e's rows of dz (unrounded)
+ * (the residual's gradient is grad_y). act needs z: pre as the forward kept
+ * it, or x_bf16 and bias, from which it is computed again, bit for bit.
+ * Rows from offsets[E] on get zeros in grad_x; an expert without rows gets a
+ * zero bias gradient.
+ *   grad_y    : device [rows, out], bf16 or fp32 (gy_dtype)
+ *   grad_x    : device bf16 [rows, in]  (written)
+ *   grad_bias : device fp32 [E, out] (written) or NULL
+ *   ws        : e4b_expert_linear_dgrad_workspace_bytes(); recompute != 0 when act
+ *               is not NONE and pre is NULL
+ * Errors: as e4b_expert_linear. */
+e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows, const int32_t *offsets,
+                                   const void *grad_y, int32_t gy_dtype, const float *pre,
+                                   const void *x_bf16, const float *bias, int32_t act,
+                                   void *grad_x_bf16, float *grad_bias, void *ws, size_t ws_bytes,
+                                   hipStream_t stream);
+size_t e4b_expert_linear_dgrad_workspace_bytes(const e4b_stack *st, int64_t rows, int32_t recompute);
+
+/* Norms before and after a block, with the block's gate and residual scale.
+ * With N(v) = v / sqrt(mean(v^2) + eps) over a row:
+ *   u = N(y) w_post (w_post NULL: u = y);  r = x + scale g u;  h = N(r) w_pre
+ * y is the block's output, x the residual stream before it, r after it, h the
+ * next block's input. y NULL: r = x, only h is made. w_pre NULL: no h. The
+ * gate g is one value per token, per channel, or 1. */
+typedef enum { E4B_GATE_NONE = 0, E4B_GATE_TOKEN = 1, E4B_GATE_CHANNEL = 2 } e4b_gate;
+typedef struct {
+  int64_t T, H;       /* rows, and their length in [1, 16384] */
+  int32_t dtype;      /* of x, r and their gradients: E4B_BF16 or E4B_F32 */
+  int32_t gate_kind;  /* e4b_gate */
+  float eps, scale;   /* eps > 0 */
+  const float *w_post, *w_pre; /* device fp32 [H] or NULL */
+  const float *gate;           /* device fp32 [T] or [H]; NULL exactly for E4B_GATE_NONE */
+} e4b_norm;
+
+/*   x      : device [T, H] (dtype);  y : device bf16 [T, H] or NULL
+ *   r      : device [T, H] (dtype), written when y is given
+ *   h      : device bf16 [T, H], written when w_pre is given
+ *   rstd_y : device fp32 [T], written when w_post is given
+ *   rstd_r : device fp32 [T], written when w_pre is given
+ * h is made from the unrounded r. Errors: NULL (a needed pointer is missing; a
+ * gate or w_post without y; neither y nor w_pre), SHAPE (also eps not above 0 or
+ * an unknown gate), DTYPE, ALIGN, HIP. */
+e4b_status e4b_block_norm(const e4b_norm *n, const void *x, const void *y, void *r, void *h,
+                          float *rstd_y, float *rstd_r, hipStream_t stream);
+
+/* Gradients of sum(grad_r r) + sum(grad_h h). r is rebuilt from x and y.
+ *   x, y, rstd_y, rstd_r : as in the forward
+ *   grad_r      : device [T, H] (dtype), or NULL for zeros (with w_pre only)
+ *   grad_h      : device bf16 [T, H], with w_pre
+ *   grad_x      : device [T, H] (dtype)   (written)
+ *   grad_y      : device bf16 [T, H]      (written, with y)
+ *   grad_gate   : device fp32, as gate    (written) or NULL
+ *   grad_w_post, grad_w_pre : device fp32 [H] (written) or NULL
+ *   ws          : e4b_block_norm_workspace_bytes()
+ * T = 0 writes the column gradients (zeros). Errors: as e4b_block_norm, plus
+ * WORKSPACE, and NULL for a gradient of something not given. */
+e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, const void *y,
+                                   const float *rstd_y, const float *rstd_r, const void *grad_r,
+                                   const void *grad_h, void *grad_x, void *grad_y,
+                                   float *grad_gate, float *grad_w_post, float *grad_w_pre,
+                                   void *ws, size_t ws_bytes, hipStream_t stream);
+size_t e4b_block_norm_workspace_bytes(const e4b_norm *n);
 
 /* Static, human-readable text for a status code. */
 const char *e4b_status_string(e4b_status status);
