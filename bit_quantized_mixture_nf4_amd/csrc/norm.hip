@@ -129,108 +129,131 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
 // v = the factor of dr in the gate / post-norm products (u for a token gate,
 // else s g u), dr = grad_r + rstd_r (c - n m1) gives
 //   sum dr v = sum (grad_r + rstd_r c) v - rstd_r m1 sum n v,   m1 = mean(c n).
-// A workgroup walks rows blockIdx.x R, + gridDim.x R, ...: each thread keeps its
-// columns' share of the weight (and channel gate) gradients in registers, the
-// workgroup adds its groups' shares through LDS and writes one partial row;
+// A workgroup walks rows blockIdx.x R, + gridDim.x R, ... with tpr threads to a
+// row (R = NT / tpr rows at a time) and 8 elements to a thread (16 beyond 8192
+// columns): each thread keeps its columns' weights and its share of the column
+// gradients in registers, and the next rows' pieces, as stored, while it works
+// on these. 32 elements to a thread spilled 150 registers and took 59.6 us at
+// 4096 x 2048 bf16 and 326 us at 8191 x 4096 fp32. At the end the workgroup
+// adds its rows' shares through LDS and writes one partial row;
 // norm_cols_kernel adds those in order. The grid depends on T alone, so results
 // are the same on every run.
-template <typename X, int TPR, int VEC, int C>
-__global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormArgs a) {
-  constexpr int R = kNormThreads / TPR, kE = VEC * C;
-  __shared__ float red[kNormThreads / 64][3];
-  __shared__ float cols[R * TPR * kE];
-  const int th = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+template <typename X, int NT, int VEC, int C, bool CHANNEL>
+__global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
+  constexpr int kE = VEC * C;
+  __shared__ float red[2][NT / 64][3];
+  __shared__ float cols[NT * kE];
+  const int tpr = a.tpr, R = NT / tpr;
+  const int th = threadIdx.x & (tpr - 1), grp = threadIdx.x / tpr;
+  const int wave = threadIdx.x >> 6, waves = tpr >> 6, w0 = wave & ~(waves - 1);
   const float inv = 1.0f / float(a.H);
-  float s_pre[C][VEC], s_post[C][VEC], s_gate[C][VEC];
+  const X *px = static_cast<const X *>(a.x), *pgr = static_cast<const X *>(a.grad_r);
+  const bf16_t *py = static_cast<const bf16_t *>(a.y), *pgh = static_cast<const bf16_t *>(a.grad_h);
+  const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  float s_pre[C][VEC], s_post[C][VEC], s_gate[C][VEC], wp[C][VEC], wq[C][VEC], gc[C][VEC];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    const int h = (c * tpr + th) * VEC;
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) s_pre[c][q] = s_post[c][q] = s_gate[c][q] = 0.0f;
-
-  for (int64_t t0 = int64_t(blockIdx.x) * R; t0 < a.T; t0 += int64_t(gridDim.x) * R) {
+    for (int q = 0; q < VEC; ++q) {
+      s_pre[c][q] = s_post[c][q] = s_gate[c][q] = wq[c][q] = 0.0f;
+      wp[c][q] = gc[c][q] = 1.0f;
+    }
+    if (h < a.H) {
+      if (post) load_row<VEC>(a.w_post + h, wp[c]);
+      if (pre) load_row<VEC>(a.w_pre + h, wq[c]);
+      if (CHANNEL) load_row<VEC>(a.gate_channel + h, gc[c]);
+    }
+  }
+  struct Row {
+    Raw<X, VEC> x[C], gr[C];
+    Raw<bf16_t, VEC> y[C], gh[C];
+    float rs_y, rs_r, gt;
+  };
+  auto fetch = [&](int64_t t, Row &f) {
+    const bool on = t < a.T;
+    const int64_t row = on ? t * a.H : 0;
+    f.rs_y = post && on ? a.rstd_y[t] : 1.0f;
+    f.rs_r = pre && on ? a.rstd_r[t] : 0.0f;
+    f.gt = !CHANNEL && a.gate_token && on ? a.gate_token[t] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * tpr + th) * VEC;
+      const bool in = on && h < a.H;
+      f.x[c].fetch(px + row + h, in && pre);
+      f.y[c].fetch(py + row + h, in && py);
+      f.gr[c].fetch(pgr + row + h, in && pgr);
+      f.gh[c].fetch(pgh + row + h, in && pre);
+    }
+  };
+  const int64_t step = int64_t(gridDim.x) * R;
+  Row cur;
+  fetch(int64_t(blockIdx.x) * R + grp, cur);
+  int turn = 0;
+  for (int64_t t0 = int64_t(blockIdx.x) * R; t0 < a.T; t0 += step, turn ^= 1) {
     const int64_t t = t0 + grp;
     const bool on = t < a.T;
     const int64_t row = on ? t * a.H : 0;
-    float x[C][VEC], y[C][VEC], dr[C][VEC], gh[C][VEC];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + th) * VEC;
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) x[c][q] = y[c][q] = dr[c][q] = gh[c][q] = 0.0f;
-      if (on && h < a.H) {
-        if (a.w_pre) load_row<VEC>(static_cast<const X *>(a.x) + row + h, x[c]);
-        if (a.y) load_row<VEC>(static_cast<const bf16_t *>(a.y) + row + h, y[c]);
-        if (a.grad_r) load_row<VEC>(static_cast<const X *>(a.grad_r) + row + h, dr[c]);
-        if (a.w_pre) load_row<VEC>(static_cast<const bf16_t *>(a.grad_h) + row + h, gh[c]);
-      }
-    }
-    const float rs_y = a.w_post && on ? a.rstd_y[t] : 1.0f;
-    const float rs_r = a.w_pre && on ? a.rstd_r[t] : 0.0f;
-    const float gt = a.gate_token && on ? a.gate_token[t] : 1.0f;
-    // y becomes m = N(y) (or y); x becomes n = N(r); dr becomes grad_r + rstd_r c
+    const float rs_y = cur.rs_y, rs_r = cur.rs_r, sg = a.scale * cur.gt;
+    // m = N(y) (or y), n = N(r), d = grad_r + rstd_r c; absent pieces are zeros
+    float m[C][VEC], n[C][VEC], d[C][VEC];
     float sums[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + th) * VEC;
-      if (!on || h >= a.H) continue;
-      float wp[VEC], wq[VEC], gc[VEC];
-      if (a.w_post) load_row<VEC>(a.w_post + h, wp);
-      if (a.w_pre) load_row<VEC>(a.w_pre + h, wq);
-      if (a.gate_channel) load_row<VEC>(a.gate_channel + h, gc);
+      float gh[VEC];
+      cur.x[c].get(n[c]);
+      cur.y[c].get(m[c]);
+      cur.gr[c].get(d[c]);
+      cur.gh[c].get(gh);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
-        const float m = y[c][q] * rs_y;
-        y[c][q] = m;
-        float v = a.w_post ? m * wp[q] : m;  // u
-        if (a.gate_channel) v *= gc[q];
-        if (a.w_pre) {
-          const float n = (x[c][q] + a.scale * gt * v) * rs_r;
-          const float cc = gh[c][q] * wq[q];
-          x[c][q] = n;
-          sums[0] += cc * n;
-          sums[2] += n * v;
-          dr[c][q] += rs_r * cc;
-          s_pre[c][q] += gh[c][q] * n;
-        }
-        sums[1] += dr[c][q] * v;
+        m[c][q] *= rs_y;
+        const float v = m[c][q] * wp[c][q] * (CHANNEL ? gc[c][q] : 1.0f);  // u, or g u
+        n[c][q] = (n[c][q] + sg * v) * rs_r;
+        const float cc = gh[q] * wq[c][q];
+        sums[0] += cc * n[c][q];
+        sums[2] += n[c][q] * v;
+        d[c][q] += rs_r * cc;
+        s_pre[c][q] += gh[q] * n[c][q];
+        sums[1] += d[c][q] * v;
       }
     }
-    row_sums<TPR, 3>(sums, red);
-    const float m1 = rs_r * sums[0] * inv;         // times n: what dr loses
-    const float dv = sums[1] - m1 * sums[2];       // sum over the row of dr v
-    if (a.gate_token && a.grad_gate && on && th == 0) a.grad_gate[t] = a.scale * dv;
-    const float sg = a.scale * gt;
+    // the next rows are on their way while this one's sums meet
+    fetch(t + step, cur);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) sums[i] = wave_sum(sums[i]);
+    if (waves > 1) {
+      // two buffers in turn: one barrier orders both the writes and the next turn's
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) red[turn][wave][i] = sums[i];
+      __syncthreads();
+      sums[0] = sums[1] = sums[2] = 0.0f;
+      for (int q = 0; q < waves; ++q)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) sums[i] += red[turn][w0 + q][i];
+    }
+    const float m1 = rs_r * sums[0] * inv;    // times n: what dr loses
+    const float dv = sums[1] - m1 * sums[2];  // sum over the row of dr v
+    if (!CHANNEL && a.gate_token && a.grad_gate && on && th == 0) a.grad_gate[t] = a.scale * dv;
     // mean of b m: b m = s g_t g_h w_post dr m = s g_t (dr v)
-    const float m2 = a.w_post ? sg * dv * inv : 0.0f;
+    const float m2 = post ? sg * dv * inv : 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + th) * VEC;
-      if (!on || h >= a.H) continue;
-      if (a.w_pre) {
+      const int h = (c * tpr + th) * VEC;
+      float o[VEC];
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) dr[c][q] -= m1 * x[c][q];
+      for (int q = 0; q < VEC; ++q) {
+        const float dr = d[c][q] - m1 * n[c][q];
+        const float du = sg * dr * (CHANNEL ? gc[c][q] : 1.0f);
+        if (CHANNEL) s_gate[c][q] += a.scale * dr * (m[c][q] * wp[c][q]);
+        s_post[c][q] += du * m[c][q];
+        d[c][q] = dr;
+        o[q] = rs_y * (du * wp[c][q] - m[c][q] * m2);
       }
-      store_row<VEC>(static_cast<X *>(a.grad_x) + row + h, dr[c]);
-      if (a.y) {
-        float wp[VEC], gc[VEC], o[VEC];
-        if (a.w_post) load_row<VEC>(a.w_post + h, wp);
-        if (a.gate_channel) load_row<VEC>(a.gate_channel + h, gc);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          const float m = y[c][q];
-          float du = sg * dr[c][q];
-          if (a.gate_channel) {
-            s_gate[c][q] += a.scale * dr[c][q] * (a.w_post ? m * wp[q] : m);
-            du *= gc[q];
-          }
-          if (a.w_post) {
-            s_post[c][q] += du * m;
-            o[q] = rs_y * (du * wp[q] - m * m2);
-          } else {
-            o[q] = du;
-          }
-        }
-        store_row<VEC>(static_cast<bf16_t *>(a.grad_y) + row + h, o);
+      if (on && h < a.H) {
+        store_row<VEC>(static_cast<X *>(a.grad_x) + row + h, d[c]);
+        if (py) store_row<VEC>(static_cast<bf16_t *>(a.grad_y) + row + h, o);
       }
     }
   }
@@ -241,17 +264,17 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int q = 0; q < VEC; ++q) cols[grp * (TPR * kE) + (c * TPR + th) * VEC + q] = s[c][q];
+      for (int q = 0; q < VEC; ++q) cols[grp * (tpr * kE) + (c * tpr + th) * VEC + q] = s[c][q];
     __syncthreads();
-    for (int h = threadIdx.x; h < a.H; h += kNormThreads) {
+    for (int h = threadIdx.x; h < a.H; h += NT) {
       float v = 0.0f;
-      for (int r = 0; r < R; ++r) v += cols[r * (TPR * kE) + h];
+      for (int r = 0; r < R; ++r) v += cols[r * (tpr * kE) + h];
       out[int64_t(blockIdx.x) * a.H + h] = v;
     }
   };
   put(s_pre, a.part_pre);
   put(s_post, a.part_post);
-  put(s_gate, a.part_gate);
+  if (CHANNEL) put(s_gate, a.part_gate);
 }
 
 // out[h] = sum over the n partial rows, 16 interleaved runs added in a fixed order.
@@ -266,6 +289,7 @@ __global__ __launch_bounds__(1024) void norm_cols_kernel(const float *__restrict
   const int h = blockIdx.x * 64 + lane;
   float v = 0.0f;
   if (h < H)
+#pragma unroll 16
     for (int i = run; i < n; i += 16) v += p[int64_t(i) * H + h];
   s[run][lane] = v;
   __syncthreads();
@@ -276,43 +300,57 @@ __global__ __launch_bounds__(1024) void norm_cols_kernel(const float *__restrict
 }
 
 template <typename X, int TPR, int VEC, int C>
-hipError_t run(const NormArgs &a, bool backward, hipStream_t s) {
+hipError_t forward(const NormArgs &a, hipStream_t s) {
   constexpr int R = kNormThreads / TPR;
-  const int64_t blocks = (a.T + R - 1) / R;
-  if (!backward)
-    hipLaunchKernelGGL((norm_fwd_kernel<X, TPR, VEC, C>), dim3(uint32_t(blocks)), dim3(kNormThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_bwd_kernel<X, TPR, VEC, C>), dim3(uint32_t(a.groups)), dim3(kNormThreads), 0, s, a);
+  hipLaunchKernelGGL((norm_fwd_kernel<X, TPR, VEC, C>), dim3(uint32_t((a.T + R - 1) / R)), dim3(kNormThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <typename X>
-hipError_t by_length(const NormArgs &a, bool backward, hipStream_t s) {
+hipError_t forward_by_length(const NormArgs &a, hipStream_t s) {
   const int H = a.H;
   if (H % 8 == 0) {
-    if (H <= 512) return run<X, 64, 8, 1>(a, backward, s);
-    if (H <= 1024) return run<X, 64, 8, 2>(a, backward, s);
-    if (H <= 2048) return run<X, 64, 8, 4>(a, backward, s);
-    if (H <= 4096) return run<X, 128, 8, 4>(a, backward, s);
-    if (H <= 8192) return run<X, 256, 8, 4>(a, backward, s);
-    return run<X, 512, 8, 4>(a, backward, s);
+    if (H <= 512) return forward<X, 64, 8, 1>(a, s);
+    if (H <= 1024) return forward<X, 64, 8, 2>(a, s);
+    if (H <= 2048) return forward<X, 64, 8, 4>(a, s);
+    if (H <= 4096) return forward<X, 128, 8, 4>(a, s);
+    if (H <= 8192) return forward<X, 256, 8, 4>(a, s);
+    return forward<X, 512, 8, 4>(a, s);
   }
-  if (H <= 512) return run<X, 64, 1, 8>(a, backward, s);
-  if (H <= 2048) return run<X, 64, 1, 32>(a, backward, s);
-  if (H <= 4096) return run<X, 128, 1, 32>(a, backward, s);
-  if (H <= 8192) return run<X, 256, 1, 32>(a, backward, s);
-  return run<X, 512, 1, 32>(a, backward, s);
+  if (H <= 512) return forward<X, 64, 1, 8>(a, s);
+  if (H <= 2048) return forward<X, 64, 1, 32>(a, s);
+  if (H <= 4096) return forward<X, 128, 1, 32>(a, s);
+  if (H <= 8192) return forward<X, 256, 1, 32>(a, s);
+  return forward<X, 512, 1, 32>(a, s);
+}
+
+template <typename X, int NT, int VEC, int C>
+hipError_t backward(const NormArgs &a, hipStream_t s) {
+  if (a.gate_channel)
+    hipLaunchKernelGGL((norm_bwd_kernel<X, NT, VEC, C, true>), dim3(uint32_t(a.groups)), dim3(NT), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<X, NT, VEC, C, false>), dim3(uint32_t(a.groups)), dim3(NT), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename X>
+hipError_t backward_by_length(const NormArgs &a, hipStream_t s) {
+  if (a.H % 8 == 0)
+    return a.H <= 4096 ? backward<X, 512, 8, 1>(a, s)
+                       : a.H <= 8192 ? backward<X, 1024, 8, 1>(a, s) : backward<X, 1024, 8, 2>(a, s);
+  return a.H <= 4096 ? backward<X, 512, 1, 8>(a, s)
+                     : a.H <= 8192 ? backward<X, 1024, 1, 8>(a, s) : backward<X, 1024, 1, 16>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t s) {
-  return a.f32 ? by_length<float>(a, false, s) : by_length<bf16_t>(a, false, s);
+  return a.f32 ? forward_by_length<float>(a, s) : forward_by_length<bf16_t>(a, s);
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s) {
   if (a.T) {
-    const hipError_t e = a.f32 ? by_length<float>(a, true, s) : by_length<bf16_t>(a, true, s);
+    const hipError_t e = a.f32 ? backward_by_length<float>(a, s) : backward_by_length<bf16_t>(a, s);
     if (e != hipSuccess) return e;
   }
   float *gate = a.gate_channel ? a.grad_gate : nullptr;

@@ -23,9 +23,13 @@ e4b_status plan_order(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dt
 
 // ---- block norms (norm.hip) ----
 constexpr int kNormMaxH = 16384;  // a row is held by one workgroup's registers
+// Threads of the backward's workgroups: 512 leave each thread the registers to hold
+// its columns' weights and sums; beyond 4096 columns a row takes 1024.
+inline int norm_bwd_threads(int64_t H) { return H <= 4096 ? 512 : 1024; }
 struct NormArgs {
   int64_t T;
-  int32_t H, f32, groups;
+  int32_t H, f32;
+  int32_t tpr, groups;  // the backward's threads per row, and its workgroups
   float eps, scale;
   const float *w_post, *w_pre, *gate_token, *gate_channel;
   const void *x, *y;

@@ -65,6 +65,48 @@ __device__ __forceinline__ void store_row(float *p, const float (&f)[VEC]) {
   }
 }
 
+// A piece as it is stored, for rows fetched ahead of their use; zeros when `in`
+// is false.
+template <typename T, int VEC>
+struct Raw;
+template <>
+struct Raw<bf16_t, 8> {
+  u32x4 v;
+  __device__ __forceinline__ void fetch(const bf16_t *p, bool in) {
+    v = u32x4{0u, 0u, 0u, 0u};
+    if (in) v = *reinterpret_cast<const u32x4 *>(p);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      f[2 * q] = bf16_lo(v[q]);
+      f[2 * q + 1] = bf16_hi(v[q]);
+    }
+  }
+};
+template <>
+struct Raw<bf16_t, 1> {
+  uint16_t v;
+  __device__ __forceinline__ void fetch(const bf16_t *p, bool in) {
+    v = 0;
+    if (in) v = p->v;
+  }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = bf16_to_f32(v); }
+};
+template <int VEC>
+struct Raw<float, VEC> {
+  float v[VEC];
+  __device__ __forceinline__ void fetch(const float *p, bool in) {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) v[q] = 0.0f;
+    if (in) load_row<VEC>(p, v);
+  }
+  __device__ __forceinline__ void get(float (&f)[VEC]) const {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) f[q] = v[q];
+  }
+};
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
