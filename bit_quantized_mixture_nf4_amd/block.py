@@ -20,14 +20,21 @@ ACTS = {"none": _lib.E4B_ACT_NONE, "relu": _lib.E4B_ACT_RELU, "silu": _lib.E4B_A
 _DTYPES = {torch.float32: _lib.E4B_F32, torch.bfloat16: _lib.E4B_BF16}
 
 
+# the current stream's handle without the Stream object that torch.cuda.current_stream makes
+# (1.9 us of a call whose launch takes 3.3); torch.cuda.current_stream where torch has no such function
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(name, device, *args):
     """Call entry point ``name`` on the current stream of ``device``."""
     fn = getattr(load(), name)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            code = fn(*args, _raw_stream(index))
     else:
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        code = fn(*args, _raw_stream(index))
     if code:
         check(name, code)
 
@@ -312,12 +319,13 @@ def expert_linear_dgrad(stack, grad_y, x=None, offsets=None, bias=None, act="non
 @dataclass
 class BlockNorm:
     """``block_norm``'s results: the residual stream ``r`` (x itself without y), the
-    next block's input ``h``, and the row statistics its gradient needs."""
+    next block's input ``h``, and the row statistics its gradient needs (``rstd``
+    float32 [2, T rounded up to 4]: 1 / rms of y's rows, then of r's; a row that its
+    norm does not have is not written)."""
 
     r: torch.Tensor
     h: torch.Tensor
-    rstd_y: torch.Tensor
-    rstd_r: torch.Tensor
+    rstd: torch.Tensor
 
 
 @dataclass
@@ -367,10 +375,16 @@ def block_norm(x, y=None, w_post=None, gate_token=None, gate_channel=None, scale
     dev, T, H, _, n = _norm_args(x, y, w_post, gate_token, gate_channel, scale, w_pre, eps)
     r = torch.empty_like(x) if y is not None else None
     h = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if w_pre is not None else None
-    rstd_y = torch.empty(T, dtype=torch.float32, device=dev) if w_post is not None else None
-    rstd_r = torch.empty(T, dtype=torch.float32, device=dev) if w_pre is not None else None
-    _run("e4b_block_norm", dev, ctypes.byref(n), x.data_ptr(), _vp(y), _vp(r), _vp(h), _vp(rstd_y), _vp(rstd_r))
-    return BlockNorm(x if r is None else r, h, rstd_y, rstd_r)
+    rstd = torch.empty(2, -(-T // 4) * 4, dtype=torch.float32, device=dev)
+    rstd_y, rstd_r = _rstd(rstd)
+    _run("e4b_block_norm", dev, ctypes.byref(n), x.data_ptr(), _vp(y), _vp(r), _vp(h), rstd_y, rstd_r)
+    return BlockNorm(x if r is None else r, h, rstd)
+
+
+def _rstd(rstd):
+    """The addresses of its two rows."""
+    p = rstd.data_ptr()
+    return p, p + rstd.shape[1] * 4
 
 
 def block_norm_backward(fwd, x, grad_r=None, grad_h=None, y=None, w_post=None, gate_token=None, gate_channel=None,
@@ -387,13 +401,12 @@ def block_norm_backward(fwd, x, grad_r=None, grad_h=None, y=None, w_post=None, g
         if grad_h is None:
             raise ValueError("w_pre needs grad_h")
         _need(grad_h, "grad_h", torch.bfloat16, dev, (T, H))
-        _need(fwd.rstd_r, "rstd_r", torch.float32, dev, (T,))
     elif grad_r is None:
         raise ValueError("give grad_r")
     if grad_r is not None:
         _need(grad_r, "grad_r", x.dtype, dev, (T, H))
-    if w_post is not None:
-        _need(fwd.rstd_y, "rstd_y", torch.float32, dev, (T,))
+    _need(fwd.rstd, "rstd", torch.float32, dev, (2, -(-T // 4) * 4))
+    rstd_y, rstd_r = _rstd(fwd.rstd)
     gx = torch.empty_like(x)
     gy = torch.empty_like(y) if y is not None else None
     gg = torch.empty_like(gate) if gate is not None and (weight_grads or gate_token is not None) else None
@@ -404,7 +417,7 @@ def block_norm_backward(fwd, x, grad_r=None, grad_h=None, y=None, w_post=None, g
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     else:
         _need_buffer(workspace, "workspace", need, dev)
-    _run("e4b_block_norm_backward", dev, ctypes.byref(n), x.data_ptr(), _vp(y), _vp(fwd.rstd_y), _vp(fwd.rstd_r),
+    _run("e4b_block_norm_backward", dev, ctypes.byref(n), x.data_ptr(), _vp(y), rstd_y, rstd_r,
          _vp(grad_r), _vp(grad_h) if w_pre is not None else None, gx.data_ptr(), _vp(gy), _vp(gg), _vp(gpost),
          _vp(gpre), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return BlockNormGrads(gx, gy, gg, gpost, gpre)

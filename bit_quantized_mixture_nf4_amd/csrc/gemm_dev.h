@@ -8,7 +8,7 @@ namespace e4b {
 
 enum { A_GATHER = 0, A_DIRECT = 1 };
 enum { B_NT = 0, B_NN = 1 };
-enum { EPI_SWIGLU = 0, EPI_STORE = 1, EPI_DSWIGLU = 2, EPI_ACT = 3, EPI_DACT = 4 };
+enum { EPI_SWIGLU = 0, EPI_STORE = 1, EPI_DSWIGLU = 2, EPI_ACT = 3, EPI_DACT = 4, EPI_LINEAR = 5 };
 
 constexpr int kLds = kBK + 8;  // padded row (bf16 elements): 144 bytes, conflict-free b128 access
 

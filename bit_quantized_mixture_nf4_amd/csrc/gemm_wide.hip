@@ -23,6 +23,8 @@
 //                 the tile's share of d y / d routing weight.
 //   EPI_ACT / EPI_DACT : the same for an ungated layer (has_gate=False in
 //                 Experts4bit.__init__: a plain up projection h, a = act(h)).
+//   EPI_LINEAR  : bias, activation and residual of a stored-weight product
+//                 (linear.hip), fp32 from the accumulators on.
 //
 // Tile: 256 pairs x 256 columns x 64 (one quantization block per K-step).
 // * 8 waves of 64 x 128 (two per SIMD, 2 x 4 MFMA 32x32x16 bf16 tiles and
@@ -55,6 +57,7 @@
 //   each tile column; the epilogues then see the adapted product.
 #include <type_traits>
 
+#include "act.h"
 #include "codebook8.h"
 #include "gemm_dev.h"
 
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(wide::Shape<WM>::kThreads, 1) void gemm_wide_kernel
   constexpr bool kC8 = SK == SK_CODE8;
   constexpr bool kNN = BMODE == B_NN;
   static_assert(EPI == EPI_SWIGLU || EPI == EPI_ACT || EPI == EPI_STORE || EPI == EPI_DSWIGLU ||
-                    EPI == EPI_DACT,
+                    EPI == EPI_DACT || EPI == EPI_LINEAR,
                 "forward / dgrad epilogues");
   // the codebook first: its LDS address fits a ds_read's immediate offset
   __shared__ __attribute__((aligned(64))) float sCode[kC8 ? 256 : 16];
@@ -764,6 +767,36 @@ __global__ __launch_bounds__(wide::Shape<WM>::kThreads, 1) void gemm_wide_kernel
         if (lane < 32 && lrow + i * 32 < valid_rows) g.partial[(seg + row0 + rr[i]) * int64_t(npb) + blk] = pr;
       }
     }
+  } else if (EPI == EPI_LINEAR) {
+    // Each row tile of the wave (32 rows x 128 columns, fp32) is staged in the
+    // wave's own LDS rows and worked on row by row, so that residual, kept
+    // pre-activation and y move in runs of 256 bytes or more of a row
+    constexpr int kLinSt = 128 + 4;
+    static_assert(EPI != EPI_LINEAR || 4 * 32 * kLinSt * 4 <= 2 * kBM * kLds * 2, "four waves' staging rows fit a stage pair");
+    __syncthreads();  // every wave has read its last fragments of the stages
+    float *stg = reinterpret_cast<float *>(wave < 4 ? sA[0] : sB[0]) + (wave & 3) * 32 * kLinSt;
+    const int cc = (lane & 15) * 8, col = nt * kBN + wn * 128 + cc;
+    float bias[8] = {};
+    if (g.lin.bias && col < g.N) load_row<8>(g.lin.bias + int64_t(e) * g.N + col, bias);
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16 &a = acc[i][j];
+          *reinterpret_cast<f32x4 *>(stg + (lane & 31) * kLinSt + j * 32 + 8 * q + 4 * (lane >> 5)) =
+              f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+        }
+      // (the wave's own rows: LDS keeps one wave's operations in order)
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const int r = 4 * it + (lane >> 4), trow = wm * kRowsW + i * 32 + r;
+        float v[8];
+        load_row<8>(stg + r * kLinSt + cc, v);
+        if (trow < valid_rows && col < g.N) linear_epilogue<8>(g.lin, (int64_t(seg) + row0 + trow) * g.N + col, bias, v);
+      }
+    }
   } else {  // EPI_ACT: ungated, h = this tile's columns of the up projection, a = silu(h)
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
@@ -819,6 +852,7 @@ hipError_t launch_gemm_wide(GemmVariant v, const GemmArgs &a, hipStream_t s, con
       E4B_WIDE(A_GATHER, B_NT, EPI_ACT);
     case GEMM_DOWN_FWD: E4B_WIDE(A_DIRECT, B_NT, EPI_STORE);
     case GEMM_GATE_UP_DGRAD: E4B_WIDE(A_DIRECT, B_NN, EPI_STORE);
+    case GEMM_LINEAR: E4B_WIDE_SK(A_DIRECT, B_NT, EPI_LINEAR, false);
     case GEMM_DOWN_DGRAD:
       if (a.gated) E4B_WIDE(A_GATHER, B_NN, EPI_DSWIGLU);
       E4B_WIDE(A_GATHER, B_NN, EPI_DACT);

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "plan.h"
+#include "plan_block.h"
 
 namespace e4b {
 
@@ -23,7 +24,8 @@ enum GemmVariant {
   GEMM_GATE_UP_FWD = 0,   // A gathered x,      B = W_gu rows,    SiLU*up (or SiLU) epilogue
   GEMM_DOWN_FWD = 1,      // A sorted a,        B = W_dn rows,    bf16 store
   GEMM_DOWN_DGRAD = 2,    // A gathered grad_y, B = W_dn^T,       SiLU-backward epilogue
-  GEMM_GATE_UP_DGRAD = 3  // A sorted dGU,      B = W_gu^T,       bf16 store
+  GEMM_GATE_UP_DGRAD = 3, // A sorted dGU,      B = W_gu^T,       bf16 store
+  GEMM_LINEAR = 4         // A sorted rows,     B = W rows,       bias, activation, residual
 };
 
 struct GemmArgs {
@@ -61,6 +63,9 @@ struct GemmArgs {
   const float *lora_p;
   const uint16_t *lora_w;
   int32_t lora_rows;
+  // GEMM_LINEAR: bias [E, N], residual [rows, N], the kept pre-activation [rows, N]
+  // (each may be null), y [rows, N] in bf16 or fp32 (null: only pre)
+  LinearArgs lin;
 };
 
 // Launch of `kernel` on `s`, bracketed by the call's events for kernel id

@@ -134,10 +134,16 @@ __device__ __forceinline__ void decode_piece(const Piece<SK> &p, const float *co
       o[q >> 2][q & 3] = pack_bf16x2(__fmul_rn(code[w & 255], p.s), __fmul_rn(code[(w >> 8) & 255], p.s));
     }
   } else {
+    // the byte offsets 4 code of a word's high (even) and low (odd) nibbles, a byte each;
+    // one byte permute then makes an address
+    const char *tbl = reinterpret_cast<const char *>(code);
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
-      const uint32_t b = p.v[0][q >> 2] >> (8 * (q & 3));
-      o[q >> 2][q & 3] = pack_bf16x2(__fmul_rn(code[(b >> 4) & 15], p.s), __fmul_rn(code[b & 15], p.s));
+      const uint32_t w = p.v[0][q >> 2], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
+      const uint32_t sel = 0x0C0C0C00u | uint32_t(q & 3);
+      const float a = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
+      const float b = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
+      o[q >> 2][q & 3] = pack_bf16x2(__fmul_rn(a, p.s), __fmul_rn(b, p.s));
     }
   }
 }
@@ -339,6 +345,184 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
     rows_of(std::integral_constant<int, 1>{});
 }
 
+// ---- few rows to an expert ----
+
+// A decode step's experts have a row or two each, so the touched weights are the
+// whole cost and each is read once: no row tile is worth filling, and there is
+// no time for a tile map. Workgroup (column group, n-th expert with rows, row
+// slice) takes the expert's rows straight from the offsets, 16 MT at a time. One MFMA 16x16x32
+// takes 16 weight rows (the A operand: a lane's D registers are 4 consecutive
+// columns of one row) and 16 of the expert's rows. A lane reads 16 bytes of
+// codes = 32 consecutive k of its weight row, the operands of four MFMAs; the
+// order of k inside the 128 of a step is the same for x, so the weights go from
+// HBM to the MFMA through registers alone, kRowDepth steps in flight per wave.
+// x waits in LDS (kRowK / MT columns of it at a time); rows past the expert's
+// last are not filled, since each only reaches its own results. The 8 waves lie
+// along the columns (8 / wk) and along k (wk slices, joined through LDS in
+// order).
+constexpr int kRowThreads = 512;
+constexpr int kRowStep = 128;  // k per step
+constexpr int kRowK = 2048;    // k of x in LDS for 16 rows
+constexpr int kRowDepth = 4;
+// 16 waves per CU: each workgroup's start (offsets, x, the first weights) costs
+// about 4 us, so more slices than the chip needs are slower (64 rows on 40 of
+// 128 experts, nf4 2048 -> 1536: 28 us with 1 slice, 33 with 2, 43 with 4; 8 rows
+// of bf16 2048 -> 128: 20.4 us with 1 slice, 6.5 with 8)
+constexpr int64_t kRowWaves = 4096;
+
+template <int SK, int MT>
+__global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, const int32_t *__restrict__ offsets,
+                                                                  int32_t rows, int wk) {
+  constexpr int kK = kRowK / MT, kLd = kK + 8;
+  __shared__ __attribute__((aligned(64))) float code[SK == LK_CODE8 ? 256 : 16];
+  __shared__ __attribute__((aligned(16))) uint16_t sx[16 * MT * kLd];
+  static_assert(8 * MT * 64 * 16 <= sizeof(sx), "the slices' sums fit x's place");
+  const int tid = threadIdx.x, lane = tid & 63;
+  // uniform over the wave, so that the loops below branch on scalars
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = 8 / wk, slice = wave % wk;
+  int e = offsets ? -1 : 0;
+  int32_t lo = 0, hi = rows;
+  if (offsets) {
+    // blockIdx.y counts the experts that have rows: a workgroup for every expert
+    // spent more on starting the idle ones than the products took
+    int skip = blockIdx.y;
+    for (int e0 = 0; e0 < g.E && e < 0; e0 += 64) {
+      const int i = min(e0 + lane, g.E - 1);
+      int32_t a = offsets[i], b = offsets[i + 1];
+      a = min(max(a, 0), rows);
+      b = min(max(b, 0), rows);
+      uint64_t has = __ballot(e0 + lane < g.E && b > a);
+      const int n = __popcll(has);
+      if (skip < n) {
+        for (; skip > 0; --skip) has &= has - 1;
+        const int at = __ffsll(static_cast<unsigned long long>(has)) - 1;
+        e = e0 + at;
+        lo = __builtin_amdgcn_readlane(a, at);
+        hi = __builtin_amdgcn_readlane(b, at);
+      } else {
+        skip -= n;
+      }
+    }
+  }
+  if (offsets && blockIdx.y == gridDim.y - 1) {  // the rows of no expert
+    const int64_t live = clamped_offset(offsets, g.E, g.E, rows), n = int64_t(16 * wn);
+    for (int64_t i = int64_t(blockIdx.z) * kRowThreads + tid; i < (rows - live) * n;
+         i += int64_t(gridDim.z) * kRowThreads) {
+      const int64_t c = int64_t(blockIdx.x) * n + i % n, at = (live + i / n) * g.out + c;
+      if (c >= g.out) continue;
+      if (g.pre) g.pre[at] = 0.0f;
+      if (!g.y) continue;
+      if (g.y_f32)
+        static_cast<float *>(g.y)[at] = 0.0f;
+      else
+        static_cast<uint16_t *>(g.y)[at] = 0;
+    }
+    return;
+  }
+  if (e < 0 || lo + int32_t(blockIdx.z) * 16 * MT >= hi) return;
+
+  const int col0 = (blockIdx.x * wn + wave / wk) * 16;  // the wave's columns
+  const int m = lane & 15, grp = lane >> 4;
+  const int64_t w_row = min(col0 + m, g.out - 1);
+  Piece<SK> f[kRowDepth];
+  // the wave's steps of the chunk at k0: k0 + (slice + i wk) 128; in is a
+  // multiple of 64, so the last step may be half
+  auto load = [&](int k0, int i, Piece<SK> &p) {
+    const int k = k0 + (slice + i * wk) * kRowStep + grp * 32;
+    load_piece<SK>(g, e, w_row, k < g.in ? k : 0, p);
+  };
+  fill_codes<SK>(code, g.cb);
+  for (int32_t r0 = lo + blockIdx.z * 16 * MT; r0 < hi; r0 += gridDim.z * 16 * MT) {
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int n_rows = min(16 * MT, hi - r0);
+    for (int k0 = 0; k0 < g.in; k0 += kK) {
+      const int len = min(kK, g.in - k0);
+      const int all = (len + kRowStep - 1) / kRowStep;       // steps of the chunk
+      const int mine = (all - slice + wk - 1) / wk;          // this slice's
+#pragma unroll
+      for (int d = 0; d < kRowDepth; ++d)
+        if (d < mine) load(k0, d, f[d]);
+      __syncthreads();  // the last chunk's x has been read
+      // a half step's second half meets zeros
+      const int per_row = all * (kRowStep / 8);
+      for (int i = tid; i < n_rows * per_row; i += kRowThreads) {
+        const int r = i / per_row, c = (i - r * per_row) * 8;
+        u32x4 v = u32x4{0u, 0u, 0u, 0u};
+        if (c < len) v = *reinterpret_cast<const u32x4 *>(g.A + int64_t(r0 + r) * g.in + k0 + c);
+        *reinterpret_cast<u32x4 *>(sx + r * kLd + c) = v;
+      }
+      // the pieces came in before x: nothing is in flight, which the compiler
+      // cannot know, and without it the loop would wait for its youngest load
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+      __syncthreads();
+      auto step = [&](int i, const u32x4 (&w)[4]) {
+        const uint16_t *xs = sx + m * kLd + (slice + i * wk) * kRowStep + grp * 32;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int q = 0; q < MT; ++q)
+            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, w[j]), *reinterpret_cast<const bf16x8 *>(xs + q * 16 * kLd + 8 * j), acc[q],
+                0, 0, 0);
+      };
+      // whole runs of kRowDepth steps without a branch (past the end the loads
+      // repeat the last step), then what is left, which is in the registers
+      int i = 0;
+      for (; i + kRowDepth <= mine; i += kRowDepth)
+#pragma unroll
+        for (int d = 0; d < kRowDepth; ++d) {
+          u32x4 w[4];
+          decode_piece<SK>(f[d], code, w);
+          load(k0, min(i + d + kRowDepth, mine - 1), f[d]);
+          step(i + d, w);
+        }
+#pragma unroll
+      for (int d = 0; d < kRowDepth - 1; ++d)
+        if (i + d < mine) {
+          u32x4 w[4];
+          decode_piece<SK>(f[d], code, w);
+          step(i + d, w);
+        }
+    }
+    if (wk > 1) {
+      float(*part)[MT][64 * 4] = reinterpret_cast<float(*)[MT][64 * 4]>(sx);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4 *>(&part[wave][i][lane * 4]) = acc[i];
+      __syncthreads();
+      if (slice == 0)
+        for (int q = 1; q < wk; ++q)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[i] += *reinterpret_cast<const f32x4 *>(&part[wave + q][i][lane * 4]);
+    }
+    if (slice == 0) {
+      const int c = col0 + 4 * grp;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int32_t r = r0 + i * 16 + m;
+        if (r >= hi) continue;
+        if (g.out % 4 == 0) {
+          if (c < g.out) {
+            float b[4] = {}, v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+            if (g.bias) load_row<4>(g.bias + int64_t(e) * g.out + c, b);
+            linear_epilogue<4>(g, int64_t(r) * g.out + c, b, v);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (c + q < g.out) {
+              float b[1] = {g.bias ? g.bias[int64_t(e) * g.out + c + q] : 0.0f}, v[1] = {acc[i][q]};
+              linear_epilogue<1>(g, int64_t(r) * g.out + c + q, b, v);
+            }
+        }
+      }
+    }
+  }
+}
+
 // ---- dz and the bias gradient ----
 
 // dz[row, c] = bf16(grad_y act'(pre)), zeros for the columns that pad a row to
@@ -363,8 +547,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs g, const G *_
       load_row<VEC>(gy + (row0 + r) * g.out + col, v);
       if (g.act != E4B_ACT_NONE) {
         load_row<VEC>(pre + (row0 + r) * g.out + col, z);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) v[q] *= act_grad(g.act, z[q]);
+        act_grads<VEC>(g.act, z, v);
       }
 #pragma unroll
       for (int q = 0; q < VEC; ++q) sum[q] += v[q];
@@ -416,6 +599,107 @@ hipError_t launch_tiles(const LinearArgs &a, int64_t m_bound, hipStream_t s) {
     default: hipLaunchKernelGGL((linear_tile_kernel<LK_ABSMAX, NN>), grid, block, 0, s, a); break;
   }
   return hipGetLastError();
+}
+
+template <int MT>
+hipError_t launch_rows_mt(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, hipStream_t s) {
+  // enough waves to fill the chip from the experts that can have rows, and a step of k for each slice
+  const int64_t busy = a.E < p.rows ? a.E : p.rows, groups = (a.out + 15) / 16;
+  const int64_t steps = (a.in < kRowK / MT ? a.in : kRowK / MT) / kRowStep;
+  int wk = 1;
+  while (wk < 8 && 2 * wk <= steps && busy * groups * wk < kRowWaves) wk *= 2;
+  const int64_t slabs = (groups + 8 / wk - 1) / (8 / wk);
+  // one expert: its row slices side by side; several: few rows each, unless the
+  // routing sends most of many rows to one
+  const int64_t z = a.E > 1 ? (p.rows > 256 ? 4 : 1) : (p.rows + 16 * MT - 1) / (16 * MT);
+  const dim3 grid(uint32_t(slabs), uint32_t(busy + (offsets ? 1 : 0)), uint32_t(z < 65535 ? z : 65535));
+  const dim3 block(kRowThreads);
+  const int32_t rows = int32_t(p.rows);
+  switch (a.cb) {
+    case E4B_CB_BF16: hipLaunchKernelGGL((linear_rows_kernel<LK_BF16, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
+    case E4B_CB_MXFP4: hipLaunchKernelGGL((linear_rows_kernel<LK_MX, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
+    case E4B_CB_INT8:
+    case E4B_CB_FP8:
+      hipLaunchKernelGGL((linear_rows_kernel<LK_CODE8, MT>), grid, block, 0, s, a, offsets, rows, wk);
+      break;
+    default: hipLaunchKernelGGL((linear_rows_kernel<LK_ABSMAX, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rows(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, hipStream_t s) {
+  const int64_t mean = (p.rows + a.E - 1) / a.E;
+  return mean <= 16 ? launch_rows_mt<1>(p, a, offsets, s)
+                    : mean <= 32 ? launch_rows_mt<2>(p, a, offsets, s) : launch_rows_mt<4>(p, a, offsets, s);
+}
+
+// The 256 x 256 tiles of the routed MLP's GEMM (gemm_wide.hip) for this product.
+GemmArgs wide_args(const LinearPlan &p, const LinearArgs &a, bool nn) {
+  GemmArgs w{};
+  w.A = a.A;
+  w.lda = int32_t(a.lda);
+  w.topk = 1;
+  w.Wp = a.packed;
+  w.mx = a.cb == E4B_CB_MXFP4;
+  w.Wa = w.mx ? nullptr : a.absmax;
+  w.Ws = w.mx ? a.scales : nullptr;
+  const int64_t n = int64_t(a.out) * a.in;
+  w.w_e_bytes = a.cb == E4B_CB_BF16 ? n * 2 : a.cb == E4B_CB_INT8 || a.cb == E4B_CB_FP8 ? n : n / 2;
+  w.w_e_blocks = a.cb == E4B_CB_BF16 ? 0 : n / (w.mx ? kMxBlock : kBlock);
+  w.w_in = a.in;
+  w.N = nn ? a.in : a.out;
+  w.K = nn ? a.out : a.in;
+  w.I = w.N;
+  w.tile_offsets = a.tile_offsets;
+  w.tile_map = a.tile_map;
+  w.E = a.E;
+  w.cb = a.cb;
+  w.n_tiles = (w.N + kBNWide - 1) / kBNWide;
+  w.grid = uint32_t((p.rows / kBM + (a.E < p.rows ? a.E : p.rows)) * w.n_tiles);
+  w.lin = a;
+  if (nn) {
+    w.C = static_cast<uint16_t *>(a.y);
+    w.ldc = a.in;
+  }
+  return w;
+}
+
+// How a product's rows are tiled: by the kernel for few rows, or in 128- or
+// 256-row tiles (us on one MI355X, nf4 unless said; rows / 128 / 256):
+//   few rows to an expert (up to 8 on average): 64 experts of 2048 -> 2048, 4 rows
+//     each 48 / 97 / 117; 16 each 83 / 97 / 119; 32 each 108 / 97 / 123
+//   one expert, up to 2^20 outputs: 2048 -> 4096, 256 rows 22 / 38 / 55, 512 rows
+//     41 / 39 / 55; 4096 -> 14336, 64 rows 41 / 67 / 98, 128 rows 83 / 69 / 98; bf16
+//     weights (four times the bytes to read again for every 64 rows) up to 2^18:
+//     4096 -> 4096, 64 rows 40 / 48 / 81, 256 rows 82 / 50 / 82
+//   256-row tiles when the experts fill half of one each and the 128-row tiles are more
+//     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
+//     - / 43 / 57, 2048 rows - / 64 / 62 (with GELU and a residual, which two workgroups
+//     to a CU overlap, 66 / 74), 4096 rows - / 117 / 76; 64 experts of 2048 -> 2048, 96
+//     rows each 222 / 108 / 133, 128 each 263 / 154 / 138
+enum { TILE_ROWS = 0, TILE_128 = 128, TILE_256 = 256 };
+
+bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
+  // (the wide tiles address their rows in 32 bits)
+  const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
+  const int64_t tiles = (rows + 64 * (st->E - 1)) / kTM * ((cols + kTN - 1) / kTN);  // a ragged one for every other expert
+  return rows >= 128 * st->E && tiles > 512 && rows * longest < (int64_t(1) << 32);
+}
+
+int forward_tiles(const e4b_stack *st, int64_t rows) {
+  const int64_t few = st->codebook == E4B_CB_BF16 ? int64_t(1) << 18 : int64_t(1) << 20;
+  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out <= few) return TILE_ROWS;
+  return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
+}
+
+int dgrad_tiles(const e4b_stack *st, int64_t rows) {
+  return st->out % kBK == 0 && fills_wide_tiles(st, rows, st->in) ? TILE_256 : TILE_128;
+}
+
+hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, int tiles, hipStream_t s) {
+  if (tiles == TILE_ROWS) return launch_rows(p, a, offsets, s);
+  if (tiles == TILE_128) return launch_tiles<false>(a, p.m_bound, s);
+  return launch_grouped_gemm(GEMM_LINEAR, wide_args(p, a, false), s);
 }
 
 hipError_t launch_map(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, int bm, int64_t bound,
@@ -495,8 +779,10 @@ extern "C" e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const
   a.y = y;
   a.y_f32 = y_dtype == E4B_F32;
   a.pre = pre;
-  E4B_TRY(launch_map(p, a, offsets, kTM, p.m_bound, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
-  E4B_TRY(launch_tiles<false>(a, p.m_bound, stream));
+  const int tiles = forward_tiles(st, rows);
+  if (tiles != TILE_ROWS)
+    E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
+  E4B_TRY(launch_forward(p, a, offsets, tiles, stream));
   return E4B_OK;
 }
 
@@ -525,7 +811,12 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   char *w = static_cast<char *>(ws);
   LinearArgs a = args_of(p, st, w);
   a.act = act;
-  E4B_TRY(launch_map(p, a, offsets, kTM, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
+  const int tiles = dgrad_tiles(st, rows), again = recompute ? forward_tiles(st, rows) : tiles;
+  // the recomputed forward takes the forward's tiles, for the same bits
+  if (recompute && again != TILE_ROWS && again != tiles)
+    E4B_TRY(launch_map(p, a, offsets, again, p.m_bound, nullptr, 0, nullptr, 0, stream));
+  if (!recompute || again == TILE_ROWS || again == tiles)
+    E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
   if (recompute) {
     // exactly the forward's pre-activation
     LinearArgs f = a;
@@ -533,7 +824,9 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
     f.lda = st->in;
     f.bias = bias;
     f.pre = reinterpret_cast<float *>(w + p.off_pre);
-    E4B_TRY(launch_tiles<false>(f, p.m_bound, stream));
+    E4B_TRY(launch_forward(p, f, offsets, again, stream));
+    if (again != TILE_ROWS && again != tiles)
+      E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
     pre = f.pre;
   }
   const bool f32 = gy_dtype == E4B_F32;
@@ -557,6 +850,9 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   a.A = direct ? static_cast<const uint16_t *>(grad_y) : dz;
   a.lda = direct ? st->out : p.ldz;
   a.y = grad_x_bf16;
-  E4B_TRY(launch_tiles<true>(a, p.m_bound, stream));
+  if (tiles == TILE_256)
+    E4B_TRY(launch_grouped_gemm(GEMM_GATE_UP_DGRAD, wide_args(p, a, true), stream));
+  else
+    E4B_TRY(launch_tiles<true>(a, p.m_bound, stream));
   return E4B_OK;
 }

@@ -17,77 +17,79 @@ namespace e4b {
 namespace {
 
 constexpr int kOrderThreads = 1024;
-constexpr int kOrderIt = 32;                                   // ids per lane and pass
-constexpr int kOrderPass = kOrderThreads * kOrderIt;           // 32768 pairs per pass
+constexpr int kOrderIt = 32;                          // ids per lane and pass
+constexpr int kOrderPass = kOrderThreads * kOrderIt;  // 32768 pairs per pass
+constexpr int kOrderSmall = 4096;                     // pairs that one launch orders and copies
 constexpr int kGatherThreads = 256;
+template <int KU>
+constexpr int kUnpermutePieces = KU == 2 ? 2 : 1;
+
+// The bucket of an id: itself, or E for one outside [0, E).
+__device__ __forceinline__ uint32_t bucket(int32_t id, int E) { return min(uint32_t(id), uint32_t(E)); }
 
 // One workgroup per bucket e (the experts, then the bucket of dropped pairs).
-// It reads every id: lower keys give the bucket's first position, equal ones
+// It reads every id: lower buckets give this one's first position, equal ones
 // the ranks. A wave takes runs of 64 consecutive pairs, so the compare's lane
 // mask is the rank information: position = base + masks' population before it.
 // E + 1 readings of 4 P bytes come from L2 and stay far below the rows' own
 // traffic (P = 32768, E = 64: 8.5 MB against 151 MB).
-__global__ __launch_bounds__(kOrderThreads) void order_kernel(const int32_t *__restrict__ ids, int64_t P, int E,
+__global__ __launch_bounds__(kOrderThreads) void order_kernel(const int32_t *__restrict__ ids, int32_t P, int E,
                                                               int32_t *__restrict__ offsets,
                                                               int32_t *__restrict__ sorted,
                                                               int32_t *__restrict__ pos) {
   __shared__ int32_t s_less[kOrderThreads / 64], s_eq[kOrderThreads / 64];
   const uint32_t e = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t below = (1ull << lane) - 1;
-  const bool drop = e == uint32_t(E);
-  auto equal = [&](int32_t id) { return drop ? uint32_t(id) >= uint32_t(E) : uint32_t(id) == e; };
-  uint64_t mask[kOrderIt];
-  int32_t less = 0, eq = 0;
-  // the masks of the wave's ids in the pass at p0
-  auto scan = [&](int64_t p0, bool count_less) {
-    const int64_t w0 = p0 + int64_t(wave) * (64 * kOrderIt);
-    int32_t id[kOrderIt];
+  uint32_t b[kOrderIt];  // the lane's buckets of one pass; past the end, one that nothing matches
+  auto fetch = [&](int32_t p0) {
+    const int32_t w0 = p0 + wave * (64 * kOrderIt) + lane;
+    // (clamped rather than guarded: the loads stay together, ahead of their first use)
 #pragma unroll
-    for (int i = 0; i < kOrderIt; ++i) {
-      const int64_t p = w0 + i * 64 + lane;
-      id[i] = p < P ? ids[p] : 0;
-    }
+    for (int i = 0; i < kOrderIt; ++i) b[i] = uint32_t(ids[min(w0 + i * 64, P - 1)]);
+#pragma unroll
+    for (int i = 0; i < kOrderIt; ++i) b[i] = w0 + i * 64 < P ? bucket(int32_t(b[i]), E) : 0xFFFFFFFFu;
+  };
+  int32_t less = 0, eq = 0;
+  for (int32_t p0 = 0; p0 < P; p0 += kOrderPass) {
+    fetch(p0);
+#pragma unroll
+    for (int i = 0; i < kOrderIt; ++i) less += b[i] < e ? 1 : 0;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) less += __shfl_xor(less, o);
+  if (lane == 0) s_less[wave] = less;
+  int32_t before = 0;  // pairs of the bucket in earlier passes
+  for (int32_t p0 = 0; p0 < P; p0 += kOrderPass) {
+    if (P > kOrderPass) fetch(p0);
     eq = 0;
 #pragma unroll
-    for (int i = 0; i < kOrderIt; ++i) {
-      const bool in = w0 + i * 64 + lane < P;
-      mask[i] = __ballot(in && equal(id[i]));
-      eq += __popcll(mask[i]);
-      if (count_less) less += __popcll(__ballot(in && uint32_t(id[i]) < e));
-    }
-  };
-  // first: how many pairs come before the bucket. One pass keeps its masks.
-  int64_t total_eq = 0;
-  for (int64_t p0 = 0; p0 < P; p0 += kOrderPass) scan(p0, true);
-  if (lane == 0) s_less[wave] = less;
-  __syncthreads();
-  int32_t first = 0;
-  for (int w = 0; w < kOrderThreads / 64; ++w) first += s_less[w];
-  if (threadIdx.x == 0 && e < uint32_t(E) + 1) offsets[e] = first;
-  // then the ranks, pass by pass
-  for (int64_t p0 = 0; p0 < P; p0 += kOrderPass) {
-    if (P > kOrderPass) scan(p0, false);
+    for (int i = 0; i < kOrderIt; ++i) eq += __popcll(__ballot(b[i] == e));
     __syncthreads();
     if (lane == 0) s_eq[wave] = eq;
     __syncthreads();
-    int64_t at = first + total_eq;
-    int32_t all = 0;
+    int32_t at = before;
     for (int w = 0; w < kOrderThreads / 64; ++w) {
-      if (w < wave) at += s_eq[w];
-      all += s_eq[w];
+      at += s_less[w] + (w < wave ? s_eq[w] : 0);
+      before += s_eq[w];
     }
-    total_eq += all;
-    const int64_t w0 = p0 + int64_t(wave) * (64 * kOrderIt);
+    const int32_t w0 = p0 + wave * (64 * kOrderIt) + lane;
 #pragma unroll
     for (int i = 0; i < kOrderIt; ++i) {
-      if ((mask[i] >> lane) & 1) {
-        const int32_t p = int32_t(w0) + i * 64 + lane, s = int32_t(at) + __popcll(mask[i] & below);
-        sorted[s] = p;
-        pos[p] = s;
+      const uint64_t m = __ballot(b[i] == e);
+      if (b[i] == e) {
+        const int32_t s = at + __popcll(m & below);
+        sorted[s] = w0 + i * 64;
+        pos[w0 + i * 64] = s;
       }
-      at += __popcll(mask[i]);
+      at += __popcll(m);
     }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int32_t first = 0;
+    for (int w = 0; w < kOrderThreads / 64; ++w) first += s_less[w];
+    offsets[e] = first;
   }
 }
 
@@ -124,108 +126,192 @@ __global__ __launch_bounds__(kGatherThreads) void gather_kernel(const T *__restr
   copy_row<T, VEC>(x, t, k, H, s_pos, offsets[E], rows);
 }
 
-// y[t] = sum_j w[t, j] rows[pos(t, j)] (no weights: the plain sum, which is
-// the gradient of the copies). One workgroup per token and kGatherThreads *
-// VEC columns, up to 8 rows in flight.
+// Few pairs: one launch instead of two. The workgroup of token t counts its
+// pairs' places from all the ids, which it holds in LDS (a wave per slot: 64
+// compares and one population count per 64 ids), then copies its row; the
+// workgroup behind the tokens' writes the offsets. 8 tokens of 128 experts:
+// 4.6 us against 9.3 + 2.9 in two launches.
 template <typename T, int VEC>
-__global__ __launch_bounds__(kGatherThreads) void unpermute_kernel(const T *__restrict__ rows, int k, int H, int E,
-                                                                   const int32_t *__restrict__ offsets,
-                                                                   const int32_t *__restrict__ pos,
-                                                                   const float *__restrict__ w, T *__restrict__ y) {
+__global__ __launch_bounds__(kGatherThreads) void order_gather_kernel(const int32_t *__restrict__ ids, int32_t n_tok,
+                                                                      const T *__restrict__ x, int k, int H, int E,
+                                                                      int32_t *__restrict__ offsets,
+                                                                      int32_t *__restrict__ sorted,
+                                                                      int32_t *__restrict__ pos, T *__restrict__ rows) {
+  __shared__ uint16_t s_b[kOrderSmall];
   __shared__ int32_t s_pos[kMaxTopK];
-  __shared__ float s_w[kMaxTopK];
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x < k) {
-    const int32_t s = pos[t * k + threadIdx.x], live = offsets[E];
-    s_pos[threadIdx.x] = s >= 0 && s < live ? s : -1;
-    s_w[threadIdx.x] = w ? w[t * k + threadIdx.x] : 1.0f;
+  __shared__ int32_t s_n[kMaxE + 1];
+  const int P = n_tok * k, t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < P; i += kGatherThreads) s_b[i] = uint16_t(bucket(ids[i], E));
+  if (t == n_tok) {
+    for (int e = threadIdx.x; e <= E; e += kGatherThreads) s_n[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < P; i += kGatherThreads) atomicAdd(&s_n[s_b[i]], 1);
+    __syncthreads();
+    if (wave == 0) {
+      // pairs of lower buckets, 64 buckets at a time
+      int32_t carry = 0;
+      for (int e0 = 0; e0 <= E; e0 += 64) {
+        const int e = e0 + lane;
+        const int32_t v = e <= E ? s_n[e] : 0;
+        int32_t incl = v;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int32_t u = __shfl_up(incl, o);
+          if (lane >= o) incl += u;
+        }
+        if (e <= E) offsets[e] = carry + incl - v;
+        carry += __shfl(incl, 63);
+      }
+    }
+    return;
   }
   __syncthreads();
-  const int h = (blockIdx.y * kGatherThreads + threadIdx.x) * VEC;
-  if (h >= H) return;
-  float acc[VEC];
-#pragma unroll
-  for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    float v[8][VEC];
-#pragma unroll
-    for (int jj = 0; jj < 8; ++jj)
-      if (j0 + jj < k && s_pos[j0 + jj] >= 0) load_row<VEC>(rows + int64_t(s_pos[j0 + jj]) * H + h, v[jj]);
-#pragma unroll
-    for (int jj = 0; jj < 8; ++jj)
-      if (j0 + jj < k && s_pos[j0 + jj] >= 0) {
-        const float wj = s_w[j0 + jj];
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] += wj * v[jj][q];
-      }
+  for (int j = wave; j < k; j += kGatherThreads / 64) {
+    const int p = t * k + j;
+    const uint32_t b = s_b[p];
+    int32_t s = 0;
+    for (int q0 = 0; q0 < P; q0 += 64) {
+      const int q = q0 + lane;
+      const uint32_t c = q < P ? s_b[q] : 0xFFFFFFFFu;
+      s += __popcll(__ballot(c < b || (c == b && q < p)));
+    }
+    if (lane == 0) {
+      s_pos[j] = b == uint32_t(E) ? ~s : s;  // (complement: a dropped pair)
+      sorted[s] = p;
+      pos[p] = s;
+    }
   }
-  store_row<VEC>(y + t * H + h, acc);
+  if (!rows) return;
+  __syncthreads();
+  for (int h = threadIdx.x * VEC; h < H; h += kGatherThreads * VEC) {
+    float f[VEC], zero[VEC];
+    load_row<VEC>(x + int64_t(t) * H + h, f);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) zero[q] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const int32_t s = s_pos[j];
+      if (s >= 0)
+        store_row<VEC>(rows + int64_t(s) * H + h, f);
+      else
+        store_row<VEC>(rows + int64_t(~s) * H + h, zero);
+    }
+  }
 }
 
-// grad_rows[pos(t, j)] = w[t, j] grad_y[t] and grad_w[t, j] = rows[pos(t, j)] . grad_y[t].
-// One workgroup per token: grad_y's row is read once per 8 slots, each pair's
-// row once; the dots end in a fixed tree over the workgroup.
-template <typename T, int VEC>
+// y[t] = sum_j w[t, j] rows[pos(t, j)], in slot order (no weights: the plain
+// sum, which is the gradient of the copies). One workgroup per token and
+// slab of columns, so that its places and weights are scalars and a row's
+// neighbouring pieces are read together: a wave per token, or per token and 1
+// KB of its row, was slower (8192 x 2 x 4096 bf16: 57 us). KU slots and CU
+// pieces are in flight at a time.
+template <typename T, int VEC, int KU>
+__global__ __launch_bounds__(kGatherThreads) void unpermute_kernel(const T *__restrict__ rows, int64_t n_tok, int k,
+                                                                   int H, int E, const int32_t *__restrict__ offsets,
+                                                                   const int32_t *__restrict__ pos,
+                                                                   const float *__restrict__ w, T *__restrict__ y) {
+  constexpr int CU = kUnpermutePieces<KU>;
+  constexpr int kPiece = kGatherThreads * VEC;
+  const int64_t t = blockIdx.x;
+  const int32_t live = int32_t(min(int64_t(offsets[E]), n_tok * k));  // no place leads out of the rows
+  const int h0 = blockIdx.y * CU * kPiece + threadIdx.x * VEC;
+  float acc[CU][VEC];
+#pragma unroll
+  for (int c = 0; c < CU; ++c)
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) acc[c][q] = 0.0f;
+  for (int j0 = 0; j0 < k; j0 += KU) {
+    Raw<T, VEC> v[KU][CU];
+    float wj[KU];
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      const int32_t s = j0 + j < k ? pos[t * k + j0 + j] : -1;
+      const bool in = s >= 0 && s < live;
+      wj[j] = w && j0 + j < k ? w[t * k + j0 + j] : 1.0f;
+      if (!in) wj[j] = 0.0f;  // (its piece is zeros, whatever the row holds)
+#pragma unroll
+      for (int c = 0; c < CU; ++c) v[j][c].fetch(rows + int64_t(s) * H + h0 + c * kPiece, in && h0 + c * kPiece < H);
+    }
+#pragma unroll
+    for (int j = 0; j < KU; ++j)
+#pragma unroll
+      for (int c = 0; c < CU; ++c) {
+        float f[VEC];
+        v[j][c].get(f);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[c][q] += wj[j] * f[q];
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < CU; ++c)
+    if (h0 + c * kPiece < H) store_row<VEC>(y + t * H + h0 + c * kPiece, acc[c]);
+}
+
+// The gradients: a wave per token, so that nothing waits at a barrier for the
+// dots (8192 x 2 x 4096 bf16: 65 us; 78 with a workgroup per token).
+// grad_rows[pos(t, j)] = w[t, j] grad_y[t] and grad_w[t, j] = rows[pos(t, j)] . grad_y[t];
+// grad_y's row is read once per KU slots, each pair's row once. Lanes sum their
+// columns in ascending order, the 64 sums meet in a fixed tree.
+template <typename T, int VEC, int KU>
 __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
-    const T *__restrict__ rows, const T *__restrict__ gy, int64_t P, int k, int H, int E,
+    const T *__restrict__ rows, const T *__restrict__ gy, int64_t n_tok, int k, int H, int E,
     const int32_t *__restrict__ offsets, const int32_t *__restrict__ pos, const float *__restrict__ w,
     T *__restrict__ grows, float *__restrict__ gw) {
-  __shared__ int32_t s_pos[kMaxTopK];
-  __shared__ float s_w[kMaxTopK];
-  __shared__ float s_dot[kGatherThreads / 64][8];
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int CU = KU >= 8 ? 1 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t t = int64_t(blockIdx.x) * (kGatherThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= n_tok) return;
   const int32_t live = offsets[E];
-  if (threadIdx.x < k) {
-    const int32_t s = pos[t * k + threadIdx.x];
-    s_pos[threadIdx.x] = s >= 0 && s < P ? s : -1;
-    s_w[threadIdx.x] = w ? w[t * k + threadIdx.x] : 1.0f;
-  }
-  __syncthreads();
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    float dot[8];
+  const int64_t P = n_tok * k;
+  for (int j0 = 0; j0 < k; j0 += KU) {
+    int32_t s[KU];
+    float wj[KU], dot[KU];
 #pragma unroll
-    for (int jj = 0; jj < 8; ++jj) dot[jj] = 0.0f;
-    for (int h = threadIdx.x * VEC; h < H; h += kGatherThreads * VEC) {
-      float g[VEC];
-      load_row<VEC>(gy + t * H + h, g);
-      float v[8][VEC];
-      if (gw) {
+    for (int j = 0; j < KU; ++j) {
+      s[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+      if (s[j] >= P) s[j] = -1;
+      // a pair without an expert: zeros in its row, no weight gradient
+      wj[j] = s[j] >= live ? 0.0f : w && j0 + j < k ? w[t * k + j0 + j] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int h0 = lane * VEC; h0 < H; h0 += CU * 64 * VEC) {
+      float g[CU][VEC], v[KU][CU][VEC];
 #pragma unroll
-        for (int jj = 0; jj < 8; ++jj)
-          if (j0 + jj < k && s_pos[j0 + jj] >= 0 && s_pos[j0 + jj] < live)
-            load_row<VEC>(rows + int64_t(s_pos[j0 + jj]) * H + h, v[jj]);
+      for (int c = 0; c < CU; ++c) {
+        const int h = h0 + c * 64 * VEC;
+        if (h < H) load_row<VEC>(gy + t * H + h, g[c]);
       }
+      if (gw)
 #pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        if (j0 + jj >= k || s_pos[j0 + jj] < 0) continue;
-        const int32_t s = s_pos[j0 + jj];
-        const bool in = s < live;
-        float o[VEC];
+        for (int j = 0; j < KU; ++j)
+          if (s[j] >= 0 && s[j] < live)
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) o[q] = in ? s_w[j0 + jj] * g[q] : 0.0f;
-        store_row<VEC>(grows + int64_t(s) * H + h, o);
-        if (gw && in) {
+            for (int c = 0; c < CU; ++c) {
+              const int h = h0 + c * 64 * VEC;
+              if (h < H) load_row<VEC>(rows + int64_t(s[j]) * H + h, v[j][c]);
+            }
 #pragma unroll
-          for (int q = 0; q < VEC; ++q) dot[jj] += v[jj][q] * g[q];
+      for (int j = 0; j < KU; ++j) {
+        if (s[j] < 0) continue;
+#pragma unroll
+        for (int c = 0; c < CU; ++c) {
+          const int h = h0 + c * 64 * VEC;
+          if (h >= H) continue;
+          float o[VEC];
+#pragma unroll
+          for (int q = 0; q < VEC; ++q) o[q] = s[j] < live ? wj[j] * g[c][q] : 0.0f;
+          store_row<VEC>(grows + int64_t(s[j]) * H + h, o);
+          if (gw && s[j] < live)
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) dot[j] += v[j][c][q] * g[c][q];
         }
       }
     }
-    if (gw) {
+    if (gw)
 #pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        const float d = wave_sum(dot[jj]);
-        if (lane == 0) s_dot[wave][jj] = d;
+      for (int j = 0; j < KU; ++j) {
+        const float d = wave_sum(dot[j]);
+        if (lane == 0 && j0 + j < k) gw[t * k + j0 + j] = d;
       }
-      __syncthreads();
-      const int jj = threadIdx.x;
-      if (jj < 8 && j0 + jj < k) {
-        float d = 0.0f;
-        for (int q = 0; q < kGatherThreads / 64; ++q) d += s_dot[q][jj];
-        gw[t * k + j0 + jj] = d;
-      }
-      __syncthreads();
-    }
   }
 }
 
@@ -236,17 +322,41 @@ hipError_t gather(const OrderArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 template <typename T, int VEC>
+hipError_t order_gather(const OrderArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL((order_gather_kernel<T, VEC>), dim3(uint32_t(a.T + 1)), dim3(kGatherThreads), 0, s, a.ids,
+                     int32_t(a.T), static_cast<const T *>(a.x), a.k, a.H, a.E, a.out_offsets, a.out_sorted, a.out_pos,
+                     static_cast<T *>(a.rows));
+  return hipGetLastError();
+}
+template <typename T, int VEC>
 hipError_t unpermute(const OrderArgs &a, hipStream_t s) {
-  const uint32_t slabs = uint32_t((a.H + kGatherThreads * VEC - 1) / (kGatherThreads * VEC));
-  hipLaunchKernelGGL((unpermute_kernel<T, VEC>), dim3(uint32_t(a.T), slabs), dim3(kGatherThreads), 0, s,
-                     static_cast<const T *>(a.x), a.k, a.H, a.E, a.offsets, a.pos, a.w, static_cast<T *>(a.rows));
+  const int piece = kGatherThreads * VEC * (a.k <= 2 ? kUnpermutePieces<2> : 1);
+  const dim3 grid(uint32_t(a.T), uint32_t((a.H + piece - 1) / piece));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kGatherThreads), 0, s, static_cast<const T *>(a.x), a.T, a.k, a.H, a.E,
+                       a.offsets, a.pos, a.w, static_cast<T *>(a.rows));
+  };
+  if (a.k <= 2)
+    go(unpermute_kernel<T, VEC, 2>);
+  else if (a.k <= 4)
+    go(unpermute_kernel<T, VEC, 4>);
+  else
+    go(unpermute_kernel<T, VEC, 8>);
   return hipGetLastError();
 }
 template <typename T, int VEC>
 hipError_t unpermute_bwd(const OrderArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL((unpermute_bwd_kernel<T, VEC>), dim3(uint32_t(a.T)), dim3(kGatherThreads), 0, s,
-                     static_cast<const T *>(a.x), static_cast<const T *>(a.gy), a.T * a.k, a.k, a.H, a.E, a.offsets,
-                     a.pos, a.w, static_cast<T *>(a.rows), a.gw);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(uint32_t((a.T + 3) / 4)), dim3(kGatherThreads), 0, s, static_cast<const T *>(a.x),
+                       static_cast<const T *>(a.gy), a.T, a.k, a.H, a.E, a.offsets, a.pos, a.w,
+                       static_cast<T *>(a.rows), a.gw);
+  };
+  if (a.k <= 2)
+    go(unpermute_bwd_kernel<T, VEC, 2>);
+  else if (a.k <= 4)
+    go(unpermute_bwd_kernel<T, VEC, 4>);
+  else
+    go(unpermute_bwd_kernel<T, VEC, 8>);
   return hipGetLastError();
 }
 
@@ -256,12 +366,12 @@ hipError_t unpermute_bwd(const OrderArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_order(const int32_t *ids, const OrderArgs &a, int32_t *offsets, int32_t *sorted, int32_t *pos,
-                        hipStream_t s) {
-  hipLaunchKernelGGL(order_kernel, dim3(uint32_t(a.E + 1)), dim3(kOrderThreads), 0, s, ids, a.T * a.k, a.E, offsets,
-                     sorted, pos);
+hipError_t launch_order(const OrderArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(order_kernel, dim3(uint32_t(a.E + 1)), dim3(kOrderThreads), 0, s, a.ids, int32_t(a.T * a.k), a.E,
+                     a.out_offsets, a.out_sorted, a.out_pos);
   return hipGetLastError();
 }
+hipError_t launch_order_gather(const OrderArgs &a, hipStream_t s) { return E4B_ROWS(order_gather, a, s); }
 hipError_t launch_gather(const OrderArgs &a, hipStream_t s) { return E4B_ROWS(gather, a, s); }
 hipError_t launch_unpermute(const OrderArgs &a, hipStream_t s) { return E4B_ROWS(unpermute, a, s); }
 hipError_t launch_unpermute_bwd(const OrderArgs &a, hipStream_t s) { return E4B_ROWS(unpermute_bwd, a, s); }
@@ -287,12 +397,18 @@ extern "C" e4b_status e4b_permute(int64_t T, int32_t top_k, int64_t E, int64_t H
   if (!aligned16(offsets) || !aligned16(topk_idx) || !aligned16(sorted_pair) || !aligned16(pos_of_pair) ||
       !aligned16(x) || !aligned16(rows))
     return E4B_ERR_ALIGN;
-  E4B_TRY(launch_order(topk_idx, a, offsets, sorted_pair, pos_of_pair, stream));
-  if (!T || !rows) return E4B_OK;
+  a.ids = topk_idx;
   a.x = x;
   a.rows = rows;
-  a.offsets = offsets;
-  a.pos = pos_of_pair;
+  a.offsets = a.out_offsets = offsets;
+  a.out_sorted = sorted_pair;
+  a.pos = a.out_pos = pos_of_pair;
+  if (T * top_k <= kOrderSmall) {
+    E4B_TRY(launch_order_gather(a, stream));
+    return E4B_OK;
+  }
+  E4B_TRY(launch_order(a, stream));
+  if (!rows) return E4B_OK;
   E4B_TRY(launch_gather(a, stream));
   return E4B_OK;
 }

@@ -1,7 +1,7 @@
 // rowvec.h -- row pieces of bf16 / fp32 tensors as fp32 registers: VEC
 // consecutive elements per thread, one or two 16-byte accesses for VEC = 8
 // (rows whose length is a multiple of 8 elements keep every piece 16-byte
-// aligned), single elements for VEC = 1 (any other length).
+// aligned), half of that for VEC = 4, single elements for VEC = 1 (any length).
 #pragma once
 
 #include "device.h"
@@ -24,8 +24,15 @@ __device__ __forceinline__ void load_row(const bf16_t *p, float (&f)[VEC]) {
       f[2 * q] = bf16_lo(v[q]);
       f[2 * q + 1] = bf16_hi(v[q]);
     }
+  } else if constexpr (VEC == 4) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f[2 * q] = bf16_lo(v[q]);
+      f[2 * q + 1] = bf16_hi(v[q]);
+    }
   } else {
-    static_assert(VEC == 1, "16-byte pieces or single elements");
+    static_assert(VEC == 1, "16- or 8-byte pieces or single elements");
     f[0] = bf16_to_f32(p->v);
   }
 }
@@ -39,6 +46,10 @@ __device__ __forceinline__ void load_row(const float *p, float (&f)[VEC]) {
       f[q] = a[q];
       f[4 + q] = b[q];
     }
+  } else if constexpr (VEC == 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[q] = v[q];
   } else {
     static_assert(VEC == 1, "16-byte pieces or single elements");
     f[0] = *p;
@@ -50,6 +61,8 @@ __device__ __forceinline__ void store_row(bf16_t *p, const float (&f)[VEC]) {
   if constexpr (VEC == 8) {
     *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
                                           pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
   } else {
     p->v = f32_to_bf16(f[0]);
   }
@@ -60,6 +73,8 @@ __device__ __forceinline__ void store_row(float *p, const float (&f)[VEC]) {
   if constexpr (VEC == 8) {
     *reinterpret_cast<f32x4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
     *reinterpret_cast<f32x4 *>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<f32x4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
   } else {
     *p = f[0];
   }

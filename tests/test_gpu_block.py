@@ -178,6 +178,9 @@ def test_unpermute_ignores_places_outside_the_rows():
     rows = torch.arange(6 * 16, device=DEV, dtype=torch.float32).view(6, 16)
     y = e4b.moe_unpermute(perm, rows)
     assert torch.equal(y, torch.stack([rows[0], rows[2], rows[1]]))
+    # offsets beyond the rows do not make more of them
+    far = e4b.Permutation(torch.tensor([0, 2, 2 ** 31 - 1], dtype=torch.int32, device=DEV), perm.sorted_pair, pos)
+    assert torch.equal(e4b.moe_unpermute(far, rows), torch.stack([rows[0], rows[2], rows[3] + rows[1]]))
     gr, gw = e4b.moe_unpermute_backward(perm, rows, torch.ones(3, 16, device=DEV))
     assert torch.equal(gw != 0, torch.tensor([[True, False], [True, False], [False, True]], device=DEV))
     assert not gr[3].any() and gr[:3].eq(1).all()
