@@ -238,10 +238,14 @@ def expert_linear_dgrad_workspace_bytes(stack, rows, recompute=False):
 
 
 def _linear_workspace(ws, need, device):
+    """(the buffer to keep alive, its address, its bytes); a call that needs none gets none"""
     if ws is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    _need_buffer(ws, "workspace", need, device)
-    return ws
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _need_buffer(ws, "workspace", need, device)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, out_dtype=torch.bfloat16, save=False,
@@ -272,9 +276,9 @@ def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, 
     pre = torch.empty(rows, stack.out, dtype=torch.float32, device=dev) if save else None
     c = stack.as_c()
     st = ctypes.byref(c)
-    ws = _linear_workspace(workspace, int(load().e4b_expert_linear_workspace_bytes(st, rows)), dev)
+    ws, at, nbytes = _linear_workspace(workspace, int(load().e4b_expert_linear_workspace_bytes(st, rows)), dev)
     _run("e4b_expert_linear", dev, st, rows, _vp(offsets), x.data_ptr(), _vp(bias), ACTS[act], _vp(residual),
-         _DTYPES[out_dtype], y.data_ptr(), _vp(pre), ws.data_ptr(), ws.numel() * ws.element_size())
+         _DTYPES[out_dtype], y.data_ptr(), _vp(pre), at, nbytes)
     return y, pre
 
 
@@ -305,11 +309,10 @@ def expert_linear_dgrad(stack, grad_y, x=None, offsets=None, bias=None, act="non
     c = stack.as_c()
     st = ctypes.byref(c)
     need = int(load().e4b_expert_linear_dgrad_workspace_bytes(st, rows, int(recompute)))
-    ws = _linear_workspace(workspace, need, dev)
+    ws, at, nbytes = _linear_workspace(workspace, need, dev)
     _run("e4b_expert_linear_dgrad", dev, st, rows, _vp(offsets), grad_y.data_ptr(), code,
          None if act == "none" else _vp(pre), x.data_ptr() if recompute else None,
-         _vp(bias) if recompute else None, ACTS[act], gx.data_ptr(), _vp(gb), ws.data_ptr(),
-         ws.numel() * ws.element_size())
+         _vp(bias) if recompute else None, ACTS[act], gx.data_ptr(), _vp(gb), at, nbytes)
     return gx, gb
 
 

@@ -178,6 +178,9 @@ __device__ __forceinline__ void load_piece(const LinearArgs &g, int64_t e, int64
 
 // NN = false: C[row, n] = sum_k A[row, k] W[n, k] with the epilogue;
 // NN = true:  C[row, n] = sum_k A[row, k] W[k, n], stored as bf16.
+// A product of few tiles is cut along k as well: with g.part, workgroup (tile, s)
+// adds up its share of the K-steps and leaves fp32 sums in part[s], which
+// linear_join_kernel adds in order.
 template <int SK, bool NN>
 __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g) {
   __shared__ __attribute__((aligned(64))) float code[SK == LK_CODE8 ? 256 : 16];
@@ -216,8 +219,8 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   const int b_n = nt * kTN + (tid >> 1);
   const int64_t b_row = b_n < N ? b_n : 0;
   const int b_c = nt * kTN + (tid & 3) * 32 < N ? nt * kTN + (tid & 3) * 32 : 0;
-  const int K = NN ? (g.out + kBK - 1) / kBK * kBK : g.in;
-  const int nK = K / kBK;
+  const int all = NN ? (g.out + kBK - 1) / kBK : g.in / kBK;  // K-steps, and this workgroup's
+  const int first = all * int(blockIdx.y) / int(gridDim.y), nK = all * int(blockIdx.y + 1) / int(gridDim.y);
 
   u32x4 ra[4];
   Piece<SK> rb;
@@ -263,12 +266,12 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  load(0);
+  load(first);
   __syncthreads();  // the code table
-  store(0);
-  if (nK > 1) load(1);
+  store(first & 1);
+  if (first + 1 < nK) load(first + 1);
   __syncthreads();
-  for (int ks = 0; ks < nK; ++ks) {
+  for (int ks = first; ks < nK; ++ks) {
     const uint16_t *sA = lds + (ks & 1) * kStageA, *sB = lds + 2 * kStageA + (ks & 1) * kStageB;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
@@ -314,6 +317,22 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
                                    4 * (lane >> 5)) = f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
       }
   __syncthreads();
+  if (g.part) {
+    float *out = g.part + int64_t(blockIdx.y) * g.rows * N;
+    const int cc = (tid & 31) * 4, col = nt * kTN + cc;
+    for (int r = tid >> 5; r < valid; r += 8) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(tile + r * kTOut + cc);
+      float *o = out + (row0 + r) * N + col;
+      if (N % 4 == 0) {
+        if (col < N) *reinterpret_cast<f32x4 *>(o) = v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (col + q < N) o[q] = v[q];
+      }
+    }
+    return;
+  }
   if (NN) {
     const int cc = (tid & 15) * 8, col = nt * kTN + cc;
     if (col < N)  // N is a multiple of 64
@@ -343,6 +362,38 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
     rows_of(std::integral_constant<int, 8>{});
   else
     rows_of(std::integral_constant<int, 1>{});
+}
+
+// The sums of a product's splits, in order, and its epilogue. One workgroup per
+// row tile and 32 VEC columns.
+template <bool NN, int VEC>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int splits) {
+  if (int(blockIdx.x) >= g.tile_offsets[g.E]) return;
+  const int4 tm = g.tile_map[blockIdx.x];
+  const int64_t row0 = int64_t(tm.y) + tm.z, N = NN ? g.in : g.out;
+  const int64_t col = int64_t(blockIdx.y) * 32 * VEC + (threadIdx.x & 31) * VEC;
+  if (col >= N) return;
+  float b[VEC];
+#pragma unroll
+  for (int q = 0; q < VEC; ++q) b[q] = 0.0f;
+  if (!NN && g.bias) load_row<VEC>(g.bias + int64_t(tm.x) * N + col, b);
+  for (int r = threadIdx.x >> 5; r < tm.w; r += 8) {
+    const int64_t at = (row0 + r) * N + col;
+    float v[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) v[q] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      float u[VEC];
+      load_row<VEC>(g.part + int64_t(s) * g.rows * N + at, u);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) v[q] += u[q];
+    }
+    if constexpr (NN)
+      store_row<VEC>(static_cast<bf16_t *>(g.y) + at, v);
+    else
+      linear_epilogue<VEC>(g, at, b, v);
+  }
 }
 
 // ---- few rows to an expert ----
@@ -588,15 +639,25 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *p, int64_t n) {
 }
 
 template <bool NN>
-hipError_t launch_tiles(const LinearArgs &a, int64_t m_bound, hipStream_t s) {
-  const int64_t N = NN ? a.in : a.out, tiles = m_bound * ((N + kTN - 1) / kTN);
-  const dim3 grid(uint32_t((tiles + 7) / 8 * 8)), block(kTThreads);
+hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws, hipStream_t s) {
+  const int64_t N = NN ? a.in : a.out, tiles = p.m_bound * ((N + kTN - 1) / kTN);
+  const dim3 grid(uint32_t((tiles + 7) / 8 * 8), uint32_t(splits)), block(kTThreads);
+  a.rows = p.rows;
+  a.part = splits > 1 ? reinterpret_cast<float *>(ws + p.off_split) : nullptr;
   switch (a.cb) {
     case E4B_CB_BF16: hipLaunchKernelGGL((linear_tile_kernel<LK_BF16, NN>), grid, block, 0, s, a); break;
     case E4B_CB_MXFP4: hipLaunchKernelGGL((linear_tile_kernel<LK_MX, NN>), grid, block, 0, s, a); break;
     case E4B_CB_INT8:
     case E4B_CB_FP8: hipLaunchKernelGGL((linear_tile_kernel<LK_CODE8, NN>), grid, block, 0, s, a); break;
     default: hipLaunchKernelGGL((linear_tile_kernel<LK_ABSMAX, NN>), grid, block, 0, s, a); break;
+  }
+  if (splits > 1) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const bool vec = N % 8 == 0;
+    const int cols = vec ? 256 : 32;
+    hipLaunchKernelGGL((vec ? linear_join_kernel<NN, 8> : linear_join_kernel<NN, 1>),
+                       dim3(uint32_t(p.m_bound), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
   }
   return hipGetLastError();
 }
@@ -664,41 +725,9 @@ GemmArgs wide_args(const LinearPlan &p, const LinearArgs &a, bool nn) {
   return w;
 }
 
-// How a product's rows are tiled: by the kernel for few rows, or in 128- or
-// 256-row tiles (us on one MI355X, nf4 unless said; rows / 128 / 256):
-//   few rows to an expert (up to 8 on average): 64 experts of 2048 -> 2048, 4 rows
-//     each 48 / 97 / 117; 16 each 83 / 97 / 119; 32 each 108 / 97 / 123
-//   one expert, up to 2^20 outputs: 2048 -> 4096, 256 rows 22 / 38 / 55, 512 rows
-//     41 / 39 / 55; 4096 -> 14336, 64 rows 41 / 67 / 98, 128 rows 83 / 69 / 98; bf16
-//     weights (four times the bytes to read again for every 64 rows) up to 2^18:
-//     4096 -> 4096, 64 rows 40 / 48 / 81, 256 rows 82 / 50 / 82
-//   256-row tiles when the experts fill half of one each and the 128-row tiles are more
-//     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
-//     - / 43 / 57, 2048 rows - / 64 / 62 (with GELU and a residual, which two workgroups
-//     to a CU overlap, 66 / 74), 4096 rows - / 117 / 76; 64 experts of 2048 -> 2048, 96
-//     rows each 222 / 108 / 133, 128 each 263 / 154 / 138
-enum { TILE_ROWS = 0, TILE_128 = 128, TILE_256 = 256 };
-
-bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
-  // (the wide tiles address their rows in 32 bits)
-  const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
-  const int64_t tiles = (rows + 64 * (st->E - 1)) / kTM * ((cols + kTN - 1) / kTN);  // a ragged one for every other expert
-  return rows >= 128 * st->E && tiles > 512 && rows * longest < (int64_t(1) << 32);
-}
-
-int forward_tiles(const e4b_stack *st, int64_t rows) {
-  const int64_t few = st->codebook == E4B_CB_BF16 ? int64_t(1) << 18 : int64_t(1) << 20;
-  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out <= few) return TILE_ROWS;
-  return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
-}
-
-int dgrad_tiles(const e4b_stack *st, int64_t rows) {
-  return st->out % kBK == 0 && fills_wide_tiles(st, rows, st->in) ? TILE_256 : TILE_128;
-}
-
-hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, int tiles, hipStream_t s) {
-  if (tiles == TILE_ROWS) return launch_rows(p, a, offsets, s);
-  if (tiles == TILE_128) return launch_tiles<false>(a, p.m_bound, s);
+hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, char *ws, hipStream_t s) {
+  if (p.fwd_tiles == TILE_ROWS) return launch_rows(p, a, offsets, s);
+  if (p.fwd_tiles == TILE_128) return launch_tiles<false>(a, p, p.fwd_splits, ws, s);
   return launch_grouped_gemm(GEMM_LINEAR, wide_args(p, a, false), s);
 }
 
@@ -765,12 +794,13 @@ extern "C" e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const
   if (s != E4B_OK) return s;
   if (!offsets && st->E != 1) return E4B_ERR_NULL;
   if (rows == 0) return E4B_OK;
-  if (!x_bf16 || !y || !ws) return E4B_ERR_NULL;
+  if (!x_bf16 || !y || (p.fwd_bytes && !ws)) return E4B_ERR_NULL;
   if (ws_bytes < p.fwd_bytes) return E4B_ERR_WORKSPACE;
   if (!aligned16(offsets) || !aligned16(x_bf16) || !aligned16(bias) || !aligned16(residual_bf16) || !aligned16(y) ||
       !aligned16(pre) || !aligned16(ws))
     return E4B_ERR_ALIGN;
-  LinearArgs a = args_of(p, st, static_cast<char *>(ws));
+  char *w = static_cast<char *>(ws);
+  LinearArgs a = args_of(p, st, w);
   a.A = static_cast<const uint16_t *>(x_bf16);
   a.lda = st->in;
   a.bias = bias;
@@ -779,10 +809,9 @@ extern "C" e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const
   a.y = y;
   a.y_f32 = y_dtype == E4B_F32;
   a.pre = pre;
-  const int tiles = forward_tiles(st, rows);
-  if (tiles != TILE_ROWS)
-    E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
-  E4B_TRY(launch_forward(p, a, offsets, tiles, stream));
+  if (p.fwd_tiles != TILE_ROWS)
+    E4B_TRY(launch_map(p, a, offsets, p.fwd_tiles, p.m_bound, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
+  E4B_TRY(launch_forward(p, a, offsets, w, stream));
   return E4B_OK;
 }
 
@@ -811,7 +840,7 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   char *w = static_cast<char *>(ws);
   LinearArgs a = args_of(p, st, w);
   a.act = act;
-  const int tiles = dgrad_tiles(st, rows), again = recompute ? forward_tiles(st, rows) : tiles;
+  const int tiles = p.bwd_tiles, again = recompute ? p.fwd_tiles : tiles;
   // the recomputed forward takes the forward's tiles, for the same bits
   if (recompute && again != TILE_ROWS && again != tiles)
     E4B_TRY(launch_map(p, a, offsets, again, p.m_bound, nullptr, 0, nullptr, 0, stream));
@@ -824,7 +853,7 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
     f.lda = st->in;
     f.bias = bias;
     f.pre = reinterpret_cast<float *>(w + p.off_pre);
-    E4B_TRY(launch_forward(p, f, offsets, again, stream));
+    E4B_TRY(launch_forward(p, f, offsets, w, stream));
     if (again != TILE_ROWS && again != tiles)
       E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
     pre = f.pre;
@@ -853,6 +882,6 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   if (tiles == TILE_256)
     E4B_TRY(launch_grouped_gemm(GEMM_GATE_UP_DGRAD, wide_args(p, a, true), stream));
   else
-    E4B_TRY(launch_tiles<true>(a, p.m_bound, stream));
+    E4B_TRY(launch_tiles<true>(a, p, p.bwd_splits, w, stream));
   return E4B_OK;
 }

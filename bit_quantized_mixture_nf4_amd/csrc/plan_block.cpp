@@ -51,6 +51,48 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   return E4B_OK;
 }
 
+// How a product's rows are tiled: by the kernel for few rows, or in 128- or
+// 256-row tiles (us on one MI355X, nf4 unless said; rows / 128 / 256):
+//   few rows to an expert (up to 8 on average): 64 experts of 2048 -> 2048, 4 rows
+//     each 48 / 97 / 117; 16 each 83 / 97 / 119; 32 each 108 / 97 / 123
+//   one expert, up to 2^20 outputs: 2048 -> 4096, 256 rows 22 / 38 / 55, 512 rows
+//     41 / 39 / 55; 4096 -> 14336, 64 rows 41 / 67 / 98, 128 rows 83 / 69 / 98; bf16
+//     weights (four times the bytes to read again for every 64 rows) up to 2^18:
+//     4096 -> 4096, 64 rows 40 / 48 / 81, 256 rows 82 / 50 / 82
+//   256-row tiles when the experts fill half of one each and the 128-row tiles are more
+//     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
+//     - / 43 / 57, 2048 rows - / 64 / 62 (with GELU and a residual, which two workgroups
+//     to a CU overlap, 66 / 74), 4096 rows - / 117 / 76; 64 experts of 2048 -> 2048, 96
+//     rows each 222 / 108 / 133, 128 each 263 / 154 / 138
+static bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
+  // (the wide tiles address their rows in 32 bits)
+  const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
+  const int64_t tiles = (rows + 64 * (st->E - 1)) / kLinearM * ((cols + 127) / 128);  // a ragged one for every other expert
+  return rows >= 128 * st->E && tiles > 512 && rows * longest < (int64_t(1) << 32);
+}
+
+static int forward_tiles(const e4b_stack *st, int64_t rows) {
+  const int64_t few = st->codebook == E4B_CB_BF16 ? int64_t(1) << 18 : int64_t(1) << 20;
+  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out <= few) return TILE_ROWS;
+  return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
+}
+
+static int dgrad_tiles(const e4b_stack *st, int64_t rows) {
+  return st->out % kBK == 0 && fills_wide_tiles(st, rows, st->in) ? TILE_256 : TILE_128;
+}
+
+// Workgroups along k, where 128-row tiles leave most of the chip idle: 512 in all
+// (two per CU), with at least four K-steps each.
+static int k_splits(const e4b_stack *st, int64_t rows, int64_t cols, int64_t k) {
+  const int64_t busy = st->E < rows ? st->E : rows;
+  const int64_t tiles = ((rows + 64 * (busy - 1)) / kLinearM + 1) * ((cols + 127) / 128), steps = (k + kBK - 1) / kBK;
+  if (tiles > 128) return 1;
+  int64_t s = 512 / tiles;
+  if (s > steps / 4) s = steps / 4;
+  if (s > 16) s = 16;
+  return int(s > 1 ? s : 1);
+}
+
 e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t dtype, LinearPlan *p) {
   *p = LinearPlan{};
   const e4b_status s = check_stack(st);
@@ -71,9 +113,19 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
     off = (off + bytes + 255) / 256 * 256;
     return o;
   };
+  p->fwd_tiles = forward_tiles(st, rows);
+  p->bwd_tiles = dgrad_tiles(st, rows);
+  p->fwd_splits = p->fwd_tiles == TILE_128 ? k_splits(st, rows, st->out, st->in) : 1;
+  p->bwd_splits = p->bwd_tiles == TILE_128 ? k_splits(st, rows, st->in, st->out) : 1;
   p->off_tile_offsets = take(size_t(st->E + 1) * 4);
   p->off_tile_map = take(size_t(p->m_bound) * 16);
-  p->fwd_bytes = off;
+  p->off_split = off;
+  const size_t fwd_split = p->fwd_splits > 1 ? size_t(p->fwd_splits) * size_t(rows) * size_t(st->out) * 4 : 0;
+  const size_t bwd_split = p->bwd_splits > 1 ? size_t(p->bwd_splits) * size_t(rows) * size_t(st->in) * 4 : 0;
+  // (the kernel for few rows reads the offsets itself)
+  p->fwd_bytes = p->fwd_tiles == TILE_ROWS || rows == 0 ? 0 : (off + fwd_split + 255) / 256 * 256;
+  // a recomputed forward is done with its sums before the gradient's begin
+  take(bwd_split > fwd_split ? bwd_split : fwd_split);
   p->off_part = take(size_t(p->m_bound) * size_t(st->out) * 4);
   p->off_dz = take(size_t(rows) * size_t(p->ldz) * 2);
   p->bwd_bytes = off;

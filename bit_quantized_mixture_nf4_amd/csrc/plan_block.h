@@ -50,7 +50,11 @@ inline size_t norm_ws_bytes(const NormArgs &a) { return size_t(a.groups) * size_
 
 // ---- stored-weight products (linear.hip) ----
 constexpr int kLinearM = 128;  // rows per tile
+enum { TILE_ROWS = 0, TILE_128 = 128, TILE_256 = 256 };  // how a product's rows are tiled
 struct LinearPlan {
+  int fwd_tiles, bwd_tiles;    // of the product, and of its gradient
+  int fwd_splits, bwd_splits;  // 128-row tiles: workgroups along k
+  size_t off_split;            // their fp32 sums
   int64_t rows, m_bound;  // m_bound: row tiles of kLinearM rows, at most
   int64_t ldz;            // row length of dz: out in whole K-steps
   size_t off_tile_offsets, off_tile_map, off_dz, off_part, off_pre;
@@ -69,6 +73,8 @@ struct LinearArgs {
   void *y;                   // [rows, out] bf16 / fp32; dgrad: grad_x [rows, in] bf16
   float *pre;                // [rows, out] or null
   int32_t act, y_f32;
+  int64_t rows;
+  float *part;  // [splits, rows, out] (dgrad: in) or null
 };
 e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t dtype, LinearPlan *p);
 

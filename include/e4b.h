@@ -428,7 +428,7 @@ e4b_status e4b_moe_perm_layout(const e4b_moe_layer *L, int64_t T, int32_t top_k,
  * over them). A logit may be -inf (an expert out of service for that token):
  * it gets weight 0 when it has to fill a slot, and a row that is -inf
  * throughout selects experts 0 .. top_k - 1 with weights 0. NaN and +inf are
- * not checked: such a row's ids and weights are meaningless.
+ * not checked: such a row's weights are meaningless, its ids are valid.
  *   logits   : device fp32 [T, E]
  *   topk_idx : device int32 [T, top_k]  (written)
  *   topk_w   : device fp32  [T, top_k]  (written)
@@ -509,7 +509,8 @@ typedef enum {
  *   residual : device bf16 [rows, out] or NULL
  *   y        : device [rows, out], bf16 or fp32 (y_dtype)  (written)
  *   pre      : device fp32 [rows, out] or NULL: z, for the gradient  (written)
- *   ws       : device workspace of e4b_expert_linear_workspace_bytes()
+ *   ws       : device workspace of e4b_expert_linear_workspace_bytes() (0 for few
+ *              rows, or for invalid arguments: then ws may be NULL)
  * Errors: NULL, SHAPE, BLOCKSIZE, CODEBOOK, ACT, DTYPE, WORKSPACE, ALIGN, HIP. */
 e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const int32_t *offsets,
                              const void *x_bf16, const float *bias, int32_t act,

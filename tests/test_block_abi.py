@@ -110,8 +110,9 @@ def test_linear_arguments(call):
     assert call(act=5) == L.E4B_ERR_ACT and call(act=-1) == L.E4B_ERR_ACT
     assert call(dt=2) == L.E4B_ERR_DTYPE
     assert call(st=_stack(E=4)) == L.E4B_ERR_NULL  # several experts need offsets
-    assert call(ws=None) == L.E4B_ERR_NULL
-    assert call(ws_bytes=16) == L.E4B_ERR_WORKSPACE
+    # (rows and columns enough for tiles)
+    assert call(st=_stack(out=4096), rows=4096, ws=None) == L.E4B_ERR_NULL
+    assert call(st=_stack(out=4096), rows=4096, ws_bytes=16) == L.E4B_ERR_WORKSPACE
 
 
 def test_linear_pointers():
@@ -131,15 +132,19 @@ def test_linear_pointers():
 
 def test_linear_workspace_sizes():
     lib = e4b.load()
-    st = _stack(E=4, out=128, inn=64)
-    fwd = lib.e4b_expert_linear_workspace_bytes(ctypes.byref(st), 300)
-    bwd = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), 300, 0)
-    rec = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), 300, 1)
+    st, rows = _stack(E=4, out=4096, inn=64), 3000
+    fwd = lib.e4b_expert_linear_workspace_bytes(ctypes.byref(st), rows)
+    bwd = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), rows, 0)
+    rec = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), rows, 1)
     assert 0 < fwd < bwd < rec
-    assert rec >= bwd + 300 * 128 * 4
-    assert _linear(st=st, rows=300, off=FAKE, ws_bytes=fwd - 1) == L.E4B_ERR_WORKSPACE
-    assert _linear_bwd(st=st, rows=300, off=FAKE, ws_bytes=bwd - 1) == L.E4B_ERR_WORKSPACE
-    assert _linear_bwd(st=st, rows=300, off=FAKE, act=2, pre=None, ws_bytes=rec - 1) == L.E4B_ERR_WORKSPACE
+    assert rec >= bwd + rows * 4096 * 4
+    assert _linear(st=st, rows=rows, off=FAKE, ws_bytes=fwd - 1) == L.E4B_ERR_WORKSPACE
+    assert _linear(st=st, rows=rows, off=FAKE, ws=None) == L.E4B_ERR_NULL
+    assert _linear_bwd(st=st, rows=rows, off=FAKE, ws_bytes=bwd - 1) == L.E4B_ERR_WORKSPACE
+    assert _linear_bwd(st=st, rows=rows, off=FAKE, act=2, pre=None, ws_bytes=rec - 1) == L.E4B_ERR_WORKSPACE
+    # few rows read the offsets themselves
+    assert lib.e4b_expert_linear_workspace_bytes(ctypes.byref(st), 8) == 0
+    assert lib.e4b_expert_linear_workspace_bytes(ctypes.byref(st), 0) == 0
     bad = _stack(inn=100)
     assert lib.e4b_expert_linear_workspace_bytes(ctypes.byref(bad), 300) == 0
     assert lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(bad), 300, 1) == 0

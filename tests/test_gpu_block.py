@@ -79,6 +79,20 @@ def test_route_and_its_gradient(T, E, k, masked):
     within(gl, ref, mag * (k + 4) * U, "grad_logits")
 
 
+def test_route_of_unusable_logits_keeps_valid_ids():
+    lg = torch.randn(6, 70, device=DEV)
+    lg[0] = float("nan")
+    lg[1, ::2] = -float("nan")
+    lg[2, 5] = float("inf")
+    lg[3] = float("inf")
+    lg.view(torch.int32)[4] = -1  # the NaN of all ones
+    idx, _ = e4b.moe_route(lg, 32)
+    idx = idx.cpu().numpy()
+    assert idx.min() >= 0 and idx.max() < 70
+    for t in (0, 1, 2, 3, 5):
+        assert len(set(idx[t])) == 32
+
+
 def test_route_equals_the_routed_forward():
     """The routing that the expert MLP makes from the same logits, bit for bit."""
     from gpu_util import Problem
@@ -224,6 +238,23 @@ LINEARS = [
     ("mxfp4", 9, 40, 0, 2112, 300, "silu", True, False, "bf16"),
     ("bf16", 2, 1500, 0, 256, 776, "silu", True, True, "bf16"),
     ("int8", 8, 48, 0, 1024, 256, "none", False, False, "fp32"),
+    # 128-row tiles, cut along k and not
+    ("nf4", 1, 700, 0, 1024, 2048, "gelu", True, True, "bf16"),
+    ("fp4", 1, 600, 3, 1088, 2049, "silu", True, False, "fp32"),
+    ("bf16", 3, 500, 9, 1024, 1000, "relu", True, True, "bf16"),
+    ("mxfp4", 2, 1030, 0, 512, 1100, "gelu_tanh", False, False, "bf16"),
+    ("int8", 1, 1300, 0, 320, 1024, "none", True, False, "bf16"),
+    ("nf4", 5, 3000, 2, 64, 1100, "silu", True, False, "bf16"),
+    ("fp8", 1, 3001, 0, 128, 1001, "none", True, True, "fp32"),
+    # 256-row tiles, forward and gradient
+    ("nf4", 2, 2500, 7, 128, 4096, "silu", True, True, "bf16"),
+    ("bf16", 1, 2049, 0, 64, 4360, "gelu", True, False, "fp32"),
+    ("fp8", 3, 2600, 0, 128, 3968, "none", False, True, "bf16"),
+    ("mxfp4", 2, 2300, 1, 192, 4224, "relu", True, False, "bf16"),
+    ("nf4", 2, 2500, 5, 4096, 128, "none", True, False, "bf16"),
+    ("int8", 1, 2200, 0, 4224, 192, "gelu_tanh", True, False, "bf16"),
+    ("mxfp4", 3, 2600, 0, 3968, 64, "none", False, False, "fp32"),
+    ("bf16", 2, 2304, 0, 4096, 128, "silu", True, False, "bf16"),
 ]
 
 
@@ -443,7 +474,7 @@ def test_refusals_on_the_device():
         lambda: e4b.expert_linear(stack, x, offsets=ids.view(-1)[:3], act="tanh"),
         lambda: e4b.expert_linear(stack, x, offsets=ids.view(-1)[:3], bias=ones),
         lambda: e4b.expert_linear(stack, x, offsets=ids.view(-1)[:3], out_dtype=torch.float16),
-        lambda: e4b.expert_linear(stack, x, offsets=ids.view(-1)[:3], workspace=torch.empty(8, device=DEV)),
+        lambda: e4b.expert_linear_dgrad(stack, x, offsets=ids.view(-1)[:3], workspace=torch.empty(8, device=DEV)),
         lambda: e4b.expert_linear_dgrad(stack, x, offsets=ids.view(-1)[:3], act="silu"),
         lambda: e4b.block_norm(x),
         lambda: e4b.block_norm(x, w_post=ones),
