@@ -122,30 +122,40 @@ struct Piece {
   float s;
 };
 
+// 8 of them, as packed bf16
 template <int SK>
-__device__ __forceinline__ void decode_piece(const Piece<SK> &p, const float *code, u32x4 (&o)[4]) {
+__device__ __forceinline__ u32x4 decode_quarter(const Piece<SK> &p, const float *code, int q) {
   if constexpr (SK == LK_BF16) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = p.v[q];
+    return p.v[q];
   } else if constexpr (SK == LK_CODE8) {
+    u32x4 o;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const uint32_t w = p.v[q >> 3][(q >> 1) & 3] >> (16 * (q & 1));
-      o[q >> 2][q & 3] = pack_bf16x2(__fmul_rn(code[w & 255], p.s), __fmul_rn(code[(w >> 8) & 255], p.s));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = p.v[q >> 1][(2 * q + (i >> 1)) & 3] >> (16 * (i & 1));
+      o[i] = pack_bf16x2(__fmul_rn(code[w & 255], p.s), __fmul_rn(code[(w >> 8) & 255], p.s));
     }
+    return o;
   } else {
     // the byte offsets 4 code of a word's high (even) and low (odd) nibbles, a byte each;
     // one byte permute then makes an address
     const char *tbl = reinterpret_cast<const char *>(code);
+    const uint32_t w = p.v[0][q], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
+    u32x4 o;
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const uint32_t w = p.v[0][q >> 2], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
-      const uint32_t sel = 0x0C0C0C00u | uint32_t(q & 3);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t sel = 0x0C0C0C00u | uint32_t(i);
       const float a = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
       const float b = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
-      o[q >> 2][q & 3] = pack_bf16x2(__fmul_rn(a, p.s), __fmul_rn(b, p.s));
+      o[i] = pack_bf16x2(__fmul_rn(a, p.s), __fmul_rn(b, p.s));
     }
+    return o;
   }
+}
+
+template <int SK>
+__device__ __forceinline__ void decode_piece(const Piece<SK> &p, const float *code, u32x4 (&o)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = decode_quarter<SK>(p, code, q);
 }
 
 template <int SK>
@@ -232,20 +242,15 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
     else  // weight rows past the last meet zeros of A
       load_piece<SK>(g, e, min(ks * kBK + (tid >> 2), g.out - 1), b_c, rb);
   };
-  auto store = [&](int st) {
+  // quarter q of what the thread puts into a stage
+  auto store = [&](int st, int q) {
     uint16_t *sA = lds + st * kStageA, *sB = lds + 2 * kStageA + st * kStageB;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<u32x4 *>(sA + ((tid >> 3) + 32 * i) * kLds + (tid & 7) * 8) = ra[i];
-    u32x4 o[4];
-    decode_piece<SK>(rb, code, o);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (!NN)
-        *reinterpret_cast<u32x4 *>(sB + (tid >> 1) * kLds + (tid & 1) * 32 + q * 8) = o[q];
-      else
-        *reinterpret_cast<u32x4 *>(sB + (tid >> 2) * kTBn + nn_unit(4 * (tid & 3) + q) * 8) = o[q];
-    }
+    *reinterpret_cast<u32x4 *>(sA + ((tid >> 3) + 32 * q) * kLds + (tid & 7) * 8) = ra[q];
+    const u32x4 o = decode_quarter<SK>(rb, code, q);
+    if (!NN)
+      *reinterpret_cast<u32x4 *>(sB + (tid >> 1) * kLds + (tid & 1) * 32 + q * 8) = o;
+    else
+      *reinterpret_cast<u32x4 *>(sB + (tid >> 2) * kTBn + nn_unit(4 * (tid & 3) + q) * 8) = o;
   };
   // transpose-read addresses of the [k][n] tile (see gemm_wide.hip)
   int q_off[2];
@@ -268,7 +273,8 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 
   load(first);
   __syncthreads();  // the code table
-  store(first & 1);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) store(first & 1, q);
   if (first + 1 < nK) load(first + 1);
   __syncthreads();
   for (int ks = first; ks < nK; ++ks) {
@@ -294,11 +300,10 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
+      // a quarter of the next stage under the MFMAs
+      if (ks + 1 < nK) store((ks + 1) & 1, kk);
     }
-    if (ks + 1 < nK) {
-      store((ks + 1) & 1);
-      if (ks + 2 < nK) load(ks + 2);
-    }
+    if (ks + 2 < nK) load(ks + 2);
     __syncthreads();
   }
 
@@ -365,35 +370,32 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 }
 
 // The sums of a product's splits, in order, and its epilogue. One workgroup per
-// row tile and 32 VEC columns.
+// 8 rows of a row tile and 32 VEC columns.
 template <bool NN, int VEC>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int splits) {
-  if (int(blockIdx.x) >= g.tile_offsets[g.E]) return;
-  const int4 tm = g.tile_map[blockIdx.x];
+  constexpr int kGroups = kTM / 8;
+  if (int(blockIdx.x / kGroups) >= g.tile_offsets[g.E]) return;
+  const int4 tm = g.tile_map[blockIdx.x / kGroups];
   const int64_t row0 = int64_t(tm.y) + tm.z, N = NN ? g.in : g.out;
+  const int r = blockIdx.x % kGroups * 8 + (threadIdx.x >> 5);
   const int64_t col = int64_t(blockIdx.y) * 32 * VEC + (threadIdx.x & 31) * VEC;
-  if (col >= N) return;
-  float b[VEC];
+  if (col >= N || r >= tm.w) return;
+  const int64_t at = (row0 + r) * N + col;
+  float b[VEC], v[VEC];
 #pragma unroll
-  for (int q = 0; q < VEC; ++q) b[q] = 0.0f;
+  for (int q = 0; q < VEC; ++q) b[q] = v[q] = 0.0f;
   if (!NN && g.bias) load_row<VEC>(g.bias + int64_t(tm.x) * N + col, b);
-  for (int r = threadIdx.x >> 5; r < tm.w; r += 8) {
-    const int64_t at = (row0 + r) * N + col;
-    float v[VEC];
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    float u[VEC];
+    load_row<VEC>(g.part + int64_t(s) * g.rows * N + at, u);
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) v[q] = 0.0f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      float u[VEC];
-      load_row<VEC>(g.part + int64_t(s) * g.rows * N + at, u);
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) v[q] += u[q];
-    }
-    if constexpr (NN)
-      store_row<VEC>(static_cast<bf16_t *>(g.y) + at, v);
-    else
-      linear_epilogue<VEC>(g, at, b, v);
+    for (int q = 0; q < VEC; ++q) v[q] += u[q];
   }
+  if constexpr (NN)
+    store_row<VEC>(static_cast<bf16_t *>(g.y) + at, v);
+  else
+    linear_epilogue<VEC>(g, at, b, v);
 }
 
 // ---- few rows to an expert ----
@@ -657,7 +659,7 @@ hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws,
     const bool vec = N % 8 == 0;
     const int cols = vec ? 256 : 32;
     hipLaunchKernelGGL((vec ? linear_join_kernel<NN, 8> : linear_join_kernel<NN, 1>),
-                       dim3(uint32_t(p.m_bound), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
+                       dim3(uint32_t(p.m_bound * (kTM / 8)), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
   }
   return hipGetLastError();
 }

@@ -51,14 +51,17 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   return E4B_OK;
 }
 
-// How a product's rows are tiled: by the kernel for few rows, or in 128- or
-// 256-row tiles (us on one MI355X, nf4 unless said; rows / 128 / 256):
-//   few rows to an expert (up to 8 on average): 64 experts of 2048 -> 2048, 4 rows
-//     each 48 / 97 / 117; 16 each 83 / 97 / 119; 32 each 108 / 97 / 123
-//   one expert, up to 2^20 outputs: 2048 -> 4096, 256 rows 22 / 38 / 55, 512 rows
-//     41 / 39 / 55; 4096 -> 14336, 64 rows 41 / 67 / 98, 128 rows 83 / 69 / 98; bf16
-//     weights (four times the bytes to read again for every 64 rows) up to 2^18:
-//     4096 -> 4096, 64 rows 40 / 48 / 81, 256 rows 82 / 50 / 82
+// How a product's rows are tiled: by the kernel for few rows, in 128-row tiles
+// (cut along k where they are few) or in 256-row tiles. In us on one MI355X, nf4
+// unless said, as few rows / 128 / 256:
+//   few rows to an expert, up to 8 on average: 64 experts of 2048 -> 2048, 4 rows each
+//     47 / 94 / 117, 8 each 48 / 94 / 117, 24 each 78 / 97 / 119; beyond 8 a skewed
+//     routing gives one expert too many rows for a kernel that reads its weights again
+//     for every 16
+//   one expert, up to 2^31 products: 2048 -> 4096, 256 rows 22 / 27 / 55, 384 rows
+//     34 / 33 / 55; 4096 -> 4096, 64 rows 27 / 24 / 95, 128 rows 28 / 29 / 95; 8- and
+//     16-bit weights, which are two and four times the bytes to read again, up to 2^29:
+//     bf16 4096 -> 4096, 16 rows 14 / 18 / 78, 64 rows 40 / 21 / 81
 //   256-row tiles when the experts fill half of one each and the 128-row tiles are more
 //     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
 //     - / 43 / 57, 2048 rows - / 64 / 62 (with GELU and a residual, which two workgroups
@@ -72,8 +75,8 @@ static bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
 }
 
 static int forward_tiles(const e4b_stack *st, int64_t rows) {
-  const int64_t few = st->codebook == E4B_CB_BF16 ? int64_t(1) << 18 : int64_t(1) << 20;
-  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out <= few) return TILE_ROWS;
+  const bool four = st->codebook == E4B_CB_NF4 || st->codebook == E4B_CB_FP4 || st->codebook == E4B_CB_MXFP4;
+  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out * st->in <= int64_t(1) << (four ? 31 : 29)) return TILE_ROWS;
   return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
 }
 
@@ -82,11 +85,13 @@ static int dgrad_tiles(const e4b_stack *st, int64_t rows) {
 }
 
 // Workgroups along k, where 128-row tiles leave most of the chip idle: 512 in all
-// (two per CU), with at least four K-steps each.
+// (two per CU), with at least four K-steps each. 4096 -> 4096, 64 rows: 24 us with
+// 16 of them, 65 without; 384 rows: 40 with 5, 66 without.
 static int k_splits(const e4b_stack *st, int64_t rows, int64_t cols, int64_t k) {
   const int64_t busy = st->E < rows ? st->E : rows;
-  const int64_t tiles = ((rows + 64 * (busy - 1)) / kLinearM + 1) * ((cols + 127) / 128), steps = (k + kBK - 1) / kBK;
-  if (tiles > 128) return 1;
+  const int64_t tiles = (rows + 64 * (busy - 1) + kLinearM - 1) / kLinearM * ((cols + 127) / 128);
+  const int64_t steps = (k + kBK - 1) / kBK;
+  if (tiles == 0 || tiles > 128) return 1;
   int64_t s = 512 / tiles;
   if (s > steps / 4) s = steps / 4;
   if (s > 16) s = 16;
