@@ -3,10 +3,14 @@
 
 namespace e4b {
 
+// Tokens of one call: a launch dimension has less than 2^32 threads, and the kernels
+// that give a token a workgroup give it 256 (the norms up to 512).
+constexpr int64_t kMaxTokens = (int64_t(1) << 24) - 1, kMaxNormRows = (int64_t(1) << 23) - 1;
+
 e4b_status plan_order(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype, OrderArgs *a) {
   if (T < 0 || top_k < 1 || top_k > kMaxTopK || E < 1 || E > kMaxE || H < 1 || H >= (int64_t(1) << 24))
     return E4B_ERR_SHAPE;
-  if (T >= (int64_t(1) << 29) || T * top_k >= (int64_t(1) << 29)) return E4B_ERR_SHAPE;
+  if (T > kMaxTokens) return E4B_ERR_SHAPE;
   if (dtype != E4B_F32 && dtype != E4B_BF16) return E4B_ERR_DTYPE;
   a->T = T;
   a->k = top_k;
@@ -18,7 +22,7 @@ e4b_status plan_order(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dt
 
 e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   if (!n) return E4B_ERR_NULL;
-  if (n->T < 0 || n->H < 1 || n->H > kNormMaxH || n->T >= (int64_t(1) << 31)) return E4B_ERR_SHAPE;
+  if (n->T < 0 || n->H < 1 || n->H > kNormMaxH || n->T > kMaxNormRows) return E4B_ERR_SHAPE;
   if (n->dtype != E4B_F32 && n->dtype != E4B_BF16) return E4B_ERR_DTYPE;
   // a mean square of zero has to have an inverse; the comparison also refuses NaN
   if (!(n->eps > 0.0f)) return E4B_ERR_SHAPE;
@@ -109,9 +113,9 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
   // every expert may end in a partial tile
   p->m_bound = rows / kLinearM + (st->E < rows ? st->E : rows);
   p->ldz = (st->out + kBK - 1) / kBK * kBK;
-  // the launch grids: one workgroup per tile, and column slabs in grid.y
+  // the launch grids: 256 threads per tile, and column slabs in grid.y
   const int64_t wide = st->out > st->in ? st->out : st->in;
-  if (p->m_bound * (wide / 128 + 1) >= (int64_t(1) << 30) || st->out > (int64_t(1) << 20)) return E4B_ERR_SHAPE;
+  if (wide > (int64_t(1) << 20) || p->m_bound * (wide / 128 + 1) >= (int64_t(1) << 24) - 8) return E4B_ERR_SHAPE;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -141,7 +145,7 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
 
 e4b_status check_route(int64_t T, int64_t E, int32_t top_k) {
   if (T < 0 || E < 1 || E > kMaxE || top_k < 1 || top_k > kMaxTopK || top_k > E) return E4B_ERR_SHAPE;
-  if (T >= (int64_t(1) << 29) || T * top_k >= (int64_t(1) << 29)) return E4B_ERR_SHAPE;
+  if (T > kMaxTokens) return E4B_ERR_SHAPE;
   return E4B_OK;
 }
 

@@ -20,7 +20,7 @@ struct OrderArgs {
   const int32_t *ids;  // the order's input and outputs
   int32_t *out_offsets, *out_sorted, *out_pos;
 };
-// T >= 0, 1 <= top_k <= 32, 1 <= E <= 1024, 1 <= H < 2^24, T top_k < 2^29.
+// 0 <= T < 2^24, 1 <= top_k <= 32, 1 <= E <= 1024, 1 <= H < 2^24.
 e4b_status plan_order(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype, OrderArgs *a);
 
 // ---- block norms (norm.hip) ----

@@ -432,8 +432,8 @@ e4b_status e4b_moe_perm_layout(const e4b_moe_layer *L, int64_t T, int32_t top_k,
  *   logits   : device fp32 [T, E]
  *   topk_idx : device int32 [T, top_k]  (written)
  *   topk_w   : device fp32  [T, top_k]  (written)
- * Errors: NULL, SHAPE (E outside [1, 1024], top_k outside [1, min(E, 32)], T < 0
- * or too large), ALIGN, HIP. */
+ * Errors: NULL, SHAPE (E outside [1, 1024], top_k outside [1, min(E, 32)], T outside
+ * [0, 2^24)), ALIGN, HIP. */
 e4b_status e4b_route(const float *logits, int64_t T, int64_t E, int32_t top_k, int32_t *topk_idx,
                      float *topk_w, hipStream_t stream);
 
@@ -460,7 +460,7 @@ e4b_status e4b_route_backward(const int32_t *topk_idx, const float *topk_w, cons
  *   sorted_pair : device int32 [T top_k]    (written: pair at each place)
  *   pos_of_pair : device int32 [T, top_k]   (written: place of each pair)
  * T = 0 writes offsets only. Errors: NULL, SHAPE (E outside [1, 1024], H outside
- * [1, 2^24), T top_k >= 2^29), DTYPE, ALIGN, HIP. */
+ * [1, 2^24), T outside [0, 2^24)), DTYPE, ALIGN, HIP. */
 e4b_status e4b_permute(int64_t T, int32_t top_k, int64_t E, int64_t H, int32_t dtype,
                        const int32_t *topk_idx, const void *x, void *rows, int32_t *offsets,
                        int32_t *sorted_pair, int32_t *pos_of_pair, hipStream_t stream);
@@ -500,7 +500,8 @@ typedef enum {
  * with W the bf16 view of the stack (any storage mode) and fp32 accumulation.
  * E = 1 with offsets NULL is a dense projection of every row. Rows from
  * offsets[E] on belong to no expert: y and pre are zeros there.
- *   st       : any out >= 1; in % 64 == 0; E <= 1024
+ *   st       : any out >= 1; in % 64 == 0; both at most 2^20; E <= 1024
+ *   rows     : 0 to 2^30, and fewer than 2^24 tiles of 128 x 128 (rows, columns)
  *   offsets  : device int32 [E + 1], ascending from 0 (as e4b_permute writes them), or
  *              NULL for E = 1. Values are not checked on the host; the kernels
  *              clamp them, so that no list leads out of a buffer.
@@ -546,7 +547,7 @@ size_t e4b_expert_linear_dgrad_workspace_bytes(const e4b_stack *st, int64_t rows
  * gate g is one value per token, per channel, or 1. */
 typedef enum { E4B_GATE_NONE = 0, E4B_GATE_TOKEN = 1, E4B_GATE_CHANNEL = 2 } e4b_gate;
 typedef struct {
-  int64_t T, H;       /* rows, and their length in [1, 16384] */
+  int64_t T, H;       /* rows (fewer than 2^23), and their length in [1, 16384] */
   int32_t dtype;      /* of x, r and their gradients: E4B_BF16 or E4B_F32 */
   int32_t gate_kind;  /* e4b_gate */
   float eps, scale;   /* eps > 0 */

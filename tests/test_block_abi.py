@@ -28,7 +28,7 @@ def _route_bwd(T=4, E=8, k=2, idx=FAKE, w=FAKE, gw=FAKE, gl=FAKE):
 
 
 @pytest.mark.parametrize("kw", [dict(E=0), dict(E=1025), dict(k=0), dict(k=9), dict(k=33, E=64), dict(T=-1),
-                                dict(T=1 << 30)])
+                                dict(T=1 << 24)])
 def test_route_shapes(kw):
     assert _route(**kw) == L.E4B_ERR_SHAPE
     assert _route_bwd(**kw) == L.E4B_ERR_SHAPE
@@ -60,7 +60,7 @@ def _unpermute_bwd(T=4, k=2, E=8, H=64, dt=1, off=FAKE, pos=FAKE, w=FAKE, rows=F
 @pytest.mark.parametrize("call", [_permute, _unpermute, _unpermute_bwd])
 def test_order_shapes_and_types(call):
     for kw in (dict(k=0), dict(k=33), dict(E=0), dict(E=1025), dict(H=0), dict(H=1 << 24), dict(T=-1),
-               dict(T=1 << 28, k=2)):
+               dict(T=1 << 24)):
         assert call(**kw) == L.E4B_ERR_SHAPE, kw
     assert call(dt=2) == L.E4B_ERR_DTYPE
     assert call(dt=-1) == L.E4B_ERR_DTYPE
@@ -107,12 +107,15 @@ def test_linear_arguments(call):
     assert call(st=_stack(cb=3, bs=32)) == L.E4B_ERR_NULL  # MXFP4 needs its scales
     assert call(rows=-1) == L.E4B_ERR_SHAPE
     assert call(rows=(1 << 30) + 1) == L.E4B_ERR_SHAPE
+    assert call(st=_stack(out=1 << 21)) == L.E4B_ERR_SHAPE
+    assert call(st=_stack(inn=1 << 21)) == L.E4B_ERR_SHAPE
+    assert call(st=_stack(out=1 << 16), rows=1 << 22) == L.E4B_ERR_SHAPE  # more tiles than a launch has
     assert call(act=5) == L.E4B_ERR_ACT and call(act=-1) == L.E4B_ERR_ACT
     assert call(dt=2) == L.E4B_ERR_DTYPE
     assert call(st=_stack(E=4)) == L.E4B_ERR_NULL  # several experts need offsets
     # (rows and columns enough for tiles)
-    assert call(st=_stack(out=4096), rows=4096, ws=None) == L.E4B_ERR_NULL
-    assert call(st=_stack(out=4096), rows=4096, ws_bytes=16) == L.E4B_ERR_WORKSPACE
+    assert call(st=_stack(out=4096), rows=16384, ws=None) == L.E4B_ERR_NULL
+    assert call(st=_stack(out=4096), rows=16384, ws_bytes=16) == L.E4B_ERR_WORKSPACE
 
 
 def test_linear_pointers():
@@ -132,7 +135,7 @@ def test_linear_pointers():
 
 def test_linear_workspace_sizes():
     lib = e4b.load()
-    st, rows = _stack(E=4, out=4096, inn=64), 3000
+    st, rows = _stack(E=4, out=4096, inn=64), 16384
     fwd = lib.e4b_expert_linear_workspace_bytes(ctypes.byref(st), rows)
     bwd = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), rows, 0)
     rec = lib.e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(st), rows, 1)
@@ -168,7 +171,7 @@ def _norm_bwd(n=None, x=FAKE, y=FAKE, ry=FAKE, rr=FAKE, gr=FAKE, gh=FAKE, gx=FAK
 
 @pytest.mark.parametrize("call", [_norm, _norm_bwd])
 def test_norm_descriptor(call):
-    for kw in (dict(T=-1), dict(H=0), dict(H=16385), dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan),
+    for kw in (dict(T=-1), dict(T=1 << 23), dict(H=0), dict(H=16385), dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan),
                dict(kind=3, gate=FAKE), dict(kind=-1, gate=FAKE)):
         assert call(**kw) == L.E4B_ERR_SHAPE, kw
     assert call(dt=2) == L.E4B_ERR_DTYPE

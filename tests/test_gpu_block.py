@@ -246,6 +246,12 @@ LINEARS = [
     ("int8", 1, 1300, 0, 320, 1024, "none", True, False, "bf16"),
     ("nf4", 5, 3000, 2, 64, 1100, "silu", True, False, "bf16"),
     ("fp8", 1, 3001, 0, 128, 1001, "none", True, True, "fp32"),
+    ("nf4", 1, 700, 0, 2048, 2048, "gelu", True, True, "bf16"),
+    ("fp4", 1, 650, 3, 2112, 2049, "silu", True, False, "fp32"),
+    ("mxfp4", 2, 1500, 0, 1024, 1500, "gelu_tanh", False, False, "bf16"),
+    ("bf16", 3, 500, 9, 1024, 1100, "relu", True, True, "bf16"),
+    ("int8", 1, 1300, 0, 448, 1024, "none", True, False, "bf16"),
+    ("fp8", 1, 3001, 0, 192, 1001, "none", True, True, "fp32"),
     # 256-row tiles, forward and gradient
     ("nf4", 2, 2500, 7, 128, 4096, "silu", True, True, "bf16"),
     ("bf16", 1, 2049, 0, 64, 4360, "gelu", True, False, "fp32"),
