@@ -57,6 +57,17 @@ def _rows(t, name, device=None, shape=None):
     return code
 
 
+def _workspace(ws, need, device):
+    """(the buffer to keep alive, its address, its bytes); a call that needs none gets none"""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _need_buffer(ws, "workspace", need, device)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 # ---- the router ----
 
 
@@ -237,17 +248,6 @@ def expert_linear_dgrad_workspace_bytes(stack, rows, recompute=False):
     return int(load().e4b_expert_linear_dgrad_workspace_bytes(ctypes.byref(c), rows, int(recompute)))
 
 
-def _linear_workspace(ws, need, device):
-    """(the buffer to keep alive, its address, its bytes); a call that needs none gets none"""
-    if ws is None:
-        if not need:
-            return None, None, 0
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _need_buffer(ws, "workspace", need, device)
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
-
-
 def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, out_dtype=torch.bfloat16, save=False,
                   workspace=None, out=None):
     """y = act(W[e] x + bias[e]) + residual for expert-sorted rows.
@@ -276,7 +276,7 @@ def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, 
     pre = torch.empty(rows, stack.out, dtype=torch.float32, device=dev) if save else None
     c = stack.as_c()
     st = ctypes.byref(c)
-    ws, at, nbytes = _linear_workspace(workspace, int(load().e4b_expert_linear_workspace_bytes(st, rows)), dev)
+    ws, at, nbytes = _workspace(workspace, int(load().e4b_expert_linear_workspace_bytes(st, rows)), dev)
     _run("e4b_expert_linear", dev, st, rows, _vp(offsets), x.data_ptr(), _vp(bias), ACTS[act], _vp(residual),
          _DTYPES[out_dtype], y.data_ptr(), _vp(pre), at, nbytes)
     return y, pre
@@ -309,7 +309,7 @@ def expert_linear_dgrad(stack, grad_y, x=None, offsets=None, bias=None, act="non
     c = stack.as_c()
     st = ctypes.byref(c)
     need = int(load().e4b_expert_linear_dgrad_workspace_bytes(st, rows, int(recompute)))
-    ws, at, nbytes = _linear_workspace(workspace, need, dev)
+    ws, at, nbytes = _workspace(workspace, need, dev)
     _run("e4b_expert_linear_dgrad", dev, st, rows, _vp(offsets), grad_y.data_ptr(), code,
          None if act == "none" else _vp(pre), x.data_ptr() if recompute else None,
          _vp(bias) if recompute else None, ACTS[act], gx.data_ptr(), _vp(gb), at, nbytes)
@@ -415,14 +415,14 @@ def block_norm_backward(fwd, x, grad_r=None, grad_h=None, y=None, w_post=None, g
     gg = torch.empty_like(gate) if gate is not None and (weight_grads or gate_token is not None) else None
     gpost = torch.empty_like(w_post) if w_post is not None and weight_grads else None
     gpre = torch.empty_like(w_pre) if w_pre is not None and weight_grads else None
-    need = int(load().e4b_block_norm_workspace_bytes(ctypes.byref(n)))
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    else:
-        _need_buffer(workspace, "workspace", need, dev)
+    # the column gradients' partial sums
+    need = 0
+    if gpost is not None or gpre is not None or (gg is not None and gate_channel is not None):
+        need = int(load().e4b_block_norm_workspace_bytes(ctypes.byref(n)))
+    ws, at, nbytes = _workspace(workspace, need, dev)
     _run("e4b_block_norm_backward", dev, ctypes.byref(n), x.data_ptr(), _vp(y), rstd_y, rstd_r,
          _vp(grad_r), _vp(grad_h) if w_pre is not None else None, gx.data_ptr(), _vp(gy), _vp(gg), _vp(gpost),
-         _vp(gpre), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+         _vp(gpre), at, nbytes)
     return BlockNormGrads(gx, gy, gg, gpost, gpre)
 
 

@@ -395,8 +395,9 @@ extern "C" e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, 
     return E4B_ERR_NULL;
   const bool g = a.gate_token || a.gate_channel;
   if ((grad_gate && !g) || (grad_w_post && !a.w_post) || (grad_w_pre && !a.w_pre)) return E4B_ERR_NULL;
-  if (a.T && !ws) return E4B_ERR_NULL;
-  if (a.T && ws_bytes < norm_ws_bytes(a)) return E4B_ERR_WORKSPACE;
+  const bool columns = grad_w_post || grad_w_pre || (grad_gate && a.gate_channel);  // what takes the workspace
+  if (a.T && columns && !ws) return E4B_ERR_NULL;
+  if (a.T && columns && ws_bytes < norm_ws_bytes(a)) return E4B_ERR_WORKSPACE;
   for (const void *p :
        {x, y, static_cast<const void *>(rstd_y), static_cast<const void *>(rstd_r), grad_r, grad_h,
         static_cast<const void *>(grad_x), static_cast<const void *>(grad_y), static_cast<const void *>(grad_gate),

@@ -196,6 +196,7 @@ def test_norm_pointers():
     assert _norm_bwd(pre=None, gpre=FAKE) == L.E4B_ERR_NULL
     assert _norm_bwd(post=None, gpost=FAKE) == L.E4B_ERR_NULL
     assert _norm_bwd(ws_bytes=8) == L.E4B_ERR_WORKSPACE
+    assert _norm_bwd(gpost=None, ws=None) == L.E4B_ERR_NULL  # one column gradient is enough to need it
     for name in ("x", "y", "ry", "rr", "gr", "gh", "gx", "gy", "gpost", "gpre", "ws"):
         assert _norm_bwd(**{name: FAKE + 4}) == L.E4B_ERR_ALIGN, name
     assert _norm(T=0, x=None, r=None, h=None, ry=None, rr=None) == L.E4B_OK
