@@ -354,7 +354,7 @@ hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   float *gate = a.gate_channel ? a.grad_gate : nullptr;
-  if (!a.grad_w_pre && !a.grad_w_post && !gate) return hipSuccess;
+  if ((!a.grad_w_pre && !a.grad_w_post && !gate) || (a.T && a.groups == 1)) return hipSuccess;
   hipLaunchKernelGGL(norm_cols_kernel, dim3(uint32_t((a.H + 63) / 64), 3), dim3(1024), 0, s, a.part_pre, a.part_post,
                      a.part_gate, a.grad_w_pre, a.grad_w_post, gate, a.T ? a.groups : 0, a.H);
   return hipGetLastError();
@@ -395,7 +395,8 @@ extern "C" e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, 
     return E4B_ERR_NULL;
   const bool g = a.gate_token || a.gate_channel;
   if ((grad_gate && !g) || (grad_w_post && !a.w_post) || (grad_w_pre && !a.w_pre)) return E4B_ERR_NULL;
-  const bool columns = grad_w_post || grad_w_pre || (grad_gate && a.gate_channel);  // what takes the workspace
+  // what takes the workspace
+  const bool columns = (grad_w_post || grad_w_pre || (grad_gate && a.gate_channel)) && norm_ws_bytes(a);
   if (a.T && columns && !ws) return E4B_ERR_NULL;
   if (a.T && columns && ws_bytes < norm_ws_bytes(a)) return E4B_ERR_WORKSPACE;
   for (const void *p :
@@ -414,11 +415,14 @@ extern "C" e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, 
   a.grad_gate = grad_gate;
   a.grad_w_post = grad_w_post;
   a.grad_w_pre = grad_w_pre;
+  // the partial rows in the workspace's (at most) three arrays, 16-byte aligned or not: they
+  // are read and written by single columns; one group's only row is the gradient itself
   float *w = static_cast<float *>(ws);
   const int64_t each = int64_t(a.groups) * a.H;
-  a.part_pre = grad_w_pre ? w : nullptr;
-  a.part_post = grad_w_post ? w + each : nullptr;
-  a.part_gate = grad_gate && a.gate_channel ? w + 2 * each : nullptr;
+  const bool one = a.groups == 1;
+  a.part_pre = grad_w_pre ? (one ? grad_w_pre : w) : nullptr;
+  a.part_post = grad_w_post ? (one ? grad_w_post : w + each) : nullptr;
+  a.part_gate = grad_gate && a.gate_channel ? (one ? grad_gate : w + 2 * each) : nullptr;
   return launch_norm_bwd(a, stream) == hipSuccess ? E4B_OK : E4B_ERR_HIP;
 }
 

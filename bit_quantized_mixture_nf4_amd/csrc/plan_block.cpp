@@ -52,6 +52,9 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   // to add the partial rows).
   const int64_t most = !a->f32 && !a->gate_channel && n->H <= 4096 ? 512 : 256;
   a->groups = int32_t(need < most ? (need ? need : 1) : most);
+  // A few rows are one workgroup's, which then writes the column gradients itself: a
+  // second launch costs more than its turns.
+  if (need <= 4) a->groups = 1;
   return E4B_OK;
 }
 

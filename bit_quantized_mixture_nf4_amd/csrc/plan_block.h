@@ -46,7 +46,9 @@ struct NormArgs {
 // column sums each).
 // (An empty batch has no y to show for its gate.)
 e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a);
-inline size_t norm_ws_bytes(const NormArgs &a) { return size_t(a.groups) * size_t(a.H) * 3 * sizeof(float) + 16; }
+inline size_t norm_ws_bytes(const NormArgs &a) {
+  return a.groups > 1 ? size_t(a.groups) * size_t(a.H) * 3 * sizeof(float) : 0;  // one group writes its sums in place
+}
 
 // ---- stored-weight products (linear.hip) ----
 constexpr int kLinearM = 128;  // rows per tile

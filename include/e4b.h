@@ -574,8 +574,9 @@ e4b_status e4b_block_norm(const e4b_norm *n, const void *x, const void *y, void 
  *   grad_y      : device bf16 [T, H]      (written, with y)
  *   grad_gate   : device fp32, as gate    (written) or NULL
  *   grad_w_post, grad_w_pre : device fp32 [H] (written) or NULL
- *   ws          : e4b_block_norm_workspace_bytes(); NULL is enough without the
- *                 gradients of w_post, w_pre and a channel gate
+ *   ws          : e4b_block_norm_workspace_bytes() (0 for a few rows, or for invalid
+ *                 arguments); NULL is enough for 0, and without the gradients of
+ *                 w_post, w_pre and a channel gate
  * T = 0 writes the column gradients (zeros). Errors: as e4b_block_norm, plus
  * WORKSPACE, and NULL for a gradient of something not given. */
 e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, const void *y,

@@ -189,14 +189,20 @@ def test_norm_pointers():
         assert _norm(**{name: None}) == L.E4B_ERR_NULL, name
     for name in ("x", "y", "r", "h", "ry", "rr"):
         assert _norm(**{name: FAKE + 4}) == L.E4B_ERR_ALIGN, name
-    for name in ("x", "ry", "rr", "gh", "gx", "gy", "ws"):
+    for name in ("x", "ry", "rr", "gh", "gx", "gy"):
         assert _norm_bwd(**{name: None}) == L.E4B_ERR_NULL, name
+    # column gradients over more than a few rows take the workspace
+    assert _norm_bwd(T=100, ws=None) == L.E4B_ERR_NULL
+    n = _norm_desc(T=100)
+    need = e4b.load().e4b_block_norm_workspace_bytes(ctypes.byref(n))
+    assert need > 0 and _norm_bwd(n=n, ws_bytes=need - 1) == L.E4B_ERR_WORKSPACE
+    n = _norm_desc(T=4)
+    assert e4b.load().e4b_block_norm_workspace_bytes(ctypes.byref(n)) == 0
     assert _norm_bwd(gr=None, pre=None, gpre=None) == L.E4B_ERR_NULL  # then nothing reaches r
     assert _norm_bwd(gg=FAKE) == L.E4B_ERR_NULL  # the gradient of a gate that is not there
     assert _norm_bwd(pre=None, gpre=FAKE) == L.E4B_ERR_NULL
     assert _norm_bwd(post=None, gpost=FAKE) == L.E4B_ERR_NULL
-    assert _norm_bwd(ws_bytes=8) == L.E4B_ERR_WORKSPACE
-    assert _norm_bwd(gpost=None, ws=None) == L.E4B_ERR_NULL  # one column gradient is enough to need it
+    assert _norm_bwd(T=100, gpost=None, ws=None) == L.E4B_ERR_NULL  # one column gradient is enough to need it
     for name in ("x", "y", "ry", "rr", "gr", "gh", "gx", "gy", "gpost", "gpre", "ws"):
         assert _norm_bwd(**{name: FAKE + 4}) == L.E4B_ERR_ALIGN, name
     assert _norm(T=0, x=None, r=None, h=None, ry=None, rr=None) == L.E4B_OK
