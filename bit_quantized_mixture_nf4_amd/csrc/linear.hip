@@ -100,6 +100,16 @@ __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__
   }
 }
 
+// The tiles of a call: the map's, or without offsets simply the rows in turn
+// (no map is made then: its launch took 4.7 us of a 2048 x 2048 -> 4096 product's 61).
+__device__ __forceinline__ int tile_count(const LinearArgs &g) {
+  return g.tile_map ? g.tile_offsets[g.E] : int((g.rows + kLinearM - 1) / kLinearM);
+}
+__device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t) {
+  if (g.tile_map) return g.tile_map[t];
+  return int4{0, 0, t * kLinearM, int(min(int64_t(kLinearM), g.rows - int64_t(t) * kLinearM))};
+}
+
 // ---- the tiled product ----
 
 // 128 rows x 128 columns x 64: 4 waves of 64 x 64 (2 x 2 MFMA 32x32x16 bf16),
@@ -202,7 +212,7 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 
   // real tiles split evenly over the 8 XCDs (block b runs on XCD b % 8), in
   // groups of 8 row tiles so that an XCD's L2 sees both operands again
-  const int n_mt = g.tile_offsets[g.E];
+  const int n_mt = tile_count(g);
   const int N = NN ? g.in : g.out;
   const uint32_t n_nt = uint32_t((N + kTN - 1) / kTN), W = uint32_t(n_mt) * n_nt;
   const uint32_t per = (W + 7) / 8, xi = blockIdx.x / 8;
@@ -212,7 +222,7 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   const uint32_t grp = L / (kGroup * n_nt), rem = L % (kGroup * n_nt), m0 = grp * kGroup;
   const uint32_t gm = min(kGroup, uint32_t(n_mt) - m0);
   const int nt = int(rem / gm);
-  const int4 tm = g.tile_map[m0 + rem % gm];
+  const int4 tm = tile_of(g, int(m0 + rem % gm));
   const int64_t e = tm.x, row0 = int64_t(tm.y) + tm.z;
   const int valid = tm.w;
 
@@ -374,8 +384,8 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 template <bool NN, int VEC>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int splits) {
   constexpr int kGroups = kTM / 8;
-  if (int(blockIdx.x / kGroups) >= g.tile_offsets[g.E]) return;
-  const int4 tm = g.tile_map[blockIdx.x / kGroups];
+  if (int(blockIdx.x / kGroups) >= tile_count(g)) return;
+  const int4 tm = tile_of(g, blockIdx.x / kGroups);
   const int64_t row0 = int64_t(tm.y) + tm.z, N = NN ? g.in : g.out;
   const int r = blockIdx.x % kGroups * 8 + (threadIdx.x >> 5);
   const int64_t col = int64_t(blockIdx.y) * 32 * VEC + (threadIdx.x & 31) * VEC;
@@ -586,8 +596,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs g, const G *_
                                                         const float *__restrict__ pre, uint16_t *__restrict__ dz,
                                                         int ldz, float *__restrict__ part) {
   __shared__ float red[8][32 * VEC];
-  if (int(blockIdx.x) >= g.tile_offsets[g.E]) return;
-  const int4 tm = g.tile_map[blockIdx.x];
+  if (int(blockIdx.x) >= tile_count(g)) return;
+  const int4 tm = tile_of(g, blockIdx.x);
   const int64_t row0 = int64_t(tm.y) + tm.z;
   const int cl = (threadIdx.x & 31) * VEC, col = blockIdx.y * 32 * VEC + cl, rl = threadIdx.x >> 5;
   float sum[VEC];
@@ -629,7 +639,7 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs g, const fl
                                                           float *__restrict__ gb) {
   const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
   if (c >= g.out) return;
-  const int t0 = g.tile_offsets[e], t1 = g.tile_offsets[e + 1];
+  const int t0 = g.tile_map ? g.tile_offsets[e] : 0, t1 = g.tile_map ? g.tile_offsets[e + 1] : tile_count(g);
   float v = 0.0f;
 #pragma unroll 8
   for (int t = t0; t < t1; ++t) v += part[int64_t(t) * g.out + c];
@@ -644,7 +654,6 @@ template <bool NN>
 hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws, hipStream_t s) {
   const int64_t N = NN ? a.in : a.out, tiles = p.m_bound * ((N + kTN - 1) / kTN);
   const dim3 grid(uint32_t((tiles + 7) / 8 * 8), uint32_t(splits)), block(kTThreads);
-  a.rows = p.rows;
   a.part = splits > 1 ? reinterpret_cast<float *>(ws + p.off_split) : nullptr;
   switch (a.cb) {
     case E4B_CB_BF16: hipLaunchKernelGGL((linear_tile_kernel<LK_BF16, NN>), grid, block, 0, s, a); break;
@@ -733,8 +742,12 @@ hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_
   return launch_grouped_gemm(GEMM_LINEAR, wide_args(p, a, false), s);
 }
 
-hipError_t launch_map(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, int bm, int64_t bound,
-                      void *zero_a, int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
+// Makes the map for tiles of bm rows where they need one, in `a`'s place for it.
+hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, const int32_t *offsets, int bm, void *zero_a,
+                      int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
+  const int64_t bound = p.m_bound;
+  a.tile_map = offsets || bm != kLinearM ? place : nullptr;
+  if (!a.tile_map) return hipSuccess;
   // without offsets every row belongs to an expert: nothing to clear
   const uint32_t grid = offsets && (zero_a || zero_b) ? 1 + kZeroBlocks : 1;
   hipLaunchKernelGGL(tile_map_kernel, dim3(grid), dim3(kMapThreads), 0, s, offsets, int(a.E), int32_t(p.rows), bm,
@@ -763,7 +776,7 @@ LinearArgs args_of(const LinearPlan &p, const e4b_stack *st, char *ws) {
   a.in = int32_t(st->in);
   a.cb = st->codebook;
   a.tile_offsets = reinterpret_cast<const int32_t *>(ws + p.off_tile_offsets);
-  a.tile_map = reinterpret_cast<const int4 *>(ws + p.off_tile_map);
+  a.rows = p.rows;
   return a;
 }
 
@@ -812,7 +825,8 @@ extern "C" e4b_status e4b_expert_linear(const e4b_stack *st, int64_t rows, const
   a.y_f32 = y_dtype == E4B_F32;
   a.pre = pre;
   if (p.fwd_tiles != TILE_ROWS)
-    E4B_TRY(launch_map(p, a, offsets, p.fwd_tiles, p.m_bound, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
+    E4B_TRY(launch_map(p, a, reinterpret_cast<const int4 *>(w + p.off_tile_map), offsets, p.fwd_tiles, y,
+                       st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4, stream));
   E4B_TRY(launch_forward(p, a, offsets, w, stream));
   return E4B_OK;
 }
@@ -842,24 +856,20 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   char *w = static_cast<char *>(ws);
   LinearArgs a = args_of(p, st, w);
   a.act = act;
-  const int tiles = p.bwd_tiles, again = recompute ? p.fwd_tiles : tiles;
-  // the recomputed forward takes the forward's tiles, for the same bits
-  if (recompute && again != TILE_ROWS && again != tiles)
-    E4B_TRY(launch_map(p, a, offsets, again, p.m_bound, nullptr, 0, nullptr, 0, stream));
-  if (!recompute || again == TILE_ROWS || again == tiles)
-    E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
+  const int tiles = p.bwd_tiles;
+  const int4 *place = reinterpret_cast<const int4 *>(w + p.off_tile_map);
   if (recompute) {
-    // exactly the forward's pre-activation
+    // exactly the forward's pre-activation, in the forward's tiles
     LinearArgs f = a;
     f.A = static_cast<const uint16_t *>(x_bf16);
     f.lda = st->in;
     f.bias = bias;
     f.pre = reinterpret_cast<float *>(w + p.off_pre);
+    if (p.fwd_tiles != TILE_ROWS) E4B_TRY(launch_map(p, f, place, offsets, p.fwd_tiles, nullptr, 0, nullptr, 0, stream));
     E4B_TRY(launch_forward(p, f, offsets, w, stream));
-    if (again != TILE_ROWS && again != tiles)
-      E4B_TRY(launch_map(p, a, offsets, tiles, p.m_bound, grad_x_bf16, st->in * 2, nullptr, 0, stream));
     pre = f.pre;
   }
+  E4B_TRY(launch_map(p, a, place, offsets, tiles, grad_x_bf16, st->in * 2, nullptr, 0, stream));
   const bool f32 = gy_dtype == E4B_F32;
   // grad_y itself is the operand when it is dz already, in whole K-steps
   const bool direct = act == E4B_ACT_NONE && !f32 && st->out == p.ldz;
