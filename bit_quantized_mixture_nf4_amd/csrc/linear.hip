@@ -15,6 +15,7 @@
 // host never waits for the counts; rows behind the last expert's are zeros in
 // every output.
 #include <type_traits>
+#include <utility>
 
 #include "act.h"
 #include "codebook8.h"
@@ -114,9 +115,23 @@ __device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t) {
 
 // 128 rows x 128 columns x 64: 4 waves of 64 x 64 (2 x 2 MFMA 32x32x16 bf16),
 // the weight as the MFMA's A operand, so that a lane's accumulators are runs of
-// 4 columns of one row. While K-step ks runs from one LDS stage, the registers
-// hold K-step ks + 1, which goes to the other stage (weights decoded on the
-// way). 78 KB of LDS: two workgroups per CU cover each other's waits.
+// 4 columns of one row. 78 KB of LDS: two workgroups per CU.
+// While K-step ks runs from one LDS stage, the other is filled for ks + 1. The
+// wave's instruction stream is cut into 16 slots of one MFMA (32 cycles) and the
+// share of that work that fits under it, each closed by a scheduling barrier:
+//   slots 0..7   two pairs of codes looked up (their LDS latency passes under the
+//                next MFMA), slots 2..9 the pairs scaled and rounded, slots 4, 6, 8,
+//                10 a quarter of the piece stored;
+//   slots 7..10  the A rows stored, slots 8..11 those of ks + 2 asked for; slot 11
+//                the weights of ks + 3 (two register sets by parity);
+//   slots 0..11  the next k-slice's fragments, one per slot;
+//   after 11     every wave has filled its share and read its last fragment: the
+//                one barrier, and slots 12..15 read the next stage's first ones.
+// In phases instead (fragments, MFMAs, decode, store; MFMA, VALU and LDS each busy
+// 26 to 40 % of the time, in turn) nf4 2048 -> 4096 took 41 us for 1024 rows (one
+// workgroup per CU) and 58 for 2048 (two); in slots 33 and 53. With two workgroups
+// LDS bounds it: a K-step of one moves 64 KB of fragments, 32 KB of stores and 8192
+// table entries, 2050 or more of its 128-byte cycles per pair against 1024 of MFMA.
 constexpr int kTM = 128, kTN = 128;
 constexpr int kTThreads = 256;
 constexpr int kTBn = kTN + 32;  // row stride of the [k][n] weight tile (dgrad)
@@ -178,6 +193,16 @@ __device__ __forceinline__ void fill_codes(float *code, int cb) {
   } else if constexpr (SK != LK_BF16) {
     if (threadIdx.x < 16) code[threadIdx.x] = codebook_value(cb, threadIdx.x);
   }
+}
+
+// f(std::integral_constant<int, s>) for the 16 slots of a K-step
+template <typename F, int... I>
+__device__ __forceinline__ void slots_of(F &&f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <typename F>
+__device__ __forceinline__ void slots(F &&f) {
+  slots_of(f, std::make_integer_sequence<int, 16>{});
 }
 
 // bytes of n stored weights
@@ -242,25 +267,49 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   const int all = NN ? (g.out + kBK - 1) / kBK : g.in / kBK;  // K-steps, and this workgroup's
   const int first = all * int(blockIdx.y) / int(gridDim.y), nK = all * int(blockIdx.y + 1) / int(gridDim.y);
 
-  u32x4 ra[4];
-  Piece<SK> rb;
-  auto load = [&](int ks) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ra[i] = *reinterpret_cast<const u32x4 *>(a_src[i] + ks * kBK);
+  u32x4 ra[4];      // A rows of the next K-step
+  Piece<SK> rb[2];  // weights of the next two, by the K-step's parity
+  auto load_a = [&](int ks, int i) { ra[i] = *reinterpret_cast<const u32x4 *>(a_src[i] + ks * kBK); };
+  auto load_b = [&](int ks, Piece<SK> &p) {
     if (!NN)
-      load_piece<SK>(g, e, b_row, ks * kBK + (tid & 1) * 32, rb);
+      load_piece<SK>(g, e, b_row, ks * kBK + (tid & 1) * 32, p);
     else  // weight rows past the last meet zeros of A
-      load_piece<SK>(g, e, min(ks * kBK + (tid >> 2), g.out - 1), b_c, rb);
+      load_piece<SK>(g, e, min(ks * kBK + (tid >> 2), g.out - 1), b_c, p);
   };
-  // quarter q of what the thread puts into a stage
-  auto store = [&](int st, int q) {
-    uint16_t *sA = lds + st * kStageA, *sB = lds + 2 * kStageA + st * kStageB;
-    *reinterpret_cast<u32x4 *>(sA + ((tid >> 3) + 32 * q) * kLds + (tid & 7) * 8) = ra[q];
-    const u32x4 o = decode_quarter<SK>(rb, code, q);
+  auto store_a = [&](int st, int i) {
+    *reinterpret_cast<u32x4 *>(lds + st * kStageA + ((tid >> 3) + 32 * i) * kLds + (tid & 7) * 8) = ra[i];
+  };
+  auto store_b = [&](int st, int q, const u32x4 &o) {
+    uint16_t *sB = lds + 2 * kStageA + st * kStageB;
     if (!NN)
       *reinterpret_cast<u32x4 *>(sB + (tid >> 1) * kLds + (tid & 1) * 32 + q * 8) = o;
     else
       *reinterpret_cast<u32x4 *>(sB + (tid >> 2) * kTBn + nn_unit(4 * (tid & 3) + q) * 8) = o;
+  };
+  // pair c of the piece: two table entries, then their packed bf16
+  float cv[32];
+  uint32_t bq[16];
+  auto lookup = [&](const Piece<SK> &p, int c) {
+    if constexpr (SK == LK_CODE8) {
+      const uint32_t w = p.v[c >> 3][(c >> 1) & 3] >> (16 * (c & 1));
+      cv[2 * c] = code[w & 255];
+      cv[2 * c + 1] = code[(w >> 8) & 255];
+    } else if constexpr (SK != LK_BF16) {
+      const char *tbl = reinterpret_cast<const char *>(code);
+      const uint32_t w = p.v[0][c >> 2], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
+      const uint32_t sel = 0x0C0C0C00u | uint32_t(c & 3);
+      cv[2 * c] = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
+      cv[2 * c + 1] = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
+    }
+  };
+  auto scale = [&](const Piece<SK> &p, int c) {
+    if constexpr (SK != LK_BF16) bq[c] = pack_bf16x2(__fmul_rn(cv[2 * c], p.s), __fmul_rn(cv[2 * c + 1], p.s));
+  };
+  auto quarter = [&](const Piece<SK> &p, int q) {
+    if constexpr (SK == LK_BF16)
+      return p.v[q];
+    else
+      return u32x4{bq[4 * q], bq[4 * q + 1], bq[4 * q + 2], bq[4 * q + 3]};
   };
   // transpose-read addresses of the [k][n] tile (see gemm_wide.hip)
   int q_off[2];
@@ -280,42 +329,84 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  // fragment f of k-slice kk of stage st: 0, 1 the columns', 2, 3 the rows'
+  bf16x8 af[2][2], bf[2][2];
+  auto frag = [&](int st, int kk, int f) {
+    const uint16_t *sA = lds + st * kStageA, *sB = lds + 2 * kStageA + st * kStageB;
+    if (f >= 2) {
+      af[kk & 1][f - 2] = *reinterpret_cast<const bf16x8 *>(sA + (wm * 64 + (f - 2) * 32 + (lane & 31)) * kLds +
+                                                            (lane >> 5) * 8 + kk * 16);
+    } else if (!NN) {
+      bf[kk & 1][f] = *reinterpret_cast<const bf16x8 *>(sB + (wn * 64 + f * 32 + (lane & 31)) * kLds + (lane >> 5) * 8 +
+                                                        kk * 16);
+    } else {
+      const uint16_t *p = sB + q_off[f] + kk * 16 * kTBn;
+      const s16x4 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 4 * kTBn);
+      bf[kk & 1][f] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
 
-  load(first);
+  // the first stage; loads past the last K-step repeat it
+  const int last = nK - 1;
+  load_b(first, rb[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_a(first, i);
+  load_b(min(first + 1, last), rb[1]);
   __syncthreads();  // the code table
 #pragma unroll
-  for (int q = 0; q < 4; ++q) store(first & 1, q);
-  if (first + 1 < nK) load(first + 1);
-  __syncthreads();
-  for (int ks = first; ks < nK; ++ks) {
-    const uint16_t *sA = lds + (ks & 1) * kStageA, *sB = lds + 2 * kStageA + (ks & 1) * kStageB;
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      bf16x8 af[2], bf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        af[i] = *reinterpret_cast<const bf16x8 *>(sA + (wm * 64 + i * 32 + (lane & 31)) * kLds + (lane >> 5) * 8 + kk * 16);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (!NN) {
-          bf[j] = *reinterpret_cast<const bf16x8 *>(sB + (wn * 64 + j * 32 + (lane & 31)) * kLds + (lane >> 5) * 8 + kk * 16);
-        } else {
-          const uint16_t *p = sB + q_off[j] + kk * 16 * kTBn;
-          const s16x4 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 4 * kTBn);
-          bf[j] = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[j], af[i], acc[i][j], 0, 0, 0);
-      // a quarter of the next stage under the MFMAs
-      if (ks + 1 < nK) store((ks + 1) & 1, kk);
-    }
-    if (ks + 2 < nK) load(ks + 2);
-    __syncthreads();
+  for (int c = 0; c < 16; ++c) {
+    lookup(rb[0], c);
+    scale(rb[0], c);
   }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    store_a(0, q);
+    store_b(0, q, quarter(rb[0], q));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_a(min(first + 1, last), i);
+  load_b(min(first + 2, last), rb[0]);
+  __syncthreads();
+#pragma unroll
+  for (int f = 0; f < 4; ++f) frag(0, 0, f);
+
+  auto kstep = [&](auto cur_c, int ks) {
+    constexpr int CUR = decltype(cur_c)::value, NXT = CUR ^ 1;
+    const int ka = min(ks + 2, last), kb = min(ks + 3, last);
+    Piece<SK> &b = rb[NXT];  // the weights of ks + 1
+    slots([&](auto sc) {
+      constexpr int s = decltype(sc)::value, kk = s >> 2, w = s & 3;
+      acc[w >> 1][w & 1] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][w & 1], af[kk & 1][w >> 1], acc[w >> 1][w & 1], 0, 0, 0);
+      // in the order in which the next k-slice uses them
+      if constexpr (kk < 3) frag(CUR, kk + 1, w == 0 ? 0 : w == 1 ? 2 : w == 2 ? 1 : 3);
+      if constexpr (s < 8) {
+        lookup(b, 2 * s);
+        lookup(b, 2 * s + 1);
+      }
+      if constexpr (s >= 2 && s < 10) {
+        scale(b, 2 * (s - 2));
+        scale(b, 2 * (s - 2) + 1);
+      }
+      if constexpr (s == 4 || s == 6 || s == 8 || s == 10) store_b(NXT, (s - 4) / 2, quarter(b, (s - 4) / 2));
+      if constexpr (s >= 7 && s < 11) store_a(NXT, s - 7);
+      if constexpr (s >= 8 && s < 12) load_a(ka, s - 8);
+      if constexpr (s == 11) {
+        load_b(kb, b);
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+      }
+      if constexpr (s >= 12) frag(NXT, 0, w == 0 ? 0 : w == 1 ? 2 : w == 2 ? 1 : 3);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  int ks = first;
+  for (; ks + 1 < nK; ks += 2) {
+    kstep(std::integral_constant<int, 0>{}, ks);
+    kstep(std::integral_constant<int, 1>{}, ks + 1);
+  }
+  if (ks < nK) kstep(std::integral_constant<int, 0>{}, ks);
+  __syncthreads();  // the last stage's fragments are read
 
   // ---- epilogue: the fp32 tile goes through LDS, so that every global access
   // is a run of a row; acc[i][j][4 q + t] is row wm 64 + 32 i + lane % 32,

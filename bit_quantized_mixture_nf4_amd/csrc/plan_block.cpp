@@ -62,18 +62,18 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
 // (cut along k where they are few) or in 256-row tiles. In us on one MI355X, nf4
 // unless said, as few rows / 128 / 256:
 //   few rows to an expert, up to 8 on average: 64 experts of 2048 -> 2048, 4 rows each
-//     47 / 94 / 117, 8 each 48 / 94 / 117, 24 each 78 / 97 / 119; beyond 8 a skewed
+//     47 / 93 / 117, 8 each 48 / 93 / 117, 24 each 78 / 95 / 119; beyond 8 a skewed
 //     routing gives one expert too many rows for a kernel that reads its weights again
 //     for every 16
-//   one expert, up to 2^31 products: 2048 -> 4096, 256 rows 22 / 27 / 55, 384 rows
-//     34 / 33 / 55; 4096 -> 4096, 64 rows 27 / 24 / 95, 128 rows 28 / 29 / 95; 8- and
-//     16-bit weights, which are two and four times the bytes to read again, up to 2^29:
-//     bf16 4096 -> 4096, 16 rows 14 / 18 / 78, 64 rows 40 / 21 / 81
+//   up to 2^31 products: 2048 -> 4096, 256 rows 21 / 24 / 55, 384 rows 34 / 26 / 55;
+//     half of that for rows longer than the 2048 that it holds at once: 4096 -> 4096, 32
+//     rows 14 / 18 / 95, 64 rows 26 / 19 / 95; 8- and 16-bit weights, which are two and
+//     four times the bytes to read again, up to 2^29: bf16 4096 -> 4096, 16 rows
+//     13 / 15 / 78, 64 rows 40 / 21 / 81
 //   256-row tiles when the experts fill half of one each and the 128-row tiles are more
 //     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
-//     - / 43 / 57, 2048 rows - / 64 / 62 (with GELU and a residual, which two workgroups
-//     to a CU overlap, 66 / 74), 4096 rows - / 117 / 76; 64 experts of 2048 -> 2048, 96
-//     rows each 222 / 108 / 133, 128 each 263 / 154 / 138
+//     - / 33 / 57, 2048 rows - / 53 / 62, 4096 rows - / 97 / 77; 64 experts of
+//     2048 -> 2048, 96 rows each 222 / 101 / 133, 128 each 263 / 150 / 138
 static bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
   // (the wide tiles address their rows in 32 bits)
   const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
@@ -83,7 +83,8 @@ static bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
 
 static int forward_tiles(const e4b_stack *st, int64_t rows) {
   const bool four = st->codebook == E4B_CB_NF4 || st->codebook == E4B_CB_FP4 || st->codebook == E4B_CB_MXFP4;
-  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out * st->in <= int64_t(1) << (four ? 31 : 29)) return TILE_ROWS;
+  const int64_t most = four ? (st->in <= 2048 ? int64_t(1) << 31 : (int64_t(1) << 30) - 1) : int64_t(1) << 29;
+  if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out * st->in <= most) return TILE_ROWS;
   return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
 }
 
@@ -92,8 +93,8 @@ static int dgrad_tiles(const e4b_stack *st, int64_t rows) {
 }
 
 // Workgroups along k, where 128-row tiles leave most of the chip idle: 512 in all
-// (two per CU), with at least four K-steps each. 4096 -> 4096, 64 rows: 24 us with
-// 16 of them, 65 without; 384 rows: 40 with 5, 66 without.
+// (two per CU), with at least four K-steps each. nf4 4096 -> 4096, 64 rows: 19 us with
+// 16 of them, 60 without; 512 rows: 38 with 4, 57 without.
 static int k_splits(const e4b_stack *st, int64_t rows, int64_t cols, int64_t k) {
   const int64_t busy = st->E < rows ? st->E : rows;
   const int64_t tiles = (rows + 64 * (busy - 1) + kLinearM - 1) / kLinearM * ((cols + 127) / 128);
