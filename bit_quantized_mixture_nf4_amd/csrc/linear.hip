@@ -103,12 +103,12 @@ __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__
 
 // The tiles of a call: the map's, or without offsets simply the rows in turn
 // (no map is made then: its launch took 4.7 us of a 2048 x 2048 -> 4096 product's 61).
-__device__ __forceinline__ int tile_count(const LinearArgs &g) {
-  return g.tile_map ? g.tile_offsets[g.E] : int((g.rows + kLinearM - 1) / kLinearM);
+__device__ __forceinline__ int tile_count(const LinearArgs &g, int bm) {
+  return g.tile_map ? g.tile_offsets[g.E] : int((g.rows + bm - 1) / bm);
 }
-__device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t) {
+__device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t, int bm) {
   if (g.tile_map) return g.tile_map[t];
-  return int4{0, 0, t * kLinearM, int(min(int64_t(kLinearM), g.rows - int64_t(t) * kLinearM))};
+  return int4{0, 0, t * bm, int(min(int64_t(bm), g.rows - int64_t(t) * bm))};
 }
 
 // ---- the tiled product ----
@@ -119,9 +119,9 @@ __device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t) {
 // While K-step ks runs from one LDS stage, the other is filled for ks + 1. The
 // wave's instruction stream is cut into 16 slots of one MFMA (32 cycles) and the
 // share of that work that fits under it, each closed by a scheduling barrier:
-//   slots 0..7   two pairs of codes looked up (their LDS latency passes under the
-//                next MFMA), slots 2..9 the pairs scaled and rounded, slots 4, 6, 8,
-//                10 a quarter of the piece stored;
+//   slots 0..7   two pairs of codes (WM = 4: one) looked up (their LDS latency passes under the
+//                next MFMA), slots 2..9 the pairs scaled and rounded, eight
+//                weights stored one slot after their last (10 at the latest);
 //   slots 7..10  the A rows stored, slots 8..11 those of ks + 2 asked for; slot 11
 //                the weights of ks + 3 (two register sets by parity);
 //   slots 0..11  the next k-slice's fragments, one per slot;
@@ -132,55 +132,65 @@ __device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t) {
 // workgroup per CU) and 58 for 2048 (two); in slots 33 and 53. With two workgroups
 // LDS bounds it: a K-step of one moves 64 KB of fragments, 32 KB of stores and 8192
 // table entries, 2050 or more of its 128-byte cycles per pair against 1024 of MFMA.
-constexpr int kTM = 128, kTN = 128;
-constexpr int kTThreads = 256;
+// WM = 4 is the same wave tile in 256 rows x 128 columns, 8 waves, one workgroup per
+// CU: a weight is decoded, stored and looked up once for 256 rows instead of 128
+// (2048 rows of 2048 -> 4096 with GELU: 50 us, two 128 x 128 workgroups a CU 60).
+constexpr int kTN = 128;
 constexpr int kTBn = kTN + 32;  // row stride of the [k][n] weight tile (dgrad)
 constexpr int kTOut = kTN + 4;  // row stride of the epilogue's fp32 tile
-constexpr int kStageA = kTM * kLds, kStageB = kBK * kTBn;  // elements of a stage
+constexpr int kStageB = kBK * kTBn;  // elements of a stage
+template <int WM>
+struct Tile {
+  static constexpr int kM = 64 * WM, kThreads = 128 * WM, kW = 64 / WM;  // rows, threads, weights a thread
+  static constexpr int kStageA = kM * kLds;
+  static constexpr int kStages = 2 * (kStageA + kStageB), kOut = kM * kTOut * 2;  // elements of 2 bytes
+  static constexpr int kElems = kStages > kOut ? kStages : kOut;
+  static_assert(kTN * kLds <= kStageB, "either form of the weight tile fits its stage");
+};
 
-// How a weight reaches bf16: the 32 codes of one thread's piece.
+// How a weight reaches bf16: the W codes of one thread's piece, and their scale.
 enum { LK_ABSMAX = 0, LK_MX = 1, LK_BF16 = 2, LK_CODE8 = 3 };
 
-template <int SK>
+template <int SK, int W = 32>
 struct Piece {
-  u32x4 v[SK == LK_BF16 ? 4 : SK == LK_CODE8 ? 2 : 1];
+  static constexpr int kWords = SK == LK_BF16 ? W / 2 : SK == LK_CODE8 ? W / 4 : W / 8;
+  uint32_t w[kWords];
   float s;
 };
 
-// 8 of them, as packed bf16
-template <int SK>
-__device__ __forceinline__ u32x4 decode_quarter(const Piece<SK> &p, const float *code, int q) {
-  if constexpr (SK == LK_BF16) {
-    return p.v[q];
-  } else if constexpr (SK == LK_CODE8) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = p.v[q >> 1][(2 * q + (i >> 1)) & 3] >> (16 * (i & 1));
-      o[i] = pack_bf16x2(__fmul_rn(code[w & 255], p.s), __fmul_rn(code[(w >> 8) & 255], p.s));
-    }
-    return o;
+// table entries of pair c of a piece (not for bf16)
+template <int SK, int W>
+__device__ __forceinline__ void lookup_pair(const Piece<SK, W> &p, const float *code, int c, float &a, float &b) {
+  if constexpr (SK == LK_CODE8) {
+    const uint32_t w = p.w[c >> 1] >> (16 * (c & 1));
+    a = code[w & 255];
+    b = code[(w >> 8) & 255];
   } else {
     // the byte offsets 4 code of a word's high (even) and low (odd) nibbles, a byte each;
     // one byte permute then makes an address
     const char *tbl = reinterpret_cast<const char *>(code);
-    const uint32_t w = p.v[0][q], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t sel = 0x0C0C0C00u | uint32_t(i);
-      const float a = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
-      const float b = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
-      o[i] = pack_bf16x2(__fmul_rn(a, p.s), __fmul_rn(b, p.s));
-    }
-    return o;
+    const uint32_t w = p.w[c >> 2], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
+    const uint32_t sel = 0x0C0C0C00u | uint32_t(c & 3);
+    a = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
+    b = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
   }
 }
 
-template <int SK>
-__device__ __forceinline__ void decode_piece(const Piece<SK> &p, const float *code, u32x4 (&o)[4]) {
+// a piece as packed bf16, 8 weights to a vector
+template <int SK, int W>
+__device__ __forceinline__ void decode_piece(const Piece<SK, W> &p, const float *code, u32x4 (&o)[W / 8]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) o[q] = decode_quarter<SK>(p, code, q);
+  for (int q = 0; q < W / 8; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (SK == LK_BF16) {
+        o[q][i] = p.w[4 * q + i];
+      } else {
+        float a, b;
+        lookup_pair<SK, W>(p, code, 4 * q + i, a, b);
+        o[q][i] = pack_bf16x2(__fmul_rn(a, p.s), __fmul_rn(b, p.s));
+      }
+    }
 }
 
 template <int SK>
@@ -211,13 +221,24 @@ __device__ __forceinline__ int64_t code_bytes(int64_t n) {
   return SK == LK_BF16 ? n * 2 : SK == LK_CODE8 ? n : n / 2;
 }
 
-// the 32 consecutive weights from column c of stored row `row`
-template <int SK>
-__device__ __forceinline__ void load_piece(const LinearArgs &g, int64_t e, int64_t row, int c, Piece<SK> &p) {
+// the W consecutive weights from column c of stored row `row`
+template <int SK, int W>
+__device__ __forceinline__ void load_piece(const LinearArgs &g, int64_t e, int64_t row, int c, Piece<SK, W> &p) {
   const int64_t at = (e * g.out + row) * g.in + c;
-  const u32x4 *src = reinterpret_cast<const u32x4 *>(g.packed + code_bytes<SK>(at));
+  const uint8_t *src = g.packed + code_bytes<SK>(at);
+  constexpr int kN = Piece<SK, W>::kWords;
+  if constexpr (kN >= 4) {
 #pragma unroll
-  for (int q = 0; q < int(sizeof(p.v) / sizeof(p.v[0])); ++q) p.v[q] = src[q];
+    for (int q = 0; q < kN / 4; ++q) {
+      const u32x4 v = reinterpret_cast<const u32x4 *>(src)[q];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.w[4 * q + i] = v[i];
+    }
+  } else {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(src);
+    p.w[0] = v[0];
+    p.w[1] = v[1];
+  }
   p.s = SK == LK_MX ? e8m0_value(g.scales[at >> 5]) : SK == LK_BF16 ? 1.0f : g.absmax[at >> 6];
 }
 
@@ -226,91 +247,77 @@ __device__ __forceinline__ void load_piece(const LinearArgs &g, int64_t e, int64
 // A product of few tiles is cut along k as well: with g.part, workgroup (tile, s)
 // adds up its share of the K-steps and leaves fp32 sums in part[s], which
 // linear_join_kernel adds in order.
-template <int SK, bool NN>
-__global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g) {
+template <int SK, bool NN, int WM>
+__global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_tile_kernel(LinearArgs g) {
+  constexpr int kM = Tile<WM>::kM, kThreads = Tile<WM>::kThreads, kStageA = Tile<WM>::kStageA, kW = Tile<WM>::kW;
   __shared__ __attribute__((aligned(64))) float code[SK == LK_CODE8 ? 256 : 16];
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * (kStageA + kStageB)];
-  static_assert(kTN * kLds <= kStageB, "either form of the weight tile fits its stage");
-  static_assert(kTM * kTOut * 4 <= (kStageA + kStageB) * 4, "the epilogue's tile fits the stages");
+  __shared__ __attribute__((aligned(16))) uint16_t lds[Tile<WM>::kElems];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 
   // real tiles split evenly over the 8 XCDs (block b runs on XCD b % 8), in
-  // groups of 8 row tiles so that an XCD's L2 sees both operands again
-  const int n_mt = tile_count(g);
+  // groups of 1024 rows so that an XCD's L2 sees both operands again
+  const int n_mt = tile_count(g, kM);
   const int N = NN ? g.in : g.out;
   const uint32_t n_nt = uint32_t((N + kTN - 1) / kTN), W = uint32_t(n_mt) * n_nt;
   const uint32_t per = (W + 7) / 8, xi = blockIdx.x / 8;
   const uint32_t L = (blockIdx.x % 8) * per + xi;
   if (xi >= per || L >= W) return;
-  constexpr uint32_t kGroup = 8;
+  constexpr uint32_t kGroup = 16 / WM;
   const uint32_t grp = L / (kGroup * n_nt), rem = L % (kGroup * n_nt), m0 = grp * kGroup;
   const uint32_t gm = min(kGroup, uint32_t(n_mt) - m0);
   const int nt = int(rem / gm);
-  const int4 tm = tile_of(g, int(m0 + rem % gm));
+  const int4 tm = tile_of(g, int(m0 + rem % gm), kM);
   const int64_t e = tm.x, row0 = int64_t(tm.y) + tm.z;
   const int valid = tm.w;
 
   fill_codes<SK>(code, g.cb);
 
-  // A: 16-byte chunk tid & 7 of rows (tid >> 3) + 32 i; rows past the tile's
+  // A: 16-byte chunk tid & 7 of rows (tid >> 3) + kM / 4 i; rows past the tile's
   // last repeat it (their results are not stored)
   const uint16_t *a_src[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    a_src[i] = g.A + (row0 + min((tid >> 3) + 32 * i, valid - 1)) * g.lda + (tid & 7) * 8;
-  // B: 32 weights. !NN: half tid & 1 of weight row (tile column) tid >> 1;
-  // NN: columns 32 (tid & 3) .. of weight row (K-step's) tid >> 2
-  const int b_n = nt * kTN + (tid >> 1);
+    a_src[i] = g.A + (row0 + min((tid >> 3) + kM / 4 * i, valid - 1)) * g.lda + (tid & 7) * 8;
+  // B: kW weights. !NN: part b_p of weight row (tile column) b_r; NN: columns kW b_p ..
+  // of weight row (K-step's) b_r
+  const int b_r = NN ? tid / (kTN / kW) : tid / (kBK / kW), b_p = NN ? tid % (kTN / kW) : tid % (kBK / kW);
+  const int b_n = nt * kTN + b_r;
   const int64_t b_row = b_n < N ? b_n : 0;
-  const int b_c = nt * kTN + (tid & 3) * 32 < N ? nt * kTN + (tid & 3) * 32 : 0;
+  const int b_c = nt * kTN + b_p * kW < N ? nt * kTN + b_p * kW : 0;
   const int all = NN ? (g.out + kBK - 1) / kBK : g.in / kBK;  // K-steps, and this workgroup's
   const int first = all * int(blockIdx.y) / int(gridDim.y), nK = all * int(blockIdx.y + 1) / int(gridDim.y);
 
   u32x4 ra[4];      // A rows of the next K-step
-  Piece<SK> rb[2];  // weights of the next two, by the K-step's parity
+  Piece<SK, kW> rb[2];  // weights of the next two, by the K-step's parity
   auto load_a = [&](int ks, int i) { ra[i] = *reinterpret_cast<const u32x4 *>(a_src[i] + ks * kBK); };
-  auto load_b = [&](int ks, Piece<SK> &p) {
+  auto load_b = [&](int ks, Piece<SK, kW> &p) {
     if (!NN)
-      load_piece<SK>(g, e, b_row, ks * kBK + (tid & 1) * 32, p);
+      load_piece<SK, kW>(g, e, b_row, ks * kBK + b_p * kW, p);
     else  // weight rows past the last meet zeros of A
-      load_piece<SK>(g, e, min(ks * kBK + (tid >> 2), g.out - 1), b_c, p);
+      load_piece<SK, kW>(g, e, min(ks * kBK + b_r, g.out - 1), b_c, p);
   };
   auto store_a = [&](int st, int i) {
-    *reinterpret_cast<u32x4 *>(lds + st * kStageA + ((tid >> 3) + 32 * i) * kLds + (tid & 7) * 8) = ra[i];
+    *reinterpret_cast<u32x4 *>(lds + st * kStageA + ((tid >> 3) + kM / 4 * i) * kLds + (tid & 7) * 8) = ra[i];
   };
   auto store_b = [&](int st, int q, const u32x4 &o) {
     uint16_t *sB = lds + 2 * kStageA + st * kStageB;
     if (!NN)
-      *reinterpret_cast<u32x4 *>(sB + (tid >> 1) * kLds + (tid & 1) * 32 + q * 8) = o;
+      *reinterpret_cast<u32x4 *>(sB + b_r * kLds + b_p * kW + q * 8) = o;
     else
-      *reinterpret_cast<u32x4 *>(sB + (tid >> 2) * kTBn + nn_unit(4 * (tid & 3) + q) * 8) = o;
+      *reinterpret_cast<u32x4 *>(sB + b_r * kTBn + nn_unit(kW / 8 * b_p + q) * 8) = o;
   };
   // pair c of the piece: two table entries, then their packed bf16
-  float cv[32];
-  uint32_t bq[16];
-  auto lookup = [&](const Piece<SK> &p, int c) {
-    if constexpr (SK == LK_CODE8) {
-      const uint32_t w = p.v[c >> 3][(c >> 1) & 3] >> (16 * (c & 1));
-      cv[2 * c] = code[w & 255];
-      cv[2 * c + 1] = code[(w >> 8) & 255];
-    } else if constexpr (SK != LK_BF16) {
-      const char *tbl = reinterpret_cast<const char *>(code);
-      const uint32_t w = p.v[0][c >> 2], hi = (w >> 2) & 0x3C3C3C3Cu, lo = (w << 2) & 0x3C3C3C3Cu;
-      const uint32_t sel = 0x0C0C0C00u | uint32_t(c & 3);
-      cv[2 * c] = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, hi, sel));
-      cv[2 * c + 1] = *reinterpret_cast<const float *>(tbl + __builtin_amdgcn_perm(0u, lo, sel));
-    }
+  float cv[kW];
+  uint32_t bq[kW / 2];
+  auto lookup = [&](const Piece<SK, kW> &p, int c) {
+    if constexpr (SK != LK_BF16) lookup_pair<SK, kW>(p, code, c, cv[2 * c], cv[2 * c + 1]);
   };
-  auto scale = [&](const Piece<SK> &p, int c) {
-    if constexpr (SK != LK_BF16) bq[c] = pack_bf16x2(__fmul_rn(cv[2 * c], p.s), __fmul_rn(cv[2 * c + 1], p.s));
+  auto scale = [&](const Piece<SK, kW> &p, int c) {
+    bq[c] = SK == LK_BF16 ? p.w[SK == LK_BF16 ? c : 0]
+                          : pack_bf16x2(__fmul_rn(cv[2 * c], p.s), __fmul_rn(cv[2 * c + 1], p.s));
   };
-  auto quarter = [&](const Piece<SK> &p, int q) {
-    if constexpr (SK == LK_BF16)
-      return p.v[q];
-    else
-      return u32x4{bq[4 * q], bq[4 * q + 1], bq[4 * q + 2], bq[4 * q + 3]};
-  };
+  auto quarter = [&](int q) { return u32x4{bq[4 * q], bq[4 * q + 1], bq[4 * q + 2], bq[4 * q + 3]}; };
   // transpose-read addresses of the [k][n] tile (see gemm_wide.hip)
   int q_off[2];
   {
@@ -354,15 +361,14 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   load_b(min(first + 1, last), rb[1]);
   __syncthreads();  // the code table
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < kW / 2; ++c) {
     lookup(rb[0], c);
     scale(rb[0], c);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    store_a(0, q);
-    store_b(0, q, quarter(rb[0], q));
-  }
+  for (int q = 0; q < kW / 8; ++q) store_b(0, q, quarter(q));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) store_a(0, i);
 #pragma unroll
   for (int i = 0; i < 4; ++i) load_a(min(first + 1, last), i);
   load_b(min(first + 2, last), rb[0]);
@@ -373,22 +379,23 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   auto kstep = [&](auto cur_c, int ks) {
     constexpr int CUR = decltype(cur_c)::value, NXT = CUR ^ 1;
     const int ka = min(ks + 2, last), kb = min(ks + 3, last);
-    Piece<SK> &b = rb[NXT];  // the weights of ks + 1
+    Piece<SK, kW> &b = rb[NXT];      // the weights of ks + 1
+    constexpr int kL = kW / 16;      // pairs per slot
     slots([&](auto sc) {
       constexpr int s = decltype(sc)::value, kk = s >> 2, w = s & 3;
       acc[w >> 1][w & 1] =
           __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[kk & 1][w & 1], af[kk & 1][w >> 1], acc[w >> 1][w & 1], 0, 0, 0);
       // in the order in which the next k-slice uses them
       if constexpr (kk < 3) frag(CUR, kk + 1, w == 0 ? 0 : w == 1 ? 2 : w == 2 ? 1 : 3);
-      if constexpr (s < 8) {
-        lookup(b, 2 * s);
-        lookup(b, 2 * s + 1);
+#pragma unroll
+      for (int c = 0; c < kL; ++c) {
+        if constexpr (s < 8) lookup(b, kL * s + c);
+        if constexpr (s >= 2 && s < 10) scale(b, kL * (s - 2) + c);
       }
-      if constexpr (s >= 2 && s < 10) {
-        scale(b, 2 * (s - 2));
-        scale(b, 2 * (s - 2) + 1);
-      }
-      if constexpr (s == 4 || s == 6 || s == 8 || s == 10) store_b(NXT, (s - 4) / 2, quarter(b, (s - 4) / 2));
+      // 8 weights once their last pair is scaled
+#pragma unroll
+      for (int q = 0; q < kW / 8; ++q)
+        if (s == (4 * q + 3) / kL + 3) store_b(NXT, q, quarter(q));
       if constexpr (s >= 7 && s < 11) store_a(NXT, s - 7);
       if constexpr (s >= 8 && s < 12) load_a(ka, s - 8);
       if constexpr (s == 11) {
@@ -426,7 +433,7 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   if (g.part) {
     float *out = g.part + int64_t(blockIdx.y) * g.rows * N;
     const int cc = (tid & 31) * 4, col = nt * kTN + cc;
-    for (int r = tid >> 5; r < valid; r += 8) {
+    for (int r = tid >> 5; r < valid; r += kThreads / 32) {
       const f32x4 v = *reinterpret_cast<const f32x4 *>(tile + r * kTOut + cc);
       float *o = out + (row0 + r) * N + col;
       if (N % 4 == 0) {
@@ -442,7 +449,7 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
   if (NN) {
     const int cc = (tid & 15) * 8, col = nt * kTN + cc;
     if (col < N)  // N is a multiple of 64
-      for (int r = tid >> 4; r < valid; r += 16) {
+      for (int r = tid >> 4; r < valid; r += kThreads / 16) {
         float v[8];
         load_row<8>(tile + r * kTOut + cc, v);
         store_row<8>(reinterpret_cast<bf16_t *>(g.y) + (row0 + r) * N + col, v);
@@ -458,7 +465,7 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 #pragma unroll
     for (int q = 0; q < VEC; ++q) b[q] = 0.0f;
     if (g.bias) load_row<VEC>(g.bias + e * g.out + col, b);
-    for (int r = tid / kCols; r < valid; r += kTThreads / kCols) {
+    for (int r = tid / kCols; r < valid; r += kThreads / kCols) {
       float v[VEC];
       load_row<VEC>(tile + r * kTOut + cc, v);
       linear_epilogue<VEC>(g, (row0 + r) * g.out + col, b, v);
@@ -474,9 +481,9 @@ __global__ __launch_bounds__(kTThreads, 2) void linear_tile_kernel(LinearArgs g)
 // 8 rows of a row tile and 32 VEC columns.
 template <bool NN, int VEC>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int splits) {
-  constexpr int kGroups = kTM / 8;
-  if (int(blockIdx.x / kGroups) >= tile_count(g)) return;
-  const int4 tm = tile_of(g, blockIdx.x / kGroups);
+  constexpr int kGroups = kLinearM / 8;
+  if (int(blockIdx.x / kGroups) >= tile_count(g, kLinearM)) return;
+  const int4 tm = tile_of(g, blockIdx.x / kGroups, kLinearM);
   const int64_t row0 = int64_t(tm.y) + tm.z, N = NN ? g.in : g.out;
   const int r = blockIdx.x % kGroups * 8 + (threadIdx.x >> 5);
   const int64_t col = int64_t(blockIdx.y) * 32 * VEC + (threadIdx.x & 31) * VEC;
@@ -687,8 +694,8 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs g, const G *_
                                                         const float *__restrict__ pre, uint16_t *__restrict__ dz,
                                                         int ldz, float *__restrict__ part) {
   __shared__ float red[8][32 * VEC];
-  if (int(blockIdx.x) >= tile_count(g)) return;
-  const int4 tm = tile_of(g, blockIdx.x);
+  if (int(blockIdx.x) >= tile_count(g, g.bm)) return;
+  const int4 tm = tile_of(g, blockIdx.x, g.bm);
   const int64_t row0 = int64_t(tm.y) + tm.z;
   const int cl = (threadIdx.x & 31) * VEC, col = blockIdx.y * 32 * VEC + cl, rl = threadIdx.x >> 5;
   float sum[VEC];
@@ -730,7 +737,7 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(LinearArgs g, const fl
                                                           float *__restrict__ gb) {
   const int e = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
   if (c >= g.out) return;
-  const int t0 = g.tile_map ? g.tile_offsets[e] : 0, t1 = g.tile_map ? g.tile_offsets[e + 1] : tile_count(g);
+  const int t0 = g.tile_map ? g.tile_offsets[e] : 0, t1 = g.tile_map ? g.tile_offsets[e + 1] : tile_count(g, g.bm);
   float v = 0.0f;
 #pragma unroll 8
   for (int t = t0; t < t1; ++t) v += part[int64_t(t) * g.out + c];
@@ -741,17 +748,17 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *p, int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = 0.0f;
 }
 
-template <bool NN>
+template <bool NN, int WM>
 hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws, hipStream_t s) {
   const int64_t N = NN ? a.in : a.out, tiles = p.m_bound * ((N + kTN - 1) / kTN);
-  const dim3 grid(uint32_t((tiles + 7) / 8 * 8), uint32_t(splits)), block(kTThreads);
+  const dim3 grid(uint32_t((tiles + 7) / 8 * 8), uint32_t(splits)), block(Tile<WM>::kThreads);
   a.part = splits > 1 ? reinterpret_cast<float *>(ws + p.off_split) : nullptr;
   switch (a.cb) {
-    case E4B_CB_BF16: hipLaunchKernelGGL((linear_tile_kernel<LK_BF16, NN>), grid, block, 0, s, a); break;
-    case E4B_CB_MXFP4: hipLaunchKernelGGL((linear_tile_kernel<LK_MX, NN>), grid, block, 0, s, a); break;
+    case E4B_CB_BF16: hipLaunchKernelGGL((linear_tile_kernel<LK_BF16, NN, WM>), grid, block, 0, s, a); break;
+    case E4B_CB_MXFP4: hipLaunchKernelGGL((linear_tile_kernel<LK_MX, NN, WM>), grid, block, 0, s, a); break;
     case E4B_CB_INT8:
-    case E4B_CB_FP8: hipLaunchKernelGGL((linear_tile_kernel<LK_CODE8, NN>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((linear_tile_kernel<LK_ABSMAX, NN>), grid, block, 0, s, a); break;
+    case E4B_CB_FP8: hipLaunchKernelGGL((linear_tile_kernel<LK_CODE8, NN, WM>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((linear_tile_kernel<LK_ABSMAX, NN, WM>), grid, block, 0, s, a); break;
   }
   if (splits > 1) {
     const hipError_t e = hipGetLastError();
@@ -759,7 +766,7 @@ hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws,
     const bool vec = N % 8 == 0;
     const int cols = vec ? 256 : 32;
     hipLaunchKernelGGL((vec ? linear_join_kernel<NN, 8> : linear_join_kernel<NN, 1>),
-                       dim3(uint32_t(p.m_bound * (kTM / 8)), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
+                       dim3(uint32_t(p.m_bound * (kLinearM / 8)), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
   }
   return hipGetLastError();
 }
@@ -829,15 +836,17 @@ GemmArgs wide_args(const LinearPlan &p, const LinearArgs &a, bool nn) {
 
 hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_t *offsets, char *ws, hipStream_t s) {
   if (p.fwd_tiles == TILE_ROWS) return launch_rows(p, a, offsets, s);
-  if (p.fwd_tiles == TILE_128) return launch_tiles<false>(a, p, p.fwd_splits, ws, s);
+  if (p.fwd_tiles == TILE_128) return launch_tiles<false, 2>(a, p, p.fwd_splits, ws, s);
+  if (p.fwd_tiles == TILE_TALL) return launch_tiles<false, 4>(a, p, 1, ws, s);
   return launch_grouped_gemm(GEMM_LINEAR, wide_args(p, a, false), s);
 }
 
-// Makes the map for tiles of bm rows where they need one, in `a`'s place for it.
-hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, const int32_t *offsets, int bm, void *zero_a,
-                      int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
+// Makes the map for a kind of tiles where they need one, in `a`'s place for it.
+hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, const int32_t *offsets, int tiles,
+                      void *zero_a, int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
   const int64_t bound = p.m_bound;
-  a.tile_map = offsets || bm != kLinearM ? place : nullptr;
+  const int bm = a.bm = tiles == TILE_128 ? kLinearM : kBM;
+  a.tile_map = offsets || tiles == TILE_256 ? place : nullptr;
   if (!a.tile_map) return hipSuccess;
   // without offsets every row belongs to an expert: nothing to clear
   const uint32_t grid = offsets && (zero_a || zero_b) ? 1 + kZeroBlocks : 1;
@@ -984,7 +993,9 @@ extern "C" e4b_status e4b_expert_linear_dgrad(const e4b_stack *st, int64_t rows,
   a.y = grad_x_bf16;
   if (tiles == TILE_256)
     E4B_TRY(launch_grouped_gemm(GEMM_GATE_UP_DGRAD, wide_args(p, a, true), stream));
+  else if (tiles == TILE_TALL)
+    E4B_TRY((launch_tiles<true, 4>(a, p, 1, w, stream)));
   else
-    E4B_TRY(launch_tiles<true>(a, p, p.bwd_splits, w, stream));
+    E4B_TRY((launch_tiles<true, 2>(a, p, p.bwd_splits, w, stream)));
   return E4B_OK;
 }

@@ -58,9 +58,9 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   return E4B_OK;
 }
 
-// How a product's rows are tiled: by the kernel for few rows, in 128-row tiles
-// (cut along k where they are few) or in 256-row tiles. In us on one MI355X, nf4
-// unless said, as few rows / 128 / 256:
+// How a product is tiled: by the kernel for few rows, or in tiles of 128 x 128
+// (cut along k where they are few), 256 x 128 or 256 x 256. In us on one MI355X, nf4
+// unless said; few rows / 128 x 128 / 256 x 256:
 //   few rows to an expert, up to 8 on average: 64 experts of 2048 -> 2048, 4 rows each
 //     47 / 93 / 117, 8 each 48 / 93 / 117, 24 each 78 / 95 / 119; beyond 8 a skewed
 //     routing gives one expert too many rows for a kernel that reads its weights again
@@ -70,27 +70,35 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
 //     rows 14 / 18 / 95, 64 rows 26 / 19 / 95; 8- and 16-bit weights, which are two and
 //     four times the bytes to read again, up to 2^29: bf16 4096 -> 4096, 16 rows
 //     13 / 15 / 78, 64 rows 40 / 21 / 81
-//   256-row tiles when the experts fill half of one each and the 128-row tiles are more
-//     than two for every CU, which is one round of those: 2048 -> 4096, 1024 rows
-//     - / 33 / 57, 2048 rows - / 53 / 62, 4096 rows - / 97 / 77; 64 experts of
-//     2048 -> 2048, 96 rows each 222 / 101 / 133, 128 each 263 / 150 / 138
-static bool fills_wide_tiles(const e4b_stack *st, int64_t rows, int64_t cols) {
-  // (the wide tiles address their rows in 32 bits)
+//   else the tiles that take the least time by the rounds that the chip needs for them:
+//     a K-step of a round takes 0.82 us with one 128 x 128 tile on every CU, 1.5 with
+//     two, 1.15 with a 256 x 128 tile and 1.9 with a 256 x 256 one, beside the 10 us or
+//     so of a launch and its epilogue (2048 -> 4096 with GELU, 128 x 128 / 256 x 128 /
+//     256 x 256: 1024 rows 37 / 46 / 65, 2048 rows 60 / 50 / 71, 4096 rows 112 / 95 / 86;
+//     64 experts of 2048 -> 2048, 64 rows each 102 / 155 / 132, 128 each 153 / 159 / 140;
+//     8 experts of 4096 -> 4096, 128 rows each 91 / 78 / 104, 256 each 140 / 137 / 116)
+static int best_tiles(const e4b_stack *st, int64_t rows, int64_t cols, bool wide) {
+  // every other expert's last tile of rows is taken as half full
+  const int64_t busy = st->E < rows ? st->E : rows, more = busy > 0 ? busy - 1 : 0;
+  const int64_t low = (rows + 64 * more + 127) / 128, tall = (rows + 128 * more + 255) / 256;
+  const int64_t narrow = (cols + 127) / 128, broad = (cols + 255) / 256;
+  const int64_t n = low * narrow;
+  const int64_t t128 = n <= 256 ? 82 : (n + 511) / 512 * 150, ttall = (tall * narrow + 255) / 256 * 115;
+  const int64_t t256 = (tall * broad + 255) / 256 * 190;
+  // (the 256 x 256 tiles address their rows in 32 bits)
   const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
-  const int64_t tiles = (rows + 64 * (st->E - 1)) / kLinearM * ((cols + 127) / 128);  // a ragged one for every other expert
-  return rows >= 128 * st->E && tiles > 512 && rows * longest < (int64_t(1) << 32);
+  if (wide && rows * longest < (int64_t(1) << 32) && t256 < t128 && t256 < ttall) return TILE_256;
+  return ttall < t128 ? TILE_TALL : TILE_128;
 }
 
 static int forward_tiles(const e4b_stack *st, int64_t rows) {
   const bool four = st->codebook == E4B_CB_NF4 || st->codebook == E4B_CB_FP4 || st->codebook == E4B_CB_MXFP4;
   const int64_t most = four ? (st->in <= 2048 ? int64_t(1) << 31 : (int64_t(1) << 30) - 1) : int64_t(1) << 29;
   if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out * st->in <= most) return TILE_ROWS;
-  return st->out % 8 == 0 && fills_wide_tiles(st, rows, st->out) ? TILE_256 : TILE_128;
+  return best_tiles(st, rows, st->out, st->out % 8 == 0);
 }
 
-static int dgrad_tiles(const e4b_stack *st, int64_t rows) {
-  return st->out % kBK == 0 && fills_wide_tiles(st, rows, st->in) ? TILE_256 : TILE_128;
-}
+static int dgrad_tiles(const e4b_stack *st, int64_t rows) { return best_tiles(st, rows, st->in, st->out % kBK == 0); }
 
 // Workgroups along k, where 128-row tiles leave most of the chip idle: 512 in all
 // (two per CU), with at least four K-steps each. nf4 4096 -> 4096, 64 rows: 19 us with

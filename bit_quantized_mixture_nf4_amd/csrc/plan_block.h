@@ -52,7 +52,8 @@ inline size_t norm_ws_bytes(const NormArgs &a) {
 
 // ---- stored-weight products (linear.hip) ----
 constexpr int kLinearM = 128;  // rows per tile
-enum { TILE_ROWS = 0, TILE_128 = 128, TILE_256 = 256 };  // how a product's rows are tiled
+// how a product is tiled: few rows, 128 x 128, 256 x 128, 256 x 256
+enum { TILE_ROWS = 0, TILE_128, TILE_TALL, TILE_256 };
 struct LinearPlan {
   int fwd_tiles, bwd_tiles;    // of the product, and of its gradient
   int fwd_splits, bwd_splits;  // 128-row tiles: workgroups along k
@@ -75,6 +76,7 @@ struct LinearArgs {
   void *y;                   // [rows, out] bf16 / fp32; dgrad: grad_x [rows, in] bf16
   float *pre;                // [rows, out] or null
   int32_t act, y_f32;
+  int32_t bm;  // rows per tile
   int64_t rows;
   float *part;  // [splits, rows, out] (dgrad: in) or null
 };

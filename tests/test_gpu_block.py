@@ -261,6 +261,18 @@ LINEARS = [
     ("int8", 1, 2200, 0, 4224, 192, "gelu_tanh", True, False, "bf16"),
     ("mxfp4", 3, 2600, 0, 3968, 64, "none", False, False, "fp32"),
     ("bf16", 2, 2304, 0, 4096, 128, "silu", True, False, "bf16"),
+    ("nf4", 2, 3500, 4, 192, 4104, "gelu", True, True, "bf16"),
+    # 256 x 128 tiles, forward and gradient
+    ("nf4", 1, 2100, 0, 448, 2300, "gelu", True, True, "bf16"),
+    ("bf16", 1, 2100, 0, 128, 2304, "none", True, True, "fp32"),
+    ("fp8", 3, 1900, 7, 128, 2322, "silu", True, False, "bf16"),
+    ("int8", 1, 1793, 1, 192, 2304, "relu", False, True, "bf16"),
+    ("fp4", 1, 2100, 3, 512, 2312, "gelu_tanh", True, False, "bf16"),
+    ("mxfp4", 2, 3000, 0, 704, 4101, "silu", True, False, "fp32"),
+    ("bf16", 1, 2100, 0, 2304, 192, "silu", True, False, "bf16"),
+    ("nf4", 2, 1900, 3, 2304, 100, "gelu", True, True, "bf16"),
+    ("mxfp4", 3, 1900, 1, 2112, 64, "none", True, False, "bf16"),
+    ("int8", 1, 2100, 0, 2176, 60, "relu", True, False, "fp32"),
 ]
 
 
