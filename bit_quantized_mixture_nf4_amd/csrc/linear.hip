@@ -258,14 +258,17 @@ __global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_ti
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 
-  // real tiles split evenly over the 8 XCDs (block b runs on XCD b % 8), in
-  // groups of 1024 rows so that an XCD's L2 sees both operands again
+  // real tiles, one share of k after the other, split evenly over the 8 XCDs (block b
+  // runs on XCD b % 8), in groups of 1024 rows so that an XCD's L2 sees both operands
+  // again; the workgroups without a tile come last
   const int n_mt = tile_count(g, kM);
   const int N = NN ? g.in : g.out;
   const uint32_t n_nt = uint32_t((N + kTN - 1) / kTN), W = uint32_t(n_mt) * n_nt;
-  const uint32_t per = (W + 7) / 8, xi = blockIdx.x / 8;
-  const uint32_t L = (blockIdx.x % 8) * per + xi;
-  if (xi >= per || L >= W) return;
+  const uint32_t per = (W * g.splits + 7) / 8, xi = blockIdx.x / 8;
+  uint32_t L = (blockIdx.x % 8) * per + xi;
+  if (xi >= per || L >= W * g.splits) return;
+  const int share = int(L / W);
+  L -= share * W;
   constexpr uint32_t kGroup = 16 / WM;
   const uint32_t grp = L / (kGroup * n_nt), rem = L % (kGroup * n_nt), m0 = grp * kGroup;
   const uint32_t gm = min(kGroup, uint32_t(n_mt) - m0);
@@ -289,7 +292,7 @@ __global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_ti
   const int64_t b_row = b_n < N ? b_n : 0;
   const int b_c = nt * kTN + b_p * kW < N ? nt * kTN + b_p * kW : 0;
   const int all = NN ? (g.out + kBK - 1) / kBK : g.in / kBK;  // K-steps, and this workgroup's
-  const int first = all * int(blockIdx.y) / int(gridDim.y), nK = all * int(blockIdx.y + 1) / int(gridDim.y);
+  const int first = all * share / g.splits, nK = all * (share + 1) / g.splits;
 
   u32x4 ra[4];      // A rows of the next K-step
   Piece<SK, kW> rb[2];  // weights of the next two, by the K-step's parity
@@ -434,7 +437,7 @@ __global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_ti
       }
   __syncthreads();
   if (g.part) {
-    float *out = g.part + int64_t(blockIdx.y) * g.rows * N;
+    float *out = g.part + int64_t(share) * g.rows * N;
     const int cc = (tid & 31) * 4, col = nt * kTN + cc;
     for (int r = tid >> 5; r < valid; r += kThreads / 32) {
       const f32x4 v = *reinterpret_cast<const f32x4 *>(tile + r * kTOut + cc);
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_ti
 // The sums of a product's splits, in order, and its epilogue. One workgroup per
 // 8 rows of a row tile and 32 VEC columns.
 template <bool NN, int VEC>
-__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int splits) {
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g) {
   constexpr int kGroups = kLinearM / 8;
   if (int(blockIdx.x / kGroups) >= tile_count(g, kLinearM)) return;
   const int4 tm = tile_of(g, blockIdx.x / kGroups, kLinearM);
@@ -497,7 +500,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g, int spli
   for (int q = 0; q < VEC; ++q) b[q] = v[q] = 0.0f;
   if (!NN && g.bias) load_row<VEC>(g.bias + int64_t(tm.x) * N + col, b);
 #pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
+  for (int s = 0; s < g.splits; ++s) {
     float u[VEC];
     load_row<VEC>(g.part + int64_t(s) * g.rows * N + at, u);
 #pragma unroll
@@ -751,15 +754,16 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *p, int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = 0.0f;
 }
 
-// row tiles of bm rows, where every expert with rows may end in a partial one
+// row tiles of bm rows, at most: the last one of every expert with rows may be partial
 int64_t tiles_at_most(const LinearPlan &p, const LinearArgs &a, int bm) {
-  return p.rows / bm + (a.E < p.rows ? a.E : p.rows);
+  return (p.rows + (bm - 1) * (a.E < p.rows ? a.E : p.rows)) / bm;
 }
 
 template <bool NN, int WM>
 hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws, hipStream_t s) {
   const int64_t N = NN ? a.in : a.out, tiles = tiles_at_most(p, a, Tile<WM>::kM) * ((N + kTN - 1) / kTN);
-  const dim3 grid(uint32_t((tiles + 7) / 8 * 8), uint32_t(splits)), block(Tile<WM>::kThreads);
+  const dim3 grid(uint32_t((tiles * splits + 7) / 8 * 8)), block(Tile<WM>::kThreads);
+  a.splits = splits;
   a.part = splits > 1 ? reinterpret_cast<float *>(ws + p.off_split) : nullptr;
   switch (a.cb) {
     case E4B_CB_BF16: hipLaunchKernelGGL((linear_tile_kernel<LK_BF16, NN, WM>), grid, block, 0, s, a); break;
@@ -774,7 +778,7 @@ hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws,
     const bool vec = N % 8 == 0;
     const int cols = vec ? 256 : 32;
     hipLaunchKernelGGL((vec ? linear_join_kernel<NN, 8> : linear_join_kernel<NN, 1>),
-                       dim3(uint32_t(p.m_bound * (kLinearM / 8)), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a, splits);
+                       dim3(uint32_t(p.m_bound * (kLinearM / 8)), uint32_t((N + cols - 1) / cols)), dim3(256), 0, s, a);
   }
   return hipGetLastError();
 }

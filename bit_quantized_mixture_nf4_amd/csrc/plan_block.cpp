@@ -58,6 +58,15 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
   return E4B_OK;
 }
 
+// Row tiles to expect of an even routing: one at least for every expert with rows, and
+// for a quarter of them one more than their rows fill.
+static int64_t row_tiles(const e4b_stack *st, int64_t rows, int64_t bm) {
+  const int64_t busy = st->E < rows ? st->E : rows;
+  if (busy <= 1) return (rows + bm - 1) / bm;
+  const int64_t n = (rows + bm / 4 * busy + bm - 1) / bm;
+  return n > busy ? n : busy;
+}
+
 // How a product is tiled: by the kernel for few rows, or in tiles of 128 x 128
 // (cut along k where they are few), 256 x 128 or 256 x 256. In us on one MI355X, nf4
 // unless said; few rows / 128 x 128 / 256 x 256:
@@ -65,11 +74,11 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
 //     47 / 93 / 117, 8 each 48 / 93 / 117, 24 each 78 / 95 / 119; beyond 8 a skewed
 //     routing gives one expert too many rows for a kernel that reads its weights again
 //     for every 16
-//   up to 2^31 products: 2048 -> 4096, 256 rows 21 / 24 / 55, 384 rows 34 / 26 / 55;
-//     half of that for rows longer than the 2048 that it holds at once: 4096 -> 4096, 32
-//     rows 14 / 18 / 95, 64 rows 26 / 19 / 95; 8- and 16-bit weights, which are two and
-//     four times the bytes to read again, up to 2^29: bf16 4096 -> 4096, 16 rows
-//     13 / 15 / 78, 64 rows 40 / 21 / 81
+//   up to 2^29 products: 4096 -> 4096, 32 rows 14 / 19 / 92, 64 rows 27 / 21 / 94;
+//     2048 -> 2048, 64 rows 15 / 14 / 53; 30000 rows of 128 -> 128 9 / 11 / 17; 4096 rows
+//     of 512 -> 512 18 / 13 / 24; 8- and 16-bit weights, which are two and four times the
+//     bytes to read again, up to 2^28: bf16 4096 -> 4096, 16 rows 12.5 / 13 / 76, 32 rows
+//     20 / 14 / 77
 //   else the tiles that take the least time by the rounds that the chip needs for them:
 //     a K-step of a round takes 0.82 us with one 128 x 128 tile on every CU, 1.5 with
 //     two, 1.15 with a 256 x 128 tile and 1.9 with a 256 x 256 one, beside the 10 us or
@@ -78,9 +87,7 @@ e4b_status plan_norm(const e4b_norm *n, bool has_y, NormArgs *a) {
 //     64 experts of 2048 -> 2048, 64 rows each 102 / 155 / 132, 128 each 153 / 159 / 140;
 //     8 experts of 4096 -> 4096, 128 rows each 91 / 78 / 104, 256 each 140 / 137 / 116)
 static int best_tiles(const e4b_stack *st, int64_t rows, int64_t cols, bool wide) {
-  // every other expert's last tile of rows is taken as half full
-  const int64_t busy = st->E < rows ? st->E : rows, more = busy > 0 ? busy - 1 : 0;
-  const int64_t low = (rows + 64 * more + 127) / 128, tall = (rows + 128 * more + 255) / 256;
+  const int64_t low = row_tiles(st, rows, 128), tall = row_tiles(st, rows, 256);
   const int64_t narrow = (cols + 127) / 128, broad = (cols + 255) / 256;
   const int64_t n = low * narrow;
   const int64_t t128 = n <= 256 ? 82 : (n + 511) / 512 * 150, ttall = (tall * narrow + 255) / 256 * 115;
@@ -93,25 +100,30 @@ static int best_tiles(const e4b_stack *st, int64_t rows, int64_t cols, bool wide
 
 static int forward_tiles(const e4b_stack *st, int64_t rows) {
   const bool four = st->codebook == E4B_CB_NF4 || st->codebook == E4B_CB_FP4 || st->codebook == E4B_CB_MXFP4;
-  const int64_t most = four ? (st->in <= 2048 ? int64_t(1) << 31 : (int64_t(1) << 30) - 1) : int64_t(1) << 29;
+  const int64_t most = int64_t(1) << (four ? 29 : 28);
   if ((st->E > 1 && rows <= 8 * st->E) || rows * st->out * st->in <= most) return TILE_ROWS;
   return best_tiles(st, rows, st->out, st->out % 8 == 0);
 }
 
 static int dgrad_tiles(const e4b_stack *st, int64_t rows) { return best_tiles(st, rows, st->in, st->out % kBK == 0); }
 
-// Workgroups along k, where 128-row tiles leave most of the chip idle: 512 in all
-// (two per CU), with at least four K-steps each. nf4 4096 -> 4096, 64 rows: 19 us with
-// 16 of them, 60 without; 512 rows: 38 with 4, 57 without.
+// Workgroups along k, where 128 x 128 tiles leave most of the chip idle: of the shares
+// that still leave one workgroup per CU (512 in all took 40 us for 512 rows of nf4
+// 4096 -> 4096, 256 take 38) the one with the least time, in us 0.68 a K-step, and for
+// the sums that are written and joined 3 and one for every 2 MB of them. nf4
+// 4096 -> 4096, 64 rows: 20 us with 8 shares, 31 with 2, 51 uncut; 512 rows of
+// 2048 -> 2048: 22.7 with 4, 29 uncut; 4096 rows of 512 -> 512: 12.7 uncut, 21 with 2.
 static int k_splits(const e4b_stack *st, int64_t rows, int64_t cols, int64_t k) {
-  const int64_t busy = st->E < rows ? st->E : rows;
-  const int64_t tiles = (rows + 64 * (busy - 1) + kLinearM - 1) / kLinearM * ((cols + 127) / 128);
+  const int64_t tiles = row_tiles(st, rows, kLinearM) * ((cols + 127) / 128);
   const int64_t steps = (k + kBK - 1) / kBK;
-  if (tiles == 0 || tiles > 128) return 1;
-  int64_t s = 512 / tiles;
-  if (s > steps / 4) s = steps / 4;
-  if (s > 16) s = 16;
-  return int(s > 1 ? s : 1);
+  int best = 1;
+  if (tiles == 0 || tiles > 128) return best;
+  int64_t least = steps * 680;  // ns
+  for (int s = 2; s <= 16 && s <= steps && s * tiles <= 256; ++s) {
+    const int64_t t = (steps + s - 1) / s * 680 + 3000 + s * rows * cols * 2 / 1000;
+    if (t < least) least = t, best = s;
+  }
+  return best;
 }
 
 e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t dtype, LinearPlan *p) {
@@ -123,7 +135,7 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
   if (dtype != E4B_F32 && dtype != E4B_BF16) return E4B_ERR_DTYPE;
   p->rows = rows;
   // every expert may end in a partial tile
-  p->m_bound = rows / kLinearM + (st->E < rows ? st->E : rows);
+  p->m_bound = (rows + (kLinearM - 1) * (st->E < rows ? st->E : rows)) / kLinearM;
   p->ldz = (st->out + kBK - 1) / kBK * kBK;
   // the launch grids: 256 threads per tile, and column slabs in grid.y
   const int64_t wide = st->out > st->in ? st->out : st->in;

@@ -78,7 +78,8 @@ struct LinearArgs {
   int32_t act, y_f32;
   int32_t bm;  // rows per tile
   int64_t rows;
-  float *part;  // [splits, rows, out] (dgrad: in) or null
+  int32_t splits;  // workgroups along k of one tile
+  float *part;     // [splits, rows, out] (dgrad: in) or null
 };
 e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t dtype, LinearPlan *p);
 
