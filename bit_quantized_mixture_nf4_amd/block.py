@@ -68,6 +68,11 @@ def _workspace(ws, need, device):
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _overlap(a, b):
+    lo = max(a.data_ptr(), b.data_ptr())
+    return lo < min(a.data_ptr() + a.numel() * a.element_size(), b.data_ptr() + b.numel() * b.element_size())
+
+
 # ---- the router ----
 
 
@@ -256,7 +261,8 @@ def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, 
     (``Permutation.offsets``; None for a stack of one expert, which then takes every
     row); ``bias`` float32 [E, out]; ``act`` one of none, relu, silu, gelu, gelu_tanh;
     ``residual`` bfloat16 [rows, out]. Rows from offsets[E] on come out as zeros.
-    ``save`` keeps the fp32 pre-activation for the gradient.
+    ``save`` keeps the fp32 pre-activation for the gradient. ``out`` may be the
+    residual itself (added in place); it must not overlap x.
     Returns ``(y [rows, out] in out_dtype, pre float32 [rows, out] or None)``.
     """
     _need(x, "x", torch.bfloat16, stack.device)
@@ -272,6 +278,9 @@ def expert_linear(stack, x, offsets=None, bias=None, act="none", residual=None, 
         y = torch.empty(rows, stack.out, dtype=out_dtype, device=dev)
     else:
         _need(out, "out", out_dtype, dev, (rows, stack.out))
+        if _overlap(out, x) or (residual is not None and _overlap(out, residual)
+                                and (out.data_ptr() != residual.data_ptr() or out_dtype != residual.dtype)):
+            raise ValueError("out must not overlap x, nor the residual unless it is the residual")
         y = out
     pre = torch.empty(rows, stack.out, dtype=torch.float32, device=dev) if save else None
     c = stack.as_c()

@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void route_kernel(const float *__restrict__ lo
 // a maximum and the lowest id that has it. With 16 lanes to a token the
 // reductions are four DPP moves within a row and serve four tokens at once; a
 // wave per token took 15.1 us at 16384 x 128, top 8, this one 7.6 us (8 MB
-// read).
+// read). More than 128 experts of few tokens keep the wave (see e4b_route).
 __device__ __forceinline__ int32_t order_key(float v) {
   const int32_t b = __builtin_bit_cast(int32_t, v + 0.0f);  // -0 is +0
   return b ^ ((b >> 31) & 0x7FFFFFFF);
@@ -368,6 +368,10 @@ extern "C" e4b_status e4b_route(const float *logits, int64_t T, int64_t E, int32
     hipLaunchKernelGGL(kernel, dim3(uint32_t((T + tokens - 1) / tokens)), dim3(256), 0, stream, logits, T, int(E),
                        int(top_k), topk_idx, topk_w);
   };
+  // 16 lanes a token do least in all, 64 get a token's maxima soonest (in us for top 16,
+  // 16 / 64 lanes: 256 experts, 2048 tokens 7.9 / 7.0, 16384 tokens 15.4 / 31.5; 512
+  // experts, 2048 tokens 12.4 / 8.0, 16384 tokens 24.8 / 37.6; 1000 experts 21 / 10, 48 / 51)
+  const bool many = T > 4096;
   if (E <= 16)
     go(route_masked_kernel<16, 1>, 16);
   else if (E <= 32)
@@ -376,8 +380,12 @@ extern "C" e4b_status e4b_route(const float *logits, int64_t T, int64_t E, int32
     go(route_masked_kernel<16, 4>, 16);
   else if (E <= 128)
     go(route_masked_kernel<16, 8>, 16);
+  else if (E <= 256 && !many)
+    go(route_masked_kernel<64, 4>, 64);
   else if (E <= 256)
     go(route_masked_kernel<16, 16>, 16);
+  else if (E <= 512 && many)
+    go(route_masked_kernel<16, 32>, 16);
   else if (E <= 512)
     go(route_masked_kernel<64, 8>, 64);
   else

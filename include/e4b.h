@@ -508,7 +508,8 @@ typedef enum {
  *   x_bf16   : device bf16 [rows, in]
  *   bias     : device fp32 [E, out] or NULL
  *   residual : device bf16 [rows, out] or NULL
- *   y        : device [rows, out], bf16 or fp32 (y_dtype)  (written)
+ *   y        : device [rows, out], bf16 or fp32 (y_dtype)  (written); a bf16 y may be
+ *              the residual, in place, and must not overlap x
  *   pre      : device fp32 [rows, out] or NULL: z, for the gradient  (written)
  *   ws       : device workspace of e4b_expert_linear_workspace_bytes() (0 for few
  *              rows, or for invalid arguments: then ws may be NULL)

@@ -49,7 +49,9 @@ def bits(t):
 
 
 @pytest.mark.parametrize("T,E,k,masked", [(1, 1, 1, False), (3, 8, 2, True), (64, 60, 5, False), (257, 128, 8, True),
-                                          (33, 1024, 32, True), (5, 65, 32, False), (0, 8, 2, False)])
+                                          (33, 1024, 32, True), (5, 65, 32, False), (0, 8, 2, False),
+                                          (300, 256, 16, False), (70, 400, 12, True), (4097, 200, 9, True),
+                                          (4100, 511, 16, True)])
 def test_route_and_its_gradient(T, E, k, masked):
     announce(f"route T={T} E={E} k={k} masked={masked}")
     rng = np.random.default_rng(T + E)
@@ -397,6 +399,24 @@ def _norm_inputs(T, H, dt, has_y, post, gate, pre):
     gr = dev(rng.standard_normal((T, H)), DT[dt])
     gh = dev(rng.standard_normal((T, H)), torch.bfloat16) if pre else None
     return x, kw, gr, gh
+
+
+@pytest.mark.parametrize("E,rows,inn,out", [(1, 20, 128, 96), (1, 300, 2048, 520), (3, 900, 1024, 1001), (1, 2100, 448, 2300),
+                                            (2, 3500, 192, 4104)])
+def test_residual_added_in_place(E, rows, inn, out):
+    """y may be written over the residual, in every tiling; over the rows of x it may not."""
+    announce(f"in place E={E} rows={rows} {inn} -> {out}")
+    rng = np.random.default_rng(rows)
+    stack, _ = _stack(E, out, inn, "nf4", 3)
+    x = dev(rng.standard_normal((rows, inn)), torch.bfloat16)
+    res = dev(rng.standard_normal((rows, out)), torch.bfloat16)
+    off = torch.linspace(0, rows - 5, E + 1, device=DEV).to(torch.int32) if E > 1 else None
+    want = e4b.expert_linear(stack, x, off, act="silu", residual=res)[0]
+    got = e4b.expert_linear(stack, x, off, act="silu", residual=res, out=res)[0]
+    assert got.data_ptr() == res.data_ptr() and torch.equal(bits(got), bits(want))
+    square, _ = _stack(1, inn, inn, "nf4", 4)
+    with pytest.raises(ValueError, match="overlap"):
+        e4b.expert_linear(square, x, out=x)
 
 
 @pytest.mark.parametrize("T,H,dt,has_y,post,gate,pre", NORMS)
