@@ -33,12 +33,12 @@ __device__ __forceinline__ float normal_cdf(float z, float &density) {
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
-// v = act(v), the branch outside the elements
+// v = act(v), the branch outside the elements; a NaN stays one
 template <int VEC>
 __device__ __forceinline__ void act_values(int act, float (&v)[VEC]) {
   if (act == E4B_ACT_RELU) {
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) v[q] = v[q] > 0.0f ? v[q] : 0.0f;
+    for (int q = 0; q < VEC; ++q) v[q] = v[q] <= 0.0f ? 0.0f : v[q];
   } else if (act == E4B_ACT_SILU) {
 #pragma unroll
     for (int q = 0; q < VEC; ++q) v[q] *= sigmoid_f32(v[q]);
@@ -54,12 +54,12 @@ __device__ __forceinline__ void act_values(int act, float (&v)[VEC]) {
   }
 }
 
-// v *= act'(z)
+// v *= act'(z); a NaN of either stays one
 template <int VEC>
 __device__ __forceinline__ void act_grads(int act, const float (&z)[VEC], float (&v)[VEC]) {
   if (act == E4B_ACT_RELU) {
 #pragma unroll
-    for (int q = 0; q < VEC; ++q) v[q] = z[q] > 0.0f ? v[q] : 0.0f;
+    for (int q = 0; q < VEC; ++q) v[q] *= z[q] > 0.0f ? 1.0f : z[q] <= 0.0f ? 0.0f : z[q];
   } else if (act == E4B_ACT_SILU) {
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {

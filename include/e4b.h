@@ -485,7 +485,7 @@ e4b_status e4b_unpermute_backward(int64_t T, int32_t top_k, int64_t E, int64_t H
                                   void *grad_rows, float *grad_topk_w, hipStream_t stream);
 
 /* Activations of e4b_expert_linear: none, max(z, 0), z sigmoid(z), z Phi(z), and
- * GELU's tanh form. */
+ * GELU's tanh form. A NaN passes every one of them, and its gradient. */
 typedef enum {
   E4B_ACT_NONE = 0,
   E4B_ACT_RELU = 1,

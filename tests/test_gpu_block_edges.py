@@ -1,0 +1,65 @@
+"""Values at the edges of the operators around the expert MLP: NaN and infinities that a
+diverged model has in live rows, far tails, skewed routings, every tiling's row counts.
+
+Tolerances as in test_gpu_block: counted in steps U = 2^-24 of fp32 and half steps of the
+output's type, derived beside each test.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_mixture_nf4_amd as e4b
+from gpu_util import DEV, announce
+from test_gpu_block import U, _stack, bits, dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+# few rows, 128 x 128 tiles cut along k, 256 x 128, 256 x 256
+TILINGS = [(1, 20, 128, 96), (1, 300, 2048, 520), (1, 2100, 448, 2300), (2, 3500, 192, 4104)]
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("E,rows,inn,out", TILINGS)
+def test_nan_passes_every_activation(E, rows, inn, out, act):
+    """A NaN in a live row's x, in a bias or in a gradient shows in everything that it enters, and
+    in nothing else: the other elements keep their bits."""
+    announce(f"NaN through {act} E={E} rows={rows} {inn} -> {out}")
+    rng = np.random.default_rng(rows)
+    stack, _ = _stack(E, out, inn, "nf4", 3)
+    off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device=DEV) if E > 1 else None
+    x = dev(rng.standard_normal((rows, inn)), torch.bfloat16)
+    bias = dev(rng.standard_normal((E, out)) * 0.1, torch.float32)
+    gy = dev(rng.standard_normal((rows, out)), torch.bfloat16)
+    y, pre = e4b.expert_linear(stack, x, off, bias, act, save=True)
+    gx, gb = e4b.expert_linear_dgrad(stack, gy, offsets=off, act=act, pre=pre, grad_bias=True)
+
+    r, c = rows - 3, out // 2  # a row of the last expert, a column
+    bad_x, bad_b = x.clone(), bias.clone()
+    bad_x[r, 5] = float("nan")
+    bad_b[0, c] = float("nan")
+    y2, pre2 = e4b.expert_linear(stack, bad_x, off, bad_b, act, save=True)
+    n0 = rows // 2 if E > 1 else rows  # rows of expert 0
+    want = torch.zeros(rows, out, dtype=torch.bool, device=DEV)
+    want[r] = True
+    want[:n0, c] = True
+    assert torch.equal(y2.isnan(), want) and torch.equal(pre2.isnan(), want)
+    assert torch.equal(bits(y2)[~want], bits(y)[~want])
+
+    # the gradient of a row whose pre-activation is NaN (an activation's), then of a NaN gradient
+    if act != "none":
+        bad_pre = pre.clone()
+        bad_pre[r] = float("nan")
+        gx2, gb2 = e4b.expert_linear_dgrad(stack, gy, offsets=off, act=act, pre=bad_pre, grad_bias=True)
+        assert gx2[r].isnan().all() and gb2[E - 1].isnan().all()
+        keep = torch.arange(rows, device=DEV) != r
+        assert torch.equal(bits(gx2)[keep], bits(gx)[keep]) and torch.equal(bits(gb2)[:E - 1], bits(gb)[:E - 1])
+    low = int(pre[r].argmin())  # where max(z, 0) is flat: NaN times 0
+    assert pre[r, low] < 0
+    bad_gy = gy.clone()
+    bad_gy[r, low] = float("nan")
+    gx2, gb2 = e4b.expert_linear_dgrad(stack, bad_gy, offsets=off, act=act, pre=pre, grad_bias=True)
+    assert gx2[r].isnan().all() and gb2[E - 1, low].isnan() and int(gb2.isnan().sum()) == 1
+    keep = torch.arange(rows, device=DEV) != r
+    assert torch.equal(bits(gx2)[keep], bits(gx)[keep])
