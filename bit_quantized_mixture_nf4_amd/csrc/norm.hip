@@ -209,10 +209,11 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
       for (int q = 0; q < VEC; ++q) {
         m[c][q] *= rs_y;
         const float v = m[c][q] * wp[c][q] * (CHANNEL ? gc[c][q] : 1.0f);  // u, or g u
-        n[c][q] = (n[c][q] + sg * v) * rs_r;
+        // (without a pre-norm nothing of r reaches a gradient, not even as 0 times an infinity)
+        n[c][q] = pre ? (n[c][q] + sg * v) * rs_r : 0.0f;
         const float cc = gh[q] * wq[c][q];
         sums[0] += cc * n[c][q];
-        sums[2] += n[c][q] * v;
+        sums[2] += pre ? n[c][q] * v : 0.0f;
         d[c][q] += rs_r * cc;
         s_pre[c][q] += gh[q] * n[c][q];
         sums[1] += d[c][q] * v;
@@ -249,7 +250,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
         if (CHANNEL) s_gate[c][q] += a.scale * dr * (m[c][q] * wp[c][q]);
         s_post[c][q] += du * m[c][q];
         d[c][q] = dr;
-        o[q] = rs_y * (du * wp[c][q] - m[c][q] * m2);
+        o[q] = post ? rs_y * (du * wp[c][q] - m[c][q] * m2) : du;
       }
       if (on && h < a.H) {
         store_row<VEC>(static_cast<X *>(a.grad_x) + row + h, d[c]);

@@ -63,3 +63,45 @@ def test_nan_passes_every_activation(E, rows, inn, out, act):
     assert gx2[r].isnan().all() and gb2[E - 1, low].isnan() and int(gb2.isnan().sum()) == 1
     keep = torch.arange(rows, device=DEV) != r
     assert torch.equal(bits(gx2)[keep], bits(gx)[keep])
+
+
+@pytest.mark.parametrize("T,H,dt", [(5, 264, "bf16"), (9, 33, "fp32"), (3, 4104, "fp32"), (600, 512, "bf16"), (2, 16384, "bf16")])
+@pytest.mark.parametrize("gate", [None, "token", "channel"])
+@pytest.mark.parametrize("post", [False, True])
+def test_block_norm_gradient_without_pre_norm_of_an_overflowed_block(T, H, dt, gate, post):
+    """Without w_pre, r = x + scale g u: grad_x is grad_r whatever y holds, and without w_post
+    grad_y = scale g grad_r. An infinity, a NaN or a product beyond fp32 in y reaches only what y is
+    a factor of: its row's token gate, its column's channel gate."""
+    announce(f"norm backward of an overflowed y T={T} H={H} {dt} gate={gate} post={post}")
+    rng = np.random.default_rng(H)
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    x, y = dev(rng.standard_normal((T, H)), dtype), dev(rng.standard_normal((T, H)), torch.bfloat16)
+    gr = dev(rng.standard_normal((T, H)), dtype)
+    kw = {"scale": 4.0}
+    if post:
+        kw["w_post"] = dev(1 + 0.1 * rng.standard_normal(H), torch.float32)
+    g = 1.0
+    if gate:
+        g = dev(1 + rng.random(T if gate == "token" else H), torch.float32)
+        kw["gate_" + gate] = g
+        g = g[:, None] if gate == "token" else g
+    clean = e4b.block_norm_backward(e4b.block_norm(x, y=y, **kw), x, gr, y=y, **kw)
+    row, cols = T - 2, [1, H // 2, H - 1]
+    bad = y.clone()
+    bad[row, cols] = torch.tensor([float("inf"), float("nan"), 3e38], dtype=torch.bfloat16, device=DEV)
+    f = e4b.block_norm(x, y=bad, **kw)
+    b = e4b.block_norm_backward(f, x, gr, y=bad, **kw)
+    assert torch.equal(bits(b.grad_x), bits(gr))
+    keep = torch.arange(T, device=DEV) != row
+    assert torch.equal(bits(b.grad_y)[keep], bits(clean.grad_y)[keep])
+    if post:  # the row's own statistic is lost: nothing to expect of its grad_y
+        return
+    # grad_y is one product of three (two of them exact powers) rounded to bf16: as without the bad values
+    assert torch.equal(bits(b.grad_y), bits(clean.grad_y))
+    if gate == "token":
+        assert torch.equal(bits(b.grad_gate)[keep], bits(clean.grad_gate)[keep]) and not b.grad_gate[row].isfinite()
+    elif gate == "channel":
+        ok = torch.ones(H, dtype=torch.bool, device=DEV)
+        ok[cols] = False
+        assert torch.equal(bits(b.grad_gate)[ok], bits(clean.grad_gate)[ok])
+        assert b.grad_gate[cols[0]].isinf() and b.grad_gate[cols[1]].isnan()
