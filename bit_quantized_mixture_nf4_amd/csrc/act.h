@@ -74,11 +74,13 @@ __device__ __forceinline__ void act_grads(int act, const float (&z)[VEC], float 
       v[q] *= cdf + z[q] * density;
     }
   } else if (act == E4B_ACT_GELU_TANH) {
-    // d/dz z S(w) = S + z S (1 - S) w', w' = 2 sqrt(2/pi) (1 + 3 0.044715 z^2)
+    // d/dz z S(w) = S + z S (1 - S) w', w' = 2 sqrt(2/pi) (1 + 3 0.044715 z^2), z^2 taken
+    // into t = z S (1 - S), which is 0 before z^2 overflows (0 times infinity has no value)
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
       const float s = sigmoid_f32(gelu_tanh_arg(z[q]));
-      v[q] *= s + z[q] * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z[q] * z[q]);
+      const float t = z[q] * s * (1.0f - s);
+      v[q] *= s + 1.5957691216057308f * (t + 0.134145f * (t * z[q] * z[q]));
     }
   }
 }

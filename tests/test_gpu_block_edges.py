@@ -105,3 +105,26 @@ def test_block_norm_gradient_without_pre_norm_of_an_overflowed_block(T, H, dt, g
         ok[cols] = False
         assert torch.equal(bits(b.grad_gate)[ok], bits(clean.grad_gate)[ok])
         assert b.grad_gate[cols[0]].isinf() and b.grad_gate[cols[1]].isnan()
+
+
+def _act_values(act, z):
+    """(act(z), act'(z)) as the kernels compute them in fp32, one value each: zero weights and the
+    bias z give the forward, a kept pre-activation z and grad_y = 1 the bias gradient."""
+    n = z.shape[0]
+    stack = e4b.quantize(torch.zeros(1, n, 64, device=DEV), "bf16")
+    zd = dev(z[None], torch.float32)
+    y, pre = e4b.expert_linear(stack, torch.zeros(1, 64, dtype=torch.bfloat16, device=DEV), bias=zd, act=act,
+                               out_dtype=torch.float32, save=True)
+    assert torch.equal(pre, zd)
+    _, gb = e4b.expert_linear_dgrad(stack, torch.ones(1, n, device=DEV), act=act, pre=zd, grad_bias=True)
+    return host(y)[0], host(gb)[0]
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_of_the_largest_values(act):
+    """Far from 0 every activation is z or 0 and its slope 1 or 0, up to the largest finite fp32."""
+    z = np.float32([100.0, 1e6, 1e13, 1.8e19, 1.9e19, 1e20, 1e30, 3.4e38])
+    y, d = _act_values(act, np.concatenate([z, -z]))
+    n = len(z)
+    assert np.array_equal(y[:n], z.astype(np.float64)) and not y[n:].any()
+    assert np.array_equal(d[:n], np.ones(n)) and not d[n:].any()
