@@ -18,17 +18,27 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
   return 1.5957691216057308f * (z + 0.044715f * z * z * z);  // 2 u
 }
 
-// Phi(z) = 0.5 erfc(-z / sqrt 2) by Abramowitz and Stegun 7.1.26 (absolute error
-// 7.5e-8 of Phi): a polynomial in t = 1 / (1 + p |x|) times e^-x^2, x = z / sqrt 2,
-// which the density needs too. The library's erff took 25 us of a 256 x 256
-// tile's epilogue; this takes a sixth of the instructions.
+// Phi(z) = 0.5 erfc(-z / sqrt 2). With x = |z| / sqrt 2, erfc(x) = e^-x^2 t P(t),
+// t = 1 / (1 + 0.33 x): the form of Abramowitz and Stegun 7.1.26 with P of degree 7, fitted
+// here to the least relative error of erfc(x) e^x^2 on 0 <= x <= 9.3 (8.2e-8; 4e-7 in
+// fp32), beyond which e^-x^2 is below the smallest normal fp32. So the tail is
+// right relative to itself (their degree 4 is right to 7.5e-8 of 1: 3 % off at z = -12.5).
+// e^-x^2 gives the density too. The library's erff took 25 us of a 256 x 256 tile's
+// epilogue; P's degree 7 takes no longer than degree 4 (2048 rows of nf4 2048 -> 4096 with
+// GELU and a residual: 52.3 us, 52.9 with degree 4).
 __device__ __forceinline__ float normal_cdf(float z, float &density) {
   const float x = fabsf(z) * 0.7071067811865476f;
   const float e = __expf(-x * x);
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-  const float p =
-      t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-  const float tail = 0.5f * p * e;  // Phi(-|z|)
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.33f * x);
+  float p = -0.135928765f;
+  p = 0.462688088f + t * p;
+  p = -0.355438709f + t * p;
+  p = 0.41254139f + t * p;
+  p = 0.0450107642f + t * p;
+  p = 0.201923788f + t * p;
+  p = 0.182837248f + t * p;
+  p = 0.186366111f + t * p;
+  const float tail = 0.5f * (t * p) * e;  // Phi(-|z|)
   density = e * 0.3989422804014327f;
   return z < 0.0f ? tail : 1.0f - tail;
 }

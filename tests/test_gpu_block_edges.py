@@ -5,6 +5,8 @@ Tolerances as in test_gpu_block: counted in steps U = 2^-24 of fp32 and half ste
 output's type, derived beside each test.
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -128,3 +130,21 @@ def test_activations_of_the_largest_values(act):
     n = len(z)
     assert np.array_equal(y[:n], z.astype(np.float64)) and not y[n:].any()
     assert np.array_equal(d[:n], np.ones(n)) and not d[n:].any()
+
+
+def test_gelu_far_below_zero():
+    """z Phi(z) and its slope to a relative accuracy where they are small: erfc(x) e^(x^2) is fitted to
+    1.4 U and evaluated within 8 (7 multiply-adds of terms that partly cancel, a reciprocal); x = |z| / sqrt 2
+    is off by 2 U, so the exponent -x^2 by 5 x^2 U and its scaling to base 2 by 2 more: 3.5 z^2 U; the
+    exponential, the halving product and z's own add 4. The slope Phi + z phi adds the density's
+    error, the same exponential's, to each of two terms that do not cancel below -2."""
+    z = np.linspace(-12.5, -0.25, 4099).astype(np.float32)
+    y, d = _act_values("gelu", z)
+    zz = z.astype(np.float64)
+    phi = np.array([0.5 * math.erfc(-v / math.sqrt(2.0)) for v in zz])
+    rel = (4 * zz * zz + 24) * U
+    bad = np.abs(y - zz * phi) > rel * np.abs(zz * phi)
+    assert not bad.any(), (zz[bad][0], y[bad][0], (zz * phi)[bad][0])
+    dens = zz * np.exp(-0.5 * zz * zz) / math.sqrt(2.0 * math.pi)
+    bad = np.abs(d - (phi + dens)) > rel * (phi + np.abs(dens))
+    assert not bad.any(), (zz[bad][0], d[bad][0], (phi + dens)[bad][0])
