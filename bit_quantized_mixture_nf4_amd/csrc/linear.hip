@@ -754,14 +754,9 @@ __global__ __launch_bounds__(256) void fill_zero_kernel(float *p, int64_t n) {
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) p[i] = 0.0f;
 }
 
-// row tiles of bm rows, at most: the last one of every expert with rows may be partial
-int64_t tiles_at_most(const LinearPlan &p, const LinearArgs &a, int bm) {
-  return (p.rows + (bm - 1) * (a.E < p.rows ? a.E : p.rows)) / bm;
-}
-
 template <bool NN, int WM>
 hipError_t launch_tiles(LinearArgs a, const LinearPlan &p, int splits, char *ws, hipStream_t s) {
-  const int64_t N = NN ? a.in : a.out, tiles = tiles_at_most(p, a, Tile<WM>::kM) * ((N + kTN - 1) / kTN);
+  const int64_t N = NN ? a.in : a.out, tiles = tiles_at_most(a.E, p.rows, Tile<WM>::kM) * ((N + kTN - 1) / kTN);
   const dim3 grid(uint32_t((tiles * splits + 7) / 8 * 8)), block(Tile<WM>::kThreads);
   a.splits = splits;
   a.part = splits > 1 ? reinterpret_cast<float *>(ws + p.off_split) : nullptr;
@@ -837,7 +832,7 @@ GemmArgs wide_args(const LinearPlan &p, const LinearArgs &a, bool nn) {
   w.E = a.E;
   w.cb = a.cb;
   w.n_tiles = (w.N + kBNWide - 1) / kBNWide;
-  w.grid = uint32_t(tiles_at_most(p, a, kBM) * w.n_tiles);
+  w.grid = uint32_t(tiles_at_most(a.E, p.rows, kBM) * w.n_tiles);
   w.lin = a;
   if (nn) {
     w.C = static_cast<uint16_t *>(a.y);
@@ -857,7 +852,7 @@ hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_
 hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, const int32_t *offsets, int tiles,
                       void *zero_a, int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
   const int bm = a.bm = tiles == TILE_128 ? kLinearM : kBM;
-  const int64_t bound = tiles_at_most(p, a, bm);
+  const int64_t bound = tiles_at_most(a.E, p.rows, bm);
   a.tile_map = offsets || tiles == TILE_256 ? place : nullptr;
   if (!a.tile_map) return hipSuccess;
   // without offsets every row belongs to an expert: nothing to clear

@@ -92,10 +92,13 @@ static int best_tiles(const e4b_stack *st, int64_t rows, int64_t cols, bool wide
   const int64_t n = low * narrow;
   const int64_t t128 = n <= 256 ? 82 : (n + 511) / 512 * 150, ttall = (tall * narrow + 255) / 256 * 115;
   const int64_t t256 = (tall * broad + 255) / 256 * 190;
+  // 512 threads a workgroup: a launch dimension has fewer than 2^32 (many experts' partial
+  // 256-row tiles can pass that where 128-row tiles of 256 threads still fit)
+  const auto fits = [&](int64_t slabs) { return tiles_at_most(st->E, rows, 256) * slabs <= (int64_t(1) << 23) - 8; };
   // (the 256 x 256 tiles address their rows in 32 bits)
   const int64_t longest = (st->out > st->in ? st->out : st->in) + kBK;
-  if (wide && rows * longest < (int64_t(1) << 32) && t256 < t128 && t256 < ttall) return TILE_256;
-  return ttall < t128 ? TILE_TALL : TILE_128;
+  if (wide && rows * longest < (int64_t(1) << 32) && fits(broad) && t256 < t128 && t256 < ttall) return TILE_256;
+  return ttall < t128 && fits(narrow) ? TILE_TALL : TILE_128;
 }
 
 static int forward_tiles(const e4b_stack *st, int64_t rows) {
@@ -135,7 +138,7 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
   if (dtype != E4B_F32 && dtype != E4B_BF16) return E4B_ERR_DTYPE;
   p->rows = rows;
   // every expert may end in a partial tile
-  p->m_bound = (rows + (kLinearM - 1) * (st->E < rows ? st->E : rows)) / kLinearM;
+  p->m_bound = tiles_at_most(st->E, rows, kLinearM);
   p->ldz = (st->out + kBK - 1) / kBK * kBK;
   // the launch grids: 256 threads per tile, and column slabs in grid.y
   const int64_t wide = st->out > st->in ? st->out : st->in;

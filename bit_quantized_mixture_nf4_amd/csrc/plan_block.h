@@ -54,6 +54,10 @@ inline size_t norm_ws_bytes(const NormArgs &a) {
 constexpr int kLinearM = 128;  // rows per tile
 // how a product is tiled: few rows, 128 x 128, 256 x 128, 256 x 256
 enum { TILE_ROWS = 0, TILE_128, TILE_TALL, TILE_256 };
+// row tiles of bm rows, at most: the last one of every expert with rows may be partial
+inline int64_t tiles_at_most(int64_t E, int64_t rows, int64_t bm) {
+  return (rows + (bm - 1) * (E < rows ? E : rows)) / bm;
+}
 struct LinearPlan {
   int fwd_tiles, bwd_tiles;    // of the product, and of its gradient
   int fwd_splits, bwd_splits;  // 128-row tiles: workgroups along k
