@@ -516,8 +516,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs g) {
 
 // A decode step's experts have a row or two each, so the touched weights are the
 // whole cost and each is read once: no row tile is worth filling, and there is
-// no time for a tile map. Workgroup (column group, n-th expert with rows, row
-// slice) takes the expert's rows straight from the offsets, 16 MT at a time. One MFMA 16x16x32
+// no time for a tile map. Workgroup (column group, n-th block of 16 MT rows) finds
+// its expert and rows straight from the offsets. Blocks are counted over every
+// expert, so that a routing that sends most rows to one spreads over the chip as well:
+// 100000 rows of 64 -> 64 on one of 4 experts take 22 us a call, 19 with that expert
+// alone (a fixed 4 row slices to an expert took 1200). One MFMA 16x16x32
 // takes 16 weight rows (the A operand: a lane's D registers are 4 consecutive
 // columns of one row) and 16 of the expert's rows. A lane reads 16 bytes of
 // codes = 32 consecutive k of its weight row, the operands of four MFMAs; the
@@ -537,10 +540,23 @@ constexpr int kRowDepth = 4;
 // of bf16 2048 -> 128: 20.4 us with 1 slice, 6.5 with 8)
 constexpr int64_t kRowWaves = 4096;
 
+// inclusive sums over the wave's lanes: shifts by 1, 2, 4, 8 within a row of 16, then
+// the rows' last lanes to the rows behind
+__device__ __forceinline__ int32_t wave_scan(int32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 template <int SK, int MT>
 __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, const int32_t *__restrict__ offsets,
-                                                                  int32_t rows, int wk) {
-  constexpr int kK = kRowK / MT, kLd = kK + 8;
+                                                                  int32_t rows, int wk, int32_t blocks,
+                                                                  int32_t zeros) {
+  constexpr int kRows = 16 * MT, kK = kRowK / MT, kLd = kK + 8;
   __shared__ __attribute__((aligned(64))) float code[SK == LK_CODE8 ? 256 : 16];
   __shared__ __attribute__((aligned(16))) uint16_t sx[16 * MT * kLd];
   static_assert(8 * MT * 64 * 16 <= sizeof(sx), "the slices' sums fit x's place");
@@ -548,34 +564,12 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
   // uniform over the wave, so that the loops below branch on scalars
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = 8 / wk, slice = wave % wk;
-  int e = offsets ? -1 : 0;
-  int32_t lo = 0, hi = rows;
-  if (offsets) {
-    // blockIdx.y counts the experts that have rows: a workgroup for every expert
-    // spent more on starting the idle ones than the products took
-    int skip = blockIdx.y;
-    for (int e0 = 0; e0 < g.E && e < 0; e0 += 64) {
-      const int i = min(e0 + lane, g.E - 1);
-      int32_t a = offsets[i], b = offsets[i + 1];
-      a = min(max(a, 0), rows);
-      b = min(max(b, 0), rows);
-      uint64_t has = __ballot(e0 + lane < g.E && b > a);
-      const int n = __popcll(has);
-      if (skip < n) {
-        for (; skip > 0; --skip) has &= has - 1;
-        const int at = __ffsll(static_cast<unsigned long long>(has)) - 1;
-        e = e0 + at;
-        lo = __builtin_amdgcn_readlane(a, at);
-        hi = __builtin_amdgcn_readlane(b, at);
-      } else {
-        skip -= n;
-      }
-    }
-  }
-  if (offsets && blockIdx.y == gridDim.y - 1) {  // the rows of no expert
+  const int32_t block = int32_t(blockIdx.z * gridDim.y + blockIdx.y);
+  if (block >= blocks) {  // the rows of no expert
+    const int32_t z = block - blocks;
+    if (z >= zeros) return;
     const int64_t live = clamped_offset(offsets, g.E, g.E, rows), n = int64_t(16 * wn);
-    for (int64_t i = int64_t(blockIdx.z) * kRowThreads + tid; i < (rows - live) * n;
-         i += int64_t(gridDim.z) * kRowThreads) {
+    for (int64_t i = int64_t(z) * kRowThreads + tid; i < (rows - live) * n; i += int64_t(zeros) * kRowThreads) {
       const int64_t c = int64_t(blockIdx.x) * n + i % n, at = (live + i / n) * g.out + c;
       if (c >= g.out) continue;
       if (g.pre) g.pre[at] = 0.0f;
@@ -587,7 +581,29 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
     }
     return;
   }
-  if (e < 0 || lo + int32_t(blockIdx.z) * 16 * MT >= hi) return;
+  int e = 0;
+  int32_t r0 = block * kRows, hi = rows;
+  if (offsets) {
+    e = -1;
+    int32_t skip = block;  // blocks before this one
+    for (int e0 = 0; e0 < g.E && e < 0; e0 += 64) {
+      const int i = min(e0 + lane, g.E - 1);
+      int32_t a = offsets[i], b = offsets[i + 1];
+      a = min(max(a, 0), rows);
+      b = min(max(b, 0), rows);
+      const int32_t n = e0 + lane < g.E && b > a ? (b - a + kRows - 1) / kRows : 0, incl = wave_scan(n);
+      const int32_t total = __builtin_amdgcn_readlane(incl, 63);
+      if (skip < total) {
+        const int at = __ffsll(static_cast<unsigned long long>(__ballot(incl > skip))) - 1;
+        e = e0 + at;
+        r0 = __builtin_amdgcn_readlane(a + (skip - incl + n) * kRows, at);
+        hi = __builtin_amdgcn_readlane(b, at);
+      } else {
+        skip -= total;
+      }
+    }
+    if (e < 0) return;
+  }
 
   const int col0 = (blockIdx.x * wn + wave / wk) * 16;  // the wave's columns
   const int m = lane & 15, grp = lane >> 4;
@@ -600,91 +616,89 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
     load_piece<SK>(g, e, w_row, k < g.in ? k : 0, p);
   };
   fill_codes<SK>(code, g.cb);
-  for (int32_t r0 = lo + blockIdx.z * 16 * MT; r0 < hi; r0 += gridDim.z * 16 * MT) {
-    f32x4 acc[MT];
+  f32x4 acc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int n_rows = min(16 * MT, hi - r0);
-    for (int k0 = 0; k0 < g.in; k0 += kK) {
-      const int len = min(kK, g.in - k0);
-      const int all = (len + kRowStep - 1) / kRowStep;       // steps of the chunk
-      const int mine = (all - slice + wk - 1) / wk;          // this slice's
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int n_rows = min(kRows, hi - r0);
+  for (int k0 = 0; k0 < g.in; k0 += kK) {
+    const int len = min(kK, g.in - k0);
+    const int all = (len + kRowStep - 1) / kRowStep;       // steps of the chunk
+    const int mine = (all - slice + wk - 1) / wk;          // this slice's
 #pragma unroll
-      for (int d = 0; d < kRowDepth; ++d)
-        if (d < mine) load(k0, d, f[d]);
-      __syncthreads();  // the last chunk's x has been read
-      // a half step's second half meets zeros
-      const int per_row = all * (kRowStep / 8);
-      for (int i = tid; i < n_rows * per_row; i += kRowThreads) {
-        const int r = i / per_row, c = (i - r * per_row) * 8;
-        u32x4 v = u32x4{0u, 0u, 0u, 0u};
-        if (c < len) v = *reinterpret_cast<const u32x4 *>(g.A + int64_t(r0 + r) * g.in + k0 + c);
-        *reinterpret_cast<u32x4 *>(sx + r * kLd + c) = v;
+    for (int d = 0; d < kRowDepth; ++d)
+      if (d < mine) load(k0, d, f[d]);
+    __syncthreads();  // the last chunk's x has been read
+    // a half step's second half meets zeros
+    const int per_row = all * (kRowStep / 8);
+    for (int i = tid; i < n_rows * per_row; i += kRowThreads) {
+      const int r = i / per_row, c = (i - r * per_row) * 8;
+      u32x4 v = u32x4{0u, 0u, 0u, 0u};
+      if (c < len) v = *reinterpret_cast<const u32x4 *>(g.A + int64_t(r0 + r) * g.in + k0 + c);
+      *reinterpret_cast<u32x4 *>(sx + r * kLd + c) = v;
+    }
+    // the pieces came in before x: nothing is in flight, which the compiler
+    // cannot know, and without it the loop would wait for its youngest load
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+    auto step = [&](int i, const u32x4 (&w)[4]) {
+      const uint16_t *xs = sx + m * kLd + (slice + i * wk) * kRowStep + grp * 32;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < MT; ++q)
+          acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, w[j]), *reinterpret_cast<const bf16x8 *>(xs + q * 16 * kLd + 8 * j), acc[q],
+              0, 0, 0);
+    };
+    // whole runs of kRowDepth steps without a branch (past the end the loads
+    // repeat the last step), then what is left, which is in the registers
+    int i = 0;
+    for (; i + kRowDepth <= mine; i += kRowDepth)
+#pragma unroll
+      for (int d = 0; d < kRowDepth; ++d) {
+        u32x4 w[4];
+        decode_piece<SK>(f[d], code, w);
+        load(k0, min(i + d + kRowDepth, mine - 1), f[d]);
+        step(i + d, w);
       }
-      // the pieces came in before x: nothing is in flight, which the compiler
-      // cannot know, and without it the loop would wait for its youngest load
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-      __syncthreads();
-      auto step = [&](int i, const u32x4 (&w)[4]) {
-        const uint16_t *xs = sx + m * kLd + (slice + i * wk) * kRowStep + grp * 32;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+    for (int d = 0; d < kRowDepth - 1; ++d)
+      if (i + d < mine) {
+        u32x4 w[4];
+        decode_piece<SK>(f[d], code, w);
+        step(i + d, w);
+      }
+  }
+  if (wk > 1) {
+    float(*part)[MT][64 * 4] = reinterpret_cast<float(*)[MT][64 * 4]>(sx);
+    __syncthreads();
 #pragma unroll
-          for (int q = 0; q < MT; ++q)
-            acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, w[j]), *reinterpret_cast<const bf16x8 *>(xs + q * 16 * kLd + 8 * j), acc[q],
-                0, 0, 0);
-      };
-      // whole runs of kRowDepth steps without a branch (past the end the loads
-      // repeat the last step), then what is left, which is in the registers
-      int i = 0;
-      for (; i + kRowDepth <= mine; i += kRowDepth)
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4 *>(&part[wave][i][lane * 4]) = acc[i];
+    __syncthreads();
+    if (slice == 0)
+      for (int q = 1; q < wk; ++q)
 #pragma unroll
-        for (int d = 0; d < kRowDepth; ++d) {
-          u32x4 w[4];
-          decode_piece<SK>(f[d], code, w);
-          load(k0, min(i + d + kRowDepth, mine - 1), f[d]);
-          step(i + d, w);
+        for (int i = 0; i < MT; ++i) acc[i] += *reinterpret_cast<const f32x4 *>(&part[wave + q][i][lane * 4]);
+  }
+  if (slice == 0) {
+    const int c = col0 + 4 * grp;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int32_t r = r0 + i * 16 + m;
+      if (r >= hi) continue;
+      if (g.out % 4 == 0) {
+        if (c < g.out) {
+          float b[4] = {}, v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+          if (g.bias) load_row<4>(g.bias + int64_t(e) * g.out + c, b);
+          linear_epilogue<4>(g, int64_t(r) * g.out + c, b, v);
         }
+      } else {
 #pragma unroll
-      for (int d = 0; d < kRowDepth - 1; ++d)
-        if (i + d < mine) {
-          u32x4 w[4];
-          decode_piece<SK>(f[d], code, w);
-          step(i + d, w);
-        }
-    }
-    if (wk > 1) {
-      float(*part)[MT][64 * 4] = reinterpret_cast<float(*)[MT][64 * 4]>(sx);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4 *>(&part[wave][i][lane * 4]) = acc[i];
-      __syncthreads();
-      if (slice == 0)
-        for (int q = 1; q < wk; ++q)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i] += *reinterpret_cast<const f32x4 *>(&part[wave + q][i][lane * 4]);
-    }
-    if (slice == 0) {
-      const int c = col0 + 4 * grp;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int32_t r = r0 + i * 16 + m;
-        if (r >= hi) continue;
-        if (g.out % 4 == 0) {
-          if (c < g.out) {
-            float b[4] = {}, v[4] = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
-            if (g.bias) load_row<4>(g.bias + int64_t(e) * g.out + c, b);
-            linear_epilogue<4>(g, int64_t(r) * g.out + c, b, v);
+        for (int q = 0; q < 4; ++q)
+          if (c + q < g.out) {
+            float b[1] = {g.bias ? g.bias[int64_t(e) * g.out + c + q] : 0.0f}, v[1] = {acc[i][q]};
+            linear_epilogue<1>(g, int64_t(r) * g.out + c + q, b, v);
           }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (c + q < g.out) {
-              float b[1] = {g.bias ? g.bias[int64_t(e) * g.out + c + q] : 0.0f}, v[1] = {acc[i][q]};
-              linear_epilogue<1>(g, int64_t(r) * g.out + c + q, b, v);
-            }
-        }
       }
     }
   }
@@ -786,20 +800,20 @@ hipError_t launch_rows_mt(const LinearPlan &p, const LinearArgs &a, const int32_
   int wk = 1;
   while (wk < 8 && 2 * wk <= steps && busy * groups * wk < kRowWaves) wk *= 2;
   const int64_t slabs = (groups + 8 / wk - 1) / (8 / wk);
-  // one expert: its row slices side by side; several: few rows each, unless the
-  // routing sends most of many rows to one
-  const int64_t z = a.E > 1 ? (p.rows > 256 ? 4 : 1) : (p.rows + 16 * MT - 1) / (16 * MT);
-  const dim3 grid(uint32_t(slabs), uint32_t(busy + (offsets ? 1 : 0)), uint32_t(z < 65535 ? z : 65535));
-  const dim3 block(kRowThreads);
-  const int32_t rows = int32_t(p.rows);
+  // blocks of 16 MT rows, at most, and workgroups that clear the rows of no expert
+  const int64_t blocks = tiles_at_most(a.E, p.rows, 16 * MT), zeros = offsets ? (p.rows > 256 ? 4 : 1) : 0;
+  const int64_t y = blocks + zeros < 32768 ? blocks + zeros : 32768;
+  const dim3 grid(uint32_t(slabs), uint32_t(y), uint32_t((blocks + zeros + y - 1) / y));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kRowThreads), 0, s, a, offsets, int32_t(p.rows), wk, int32_t(blocks),
+                       int32_t(zeros));
+  };
   switch (a.cb) {
-    case E4B_CB_BF16: hipLaunchKernelGGL((linear_rows_kernel<LK_BF16, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
-    case E4B_CB_MXFP4: hipLaunchKernelGGL((linear_rows_kernel<LK_MX, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
+    case E4B_CB_BF16: go(linear_rows_kernel<LK_BF16, MT>); break;
+    case E4B_CB_MXFP4: go(linear_rows_kernel<LK_MX, MT>); break;
     case E4B_CB_INT8:
-    case E4B_CB_FP8:
-      hipLaunchKernelGGL((linear_rows_kernel<LK_CODE8, MT>), grid, block, 0, s, a, offsets, rows, wk);
-      break;
-    default: hipLaunchKernelGGL((linear_rows_kernel<LK_ABSMAX, MT>), grid, block, 0, s, a, offsets, rows, wk); break;
+    case E4B_CB_FP8: go(linear_rows_kernel<LK_CODE8, MT>); break;
+    default: go(linear_rows_kernel<LK_ABSMAX, MT>); break;
   }
   return hipGetLastError();
 }

@@ -75,7 +75,8 @@ static int64_t row_tiles(const e4b_stack *st, int64_t rows, int64_t bm) {
 //     routing gives one expert too many rows for a kernel that reads its weights again
 //     for every 16
 //   up to 2^29 products: 4096 -> 4096, 32 rows 14 / 19 / 92, 64 rows 27 / 21 / 94;
-//     2048 -> 2048, 64 rows 15 / 14 / 53; 30000 rows of 128 -> 128 9 / 11 / 17; 4096 rows
+//     2048 -> 2048, 64 rows 15 / 14 / 53; 30000 rows of 128 -> 128 9 / 11 / 17 (a call takes
+//     16 us with one expert and with two); 4096 rows
 //     of 512 -> 512 18 / 13 / 24; 8- and 16-bit weights, which are two and four times the
 //     bytes to read again, up to 2^28: bf16 4096 -> 4096, 16 rows 12.5 / 13 / 76, 32 rows
 //     20 / 14 / 77

@@ -13,7 +13,9 @@ import torch
 
 import bit_quantized_mixture_nf4_amd as e4b
 from gpu_util import DEV, announce
-from test_gpu_block import U, _stack, bits, dev, host
+from oracle import block
+from plan_util import ROWS, T128, T256, TALL, linear_plan
+from test_gpu_block import U, _stack, bits, dev, host, within
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +150,65 @@ def test_gelu_far_below_zero():
     dens = zz * np.exp(-0.5 * zz * zz) / math.sqrt(2.0 * math.pi)
     bad = np.abs(d - (phi + dens)) > rel * (phi + np.abs(dens))
     assert not bad.any(), (zz[bad][0], d[bad][0], (phi + dens)[bad][0])
+
+
+# E, rows, in, out, the expert that takes all but a few rows, the forward's tiles
+SKEWED = [(128, 1024, 256, 128, 77, ROWS), (4, 5000, 64, 96, 2, ROWS), (2, 700, 512, 130, 0, ROWS), (512, 4000, 128, 64, 511, ROWS),
+          (3, 200, 192, 96, 1, ROWS), (16, 600, 1088, 1024, 5, T128), (3, 1900, 448, 2304, 1, TALL), (2, 3500, 192, 4104, 1, T256)]
+
+
+@pytest.mark.parametrize("E,rows,inn,out,hot,tiles", SKEWED)
+def test_one_hot_expert_of_many(E, rows, inn, out, hot, tiles):
+    """Nearly every row on one expert, in every tiling: each element against 64 bits, and rows of no
+    expert as zeros."""
+    announce(f"hot expert {hot} of {E}, rows={rows} {inn} -> {out}")
+    rng = np.random.default_rng(E + rows)
+    R = rows + 7
+    assert linear_plan(E, R, inn, out)[0] == tiles
+    stack, w = _stack(E, out, inn, "nf4", 5)
+    counts = np.zeros(E, dtype=np.int64)
+    counts[(hot + 1) % E] = counts[(hot * 7 + 3) % E] = 3
+    counts[hot] = 0
+    counts[hot] = rows - counts.sum()
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    off = torch.from_numpy(offsets).to(DEV)
+    x = dev(rng.standard_normal((R, inn)), torch.bfloat16)
+    bias = dev(rng.standard_normal((E, out)) * 0.1, torch.float32)
+    y, pre = e4b.expert_linear(stack, x, off, bias, out_dtype=torch.float32, save=True)
+    ref = block.expert_linear(host(x), w, offsets, host(bias))[0]
+    mag = block.expert_linear(np.abs(host(x)), np.abs(w), offsets, np.abs(host(bias)))[0]
+    within(y, ref, mag * (inn + 4) * U, "y")
+    assert torch.equal(y, pre) and not bits(y[rows:]).any()
+    gy = dev(rng.standard_normal((R, out)), torch.bfloat16)
+    gx, gb = e4b.expert_linear_dgrad(stack, gy, offsets=off, grad_bias=True)
+    gyh = host(gy)
+    gyh[rows:] = 0.0
+    gx_ref, gb_ref = block.expert_linear_dgrad(gyh, gyh, w, offsets)
+    within(gx, gx_ref, block.expert_linear_dgrad(np.abs(gyh), gyh, np.abs(w), offsets)[0] * (out + 4) * U, "grad_x")
+    within(gb, gb_ref, block.expert_linear_dgrad(np.abs(gyh), gyh, w, offsets)[1] * (rows + 8) * U, "grad_bias")
+
+
+def test_a_hot_expert_takes_no_longer_than_the_same_rows_alone():
+    """100000 rows of one of four experts spread over the chip as those of a single expert do (19 us;
+    in a fixed number of row slices per expert they took 1200). Ten times is a bound on the spread of
+    the work, not on its speed."""
+    announce("time of a hot expert")
+    rows = 100000
+    x = torch.randn(rows, 64, device=DEV).to(torch.bfloat16)
+    off = torch.tensor([0, 0, rows, rows, rows], dtype=torch.int32, device=DEV)
+    one, four = _stack(1, 64, 64, "nf4", 6)[0], _stack(4, 64, 64, "nf4", 6)[0]
+
+    def time(call):
+        best = float("inf")
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    alone, hot = time(lambda: e4b.expert_linear(one, x)), time(lambda: e4b.expert_linear(four, x, off))
+    assert hot < 10 * alone, (hot, alone)
