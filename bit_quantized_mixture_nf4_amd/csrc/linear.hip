@@ -35,11 +35,27 @@ namespace {
 // Offsets are clamped to [0, rows] and to ascending order, so that no list of
 // offsets leads out of a buffer.
 constexpr int kMapThreads = 1024;
-constexpr int kZeroBlocks = 64;
 
 __device__ __forceinline__ int32_t clamped_offset(const int32_t *offsets, int i, int E, int32_t rows) {
   if (!offsets) return i < E ? 0 : rows;
   return min(max(offsets[i], 0), rows);
+}
+
+// Zeros to bytes from .. to of p (p 16-byte aligned, from and to even), the work of
+// `threads` threads: 16 bytes a store but for the ends.
+__device__ __forceinline__ void clear_bytes(char *p, int64_t from, int64_t to, int64_t thread, int64_t threads) {
+  const int64_t a = min((from + 15) / 16 * 16, to), b = max(to / 16 * 16, a);
+  if (thread < (a - from) / 2) reinterpret_cast<uint16_t *>(p + from)[thread] = 0;
+  if (thread < (to - b) / 2) reinterpret_cast<uint16_t *>(p + b)[thread] = 0;
+  for (int64_t i = a + thread * 16; i < b; i += threads * 16) *reinterpret_cast<u32x4 *>(p + i) = u32x4{0u, 0u, 0u, 0u};
+}
+
+// Workgroups that clear the rows of no expert, of `bytes` at most (the host does not
+// know how many of the rows those are).
+constexpr int64_t kClearBytes = 1 << 16;  // a workgroup's share
+int64_t clear_groups(int64_t bytes, int64_t most) {
+  const int64_t n = (bytes + kClearBytes - 1) / kClearBytes;
+  return n < most ? n : most;
 }
 
 __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__restrict__ offsets, int E,
@@ -48,15 +64,9 @@ __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__
                                                                int64_t row_bytes_a, char *zero_b, int64_t row_bytes_b) {
   if (blockIdx.x > 0) {
     const int64_t live = clamped_offset(offsets, E, E, rows);
-    const int64_t i0 = int64_t(blockIdx.x - 1) * kMapThreads + threadIdx.x;
-    const int64_t step = int64_t(gridDim.x - 1) * kMapThreads;
-    // row lengths are multiples of 2 bytes; the rows' start may be unaligned
-    if (zero_a)
-      for (int64_t i = live * row_bytes_a / 2 + i0; i < rows * row_bytes_a / 2; i += step)
-        reinterpret_cast<uint16_t *>(zero_a)[i] = 0;
-    if (zero_b)
-      for (int64_t i = live * row_bytes_b / 2 + i0; i < rows * row_bytes_b / 2; i += step)
-        reinterpret_cast<uint16_t *>(zero_b)[i] = 0;
+    const int64_t i = int64_t(blockIdx.x - 1) * kMapThreads + threadIdx.x, n = int64_t(gridDim.x - 1) * kMapThreads;
+    if (zero_a) clear_bytes(zero_a, live * row_bytes_a, rows * row_bytes_a, i, n);
+    if (zero_b) clear_bytes(zero_b, live * row_bytes_b, rows * row_bytes_b, i, n);
     return;
   }
   __shared__ int32_t first[kMaxE + 1];  // first tile of each expert
@@ -568,17 +578,12 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
   if (block >= blocks) {  // the rows of no expert
     const int32_t z = block - blocks;
     if (z >= zeros) return;
-    const int64_t live = clamped_offset(offsets, g.E, g.E, rows), n = int64_t(16 * wn);
-    for (int64_t i = int64_t(z) * kRowThreads + tid; i < (rows - live) * n; i += int64_t(zeros) * kRowThreads) {
-      const int64_t c = int64_t(blockIdx.x) * n + i % n, at = (live + i / n) * g.out + c;
-      if (c >= g.out) continue;
-      if (g.pre) g.pre[at] = 0.0f;
-      if (!g.y) continue;
-      if (g.y_f32)
-        static_cast<float *>(g.y)[at] = 0.0f;
-      else
-        static_cast<uint16_t *>(g.y)[at] = 0;
-    }
+    const int64_t from = clamped_offset(offsets, g.E, g.E, rows) * int64_t(g.out), to = rows * int64_t(g.out);
+    const int64_t i = (int64_t(z) * gridDim.x + blockIdx.x) * kRowThreads + tid;
+    const int64_t n = int64_t(zeros) * gridDim.x * kRowThreads;
+    if (g.pre) clear_bytes(reinterpret_cast<char *>(g.pre), from * 4, to * 4, i, n);
+    const int y_bytes = g.y_f32 ? 4 : 2;
+    if (g.y) clear_bytes(static_cast<char *>(g.y), from * y_bytes, to * y_bytes, i, n);
     return;
   }
   int e = 0;
@@ -586,6 +591,9 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
   if (offsets) {
     e = -1;
     int32_t skip = block;  // blocks before this one
+    // (where most rows are no expert's, most workgroups have no block: they do not look through all experts)
+    const int32_t live = clamped_offset(offsets, g.E, g.E, rows);
+    const int32_t most = (live + (kRows - 1) * min(g.E, live)) / kRows;
     for (int e0 = 0; e0 < g.E && e < 0; e0 += 64) {
       const int i = min(e0 + lane, g.E - 1);
       int32_t a = offsets[i], b = offsets[i + 1];
@@ -600,6 +608,7 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
         hi = __builtin_amdgcn_readlane(b, at);
       } else {
         skip -= total;
+        if (block >= most) return;
       }
     }
     if (e < 0) return;
@@ -800,8 +809,10 @@ hipError_t launch_rows_mt(const LinearPlan &p, const LinearArgs &a, const int32_
   int wk = 1;
   while (wk < 8 && 2 * wk <= steps && busy * groups * wk < kRowWaves) wk *= 2;
   const int64_t slabs = (groups + 8 / wk - 1) / (8 / wk);
-  // blocks of 16 MT rows, at most, and workgroups that clear the rows of no expert
-  const int64_t blocks = tiles_at_most(a.E, p.rows, 16 * MT), zeros = offsets ? (p.rows > 256 ? 4 : 1) : 0;
+  // blocks of 16 MT rows, at most, and slab rows of workgroups that clear the rows of no expert
+  const int64_t blocks = tiles_at_most(a.E, p.rows, 16 * MT);
+  const int64_t bytes = p.rows * a.out * ((a.y ? (a.y_f32 ? 4 : 2) : 0) + (a.pre ? 4 : 0));
+  const int64_t zeros = offsets ? (clear_groups(bytes, 1024) + slabs - 1) / slabs : 0;
   const int64_t y = blocks + zeros < 32768 ? blocks + zeros : 32768;
   const dim3 grid(uint32_t(slabs), uint32_t(y), uint32_t((blocks + zeros + y - 1) / y));
   auto go = [&](auto kernel) {
@@ -870,7 +881,8 @@ hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, con
   a.tile_map = offsets || tiles == TILE_256 ? place : nullptr;
   if (!a.tile_map) return hipSuccess;
   // without offsets every row belongs to an expert: nothing to clear
-  const uint32_t grid = offsets && (zero_a || zero_b) ? 1 + kZeroBlocks : 1;
+  const int64_t bytes = p.rows * ((zero_a ? bytes_a : 0) + (zero_b ? bytes_b : 0));
+  const uint32_t grid = 1 + uint32_t(offsets ? clear_groups(bytes, 256) : 0);
   hipLaunchKernelGGL(tile_map_kernel, dim3(grid), dim3(kMapThreads), 0, s, offsets, int(a.E), int32_t(p.rows), bm,
                      const_cast<int32_t *>(a.tile_offsets), const_cast<int4 *>(a.tile_map), bound,
                      static_cast<char *>(zero_a), bytes_a, static_cast<char *>(zero_b), bytes_b);

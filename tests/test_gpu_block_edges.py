@@ -188,6 +188,19 @@ def test_one_hot_expert_of_many(E, rows, inn, out, hot, tiles):
     within(gb, gb_ref, block.expert_linear_dgrad(np.abs(gyh), gyh, w, offsets)[1] * (rows + 8) * U, "grad_bias")
 
 
+def _time(call):
+    best = float("inf")
+    for _ in range(8):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(5):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
 def test_a_hot_expert_takes_no_longer_than_the_same_rows_alone():
     """100000 rows of one of four experts spread over the chip as those of a single expert do (19 us;
     in a fixed number of row slices per expert they took 1200). Ten times is a bound on the spread of
@@ -198,17 +211,50 @@ def test_a_hot_expert_takes_no_longer_than_the_same_rows_alone():
     off = torch.tensor([0, 0, rows, rows, rows], dtype=torch.int32, device=DEV)
     one, four = _stack(1, 64, 64, "nf4", 6)[0], _stack(4, 64, 64, "nf4", 6)[0]
 
-    def time(call):
-        best = float("inf")
-        for _ in range(8):
-            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-            a.record()
-            for _ in range(5):
-                call()
-            b.record()
-            b.synchronize()
-            best = min(best, a.elapsed_time(b))
-        return best
-
-    alone, hot = time(lambda: e4b.expert_linear(one, x)), time(lambda: e4b.expert_linear(four, x, off))
+    alone, hot = _time(lambda: e4b.expert_linear(one, x)), _time(lambda: e4b.expert_linear(four, x, off))
     assert hot < 10 * alone, (hot, alone)
+
+
+# E, rows, those of an expert, in, out, y, the forward's tiles
+TAILS = [(3, 3000, 5, 64, 129, "bf16", ROWS), (1, 500, 0, 64, 64, "bf16", ROWS), (3, 3001, 1, 64, 33, "fp32", ROWS),
+         (2, 700, 9, 1024, 1023, "bf16", T128), (2, 700, 699, 1024, 1024, "fp32", T128), (3, 1907, 11, 448, 2303, "bf16", TALL),
+         (2, 3507, 300, 192, 4104, "bf16", T256)]
+
+
+@pytest.mark.parametrize("E,R,live,inn,out,yt,tiles", TAILS)
+def test_most_rows_of_no_expert(E, R, live, inn, out, yt, tiles):
+    """Every row from offsets[E] on is zeros in y, the pre-activation and grad_x, to the last element
+    and no further; the rows before are those of the same call without them."""
+    announce(f"{R - live} of {R} rows of no expert, {inn} -> {out} {yt}")
+    rng = np.random.default_rng(R)
+    assert linear_plan(E, R, inn, out)[0] == tiles
+    stack, w = _stack(E, out, inn, "nf4", 7)
+    offsets = np.linspace(0, live, E + 1).astype(np.int32)
+    off = torch.from_numpy(offsets).to(DEV)
+    x = dev(rng.standard_normal((R, inn)), torch.bfloat16)
+    x[live:] = float("nan")
+    dtype = {"bf16": torch.bfloat16, "fp32": torch.float32}[yt]
+    big = torch.full((R + 3, out), 7.0, dtype=dtype, device=DEV)
+    y, pre = e4b.expert_linear(stack, x, off, out_dtype=dtype, save=True, out=big[:R])
+    assert not bits(y[live:]).any() and not bits(pre[live:]).any() and big[R:].eq(7.0).all()
+    xh = host(x)
+    xh[live:] = 0.0
+    ref = block.expert_linear(xh, w, offsets)[0]
+    mag = block.expert_linear(np.abs(xh), np.abs(w), offsets)[0]
+    within(y, ref, mag * (inn + 4) * U, "y")
+    gy = dev(rng.standard_normal((R, out)), torch.bfloat16)
+    gy[live:] = float("inf")
+    gx, _ = e4b.expert_linear_dgrad(stack, gy, offsets=off)
+    assert not bits(gx[live:]).any() and (live < 2 or bits(gx[:live]).any())
+
+
+def test_rows_of_no_expert_cost_no_more_than_rows_of_one():
+    """100000 rows of no expert are cleared by the whole chip (four workgroups took 1200 us, the same rows
+    of an expert 19). Ten times is a bound on the spread of the work, not on its speed."""
+    announce("time of rows of no expert")
+    rows = 100100
+    x = torch.randn(rows, 64, device=DEV).to(torch.bfloat16)
+    off = torch.tensor([0, 100], dtype=torch.int32, device=DEV)
+    stack = _stack(1, 64, 64, "nf4", 6)[0]
+    alone, none = _time(lambda: e4b.expert_linear(stack, x)), _time(lambda: e4b.expert_linear(stack, x, off))
+    assert none < 10 * alone, (none, alone)
