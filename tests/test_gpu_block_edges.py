@@ -5,6 +5,7 @@ Tolerances as in test_gpu_block: counted in steps U = 2^-24 of fp32 and half ste
 output's type, derived beside each test.
 """
 
+import functools
 import math
 
 import numpy as np
@@ -258,3 +259,48 @@ def test_rows_of_no_expert_cost_no_more_than_rows_of_one():
     stack = _stack(1, 64, 64, "nf4", 6)[0]
     alone, none = _time(lambda: e4b.expert_linear(stack, x)), _time(lambda: e4b.expert_linear(stack, x, off))
     assert none < 10 * alone, (none, alone)
+
+
+@functools.lru_cache(maxsize=None)
+def _wide_stack(out, inn):
+    return _stack(1, out, inn, "nf4", 8)
+
+
+# rows, the forward's tiles, in, out; the products of 4096 -> 1100 are cut along k
+COUNTS = [(127, T128, 320, 16520), (128, T128, 320, 16520), (129, TALL, 320, 16520), (255, TALL, 320, 16520),
+          (256, TALL, 320, 16520), (257, T128, 320, 16520), (384, T128, 320, 16520), (385, T256, 320, 16520),
+          (511, T256, 320, 16520), (512, T256, 320, 16520), (513, T256, 320, 16520), (127, T128, 4096, 1100),
+          (128, T128, 4096, 1100), (129, T128, 4096, 1100), (256, T128, 4096, 1100), (257, T128, 4096, 1100)]
+
+
+@pytest.mark.parametrize("rows,tiles,inn,out", COUNTS)
+def test_counts_at_which_a_row_tile_begins_or_ends(rows, tiles, inn, out):
+    """Against 64 bits, in the tiles that the count is meant to reach; a row's bits do not depend on
+    where it stands among the rows."""
+    announce(f"{rows} rows of {inn} -> {out}")
+    plan = linear_plan(1, rows, inn, out)
+    assert plan[0] == tiles and (plan[2] > 1) == (inn == 4096)
+    stack, w = _wide_stack(out, inn)
+    x = dev(np.random.default_rng(rows).standard_normal((rows, inn)), torch.bfloat16)
+    y, _ = e4b.expert_linear(stack, x, out_dtype=torch.float32)
+    ref = block.expert_linear(host(x), w)[0]
+    within(y, ref, block.expert_linear(np.abs(host(x)), np.abs(w))[0] * (inn + 4) * U, "y")
+    back, _ = e4b.expert_linear(stack, x.flip(0).contiguous(), out_dtype=torch.float32)
+    assert torch.equal(bits(back.flip(0)), bits(y))
+
+
+@pytest.mark.parametrize("rows,tiles", [(127, T128), (128, T128), (129, TALL), (256, TALL), (257, T128), (384, T128),
+                                        (385, T256), (512, T256), (513, T256)])
+def test_counts_at_which_a_row_tile_of_the_gradient_begins_or_ends(rows, tiles):
+    announce(f"gradient of {rows} rows of 16512 -> 320")
+    assert linear_plan(1, rows, 16512, 320)[1] == tiles
+    stack, w = _wide_stack(320, 16512)
+    gy = dev(np.random.default_rng(rows).standard_normal((rows, 320)), torch.bfloat16)
+    gx, gb = e4b.expert_linear_dgrad(stack, gy, grad_bias=True)
+    gyh = host(gy)
+    ref, gb_ref = block.expert_linear_dgrad(gyh, gyh, w)
+    mag, gb_mag = block.expert_linear_dgrad(np.abs(gyh), gyh, np.abs(w))
+    within(gx, ref, mag * (320 + 4) * U, "grad_x")
+    within(gb, gb_ref, gb_mag * (rows + 8) * U, "grad_bias")
+    back, _ = e4b.expert_linear_dgrad(stack, gy.flip(0).contiguous())
+    assert torch.equal(bits(back.flip(0)), bits(gx))
