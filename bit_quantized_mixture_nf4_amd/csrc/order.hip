@@ -21,6 +21,7 @@ constexpr int kOrderIt = 32;                          // ids per lane and pass
 constexpr int kOrderPass = kOrderThreads * kOrderIt;  // 32768 pairs per pass
 constexpr int kOrderSmall = 4096;                     // pairs that one launch orders and copies
 constexpr int kGatherThreads = 256;
+constexpr int kNarrow = 16;  // threads to a token whose row has no more pieces
 template <int KU>
 constexpr int kUnpermutePieces = KU == 2 ? 2 : 1;
 
@@ -203,17 +204,21 @@ __global__ __launch_bounds__(kGatherThreads) void order_gather_kernel(const int3
 // slab of columns, so that its places and weights are scalars and a row's
 // neighbouring pieces are read together: a wave per token, or per token and 1
 // KB of its row, was slower (8192 x 2 x 4096 bf16: 57 us). KU slots and CU
-// pieces are in flight at a time.
-template <typename T, int VEC, int KU>
+// pieces are in flight at a time. Rows of 16 pieces or fewer leave a workgroup almost
+// empty: TPT = 16 threads take a token then (48482 tokens of 27 x 3 fp32: 26 us, 211
+// with a workgroup each).
+template <typename T, int VEC, int KU, int TPT>
 __global__ __launch_bounds__(kGatherThreads) void unpermute_kernel(const T *__restrict__ rows, int64_t n_tok, int k,
                                                                    int H, int E, const int32_t *__restrict__ offsets,
                                                                    const int32_t *__restrict__ pos,
                                                                    const float *__restrict__ w, T *__restrict__ y) {
-  constexpr int CU = kUnpermutePieces<KU>;
-  constexpr int kPiece = kGatherThreads * VEC;
-  const int64_t t = blockIdx.x;
+  constexpr int CU = TPT == kGatherThreads ? kUnpermutePieces<KU> : 1;
+  constexpr int kPiece = TPT * VEC;
+  const int64_t t = TPT == kGatherThreads ? int64_t(blockIdx.x)
+                                          : int64_t(blockIdx.x) * (kGatherThreads / TPT) + threadIdx.x / TPT;
+  if (TPT < kGatherThreads && t >= n_tok) return;
   const int32_t live = int32_t(min(int64_t(offsets[E]), n_tok * k));  // no place leads out of the rows
-  const int h0 = blockIdx.y * CU * kPiece + threadIdx.x * VEC;
+  const int h0 = blockIdx.y * CU * kPiece + threadIdx.x % TPT * VEC;
   float acc[CU][VEC];
 #pragma unroll
   for (int c = 0; c < CU; ++c)
@@ -246,23 +251,29 @@ __global__ __launch_bounds__(kGatherThreads) void unpermute_kernel(const T *__re
     if (h0 + c * kPiece < H) store_row<VEC>(y + t * H + h0 + c * kPiece, acc[c]);
 }
 
-// The gradients: a wave per token, so that nothing waits at a barrier for the
-// dots (8192 x 2 x 4096 bf16: 65 us; 78 with a workgroup per token).
+// The gradients: a wave per token, so that nothing waits at a barrier for the dots
+// (8192 x 2 x 4096 bf16: 65 us; 78 with a workgroup per token).
 // grad_rows[pos(t, j)] = w[t, j] grad_y[t] and grad_w[t, j] = rows[pos(t, j)] . grad_y[t];
-// grad_y's row is read once per KU slots, each pair's row once. Lanes sum their
-// columns in ascending order, the 64 sums meet in a fixed tree.
-template <typename T, int VEC, int KU>
+// grad_y's row is read once per KU slots, each pair's row once. Fewer than 4096 tokens:
+// a wave to each KU of a token's slots (its `groups`), fewer still: to every slot with 8
+// pieces in flight, since a wave's own turns bound it then (17 tokens of 17 x 2337 fp32
+// 107 us with a wave per token, 11 so; 1 of 32 x 16383 1200 and 25; 4096 tokens of
+// 16 x 2048 read grad_y twice so, 60 against 50). Lanes sum their columns in
+// ascending order, the sums meet in a fixed tree; LPT = 16 lanes take a token where its
+// row has no more pieces (the tree's first two levels would add zeros).
+template <typename T, int VEC, int KU, int CU, int LPT>
 __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
     const T *__restrict__ rows, const T *__restrict__ gy, int64_t n_tok, int k, int H, int E,
     const int32_t *__restrict__ offsets, const int32_t *__restrict__ pos, const float *__restrict__ w,
-    T *__restrict__ grows, float *__restrict__ gw) {
-  constexpr int CU = KU >= 8 ? 1 : 2;
-  const int lane = threadIdx.x & 63;
-  const int64_t t = int64_t(blockIdx.x) * (kGatherThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    T *__restrict__ grows, float *__restrict__ gw, uint32_t groups) {
+  const int lane = threadIdx.x % LPT;
+  const uint32_t item = LPT == 64 ? blockIdx.x * (kGatherThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+                                  : blockIdx.x * (kGatherThreads / LPT) + threadIdx.x / LPT;
+  const int64_t t = item / groups;
   if (t >= n_tok) return;
   const int32_t live = offsets[E];
   const int64_t P = n_tok * k;
-  for (int j0 = 0; j0 < k; j0 += KU) {
+  for (int j0 = int(item % groups) * KU; j0 < k; j0 += int(groups) * KU) {
     int32_t s[KU];
     float wj[KU], dot[KU];
 #pragma unroll
@@ -273,11 +284,11 @@ __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
       wj[j] = s[j] >= live ? 0.0f : w && j0 + j < k ? w[t * k + j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
-    for (int h0 = lane * VEC; h0 < H; h0 += CU * 64 * VEC) {
+    for (int h0 = lane * VEC; h0 < H; h0 += CU * LPT * VEC) {
       float g[CU][VEC], v[KU][CU][VEC];
 #pragma unroll
       for (int c = 0; c < CU; ++c) {
-        const int h = h0 + c * 64 * VEC;
+        const int h = h0 + c * LPT * VEC;
         if (h < H) load_row<VEC>(gy + t * H + h, g[c]);
       }
       if (gw)
@@ -286,7 +297,7 @@ __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
           if (s[j] >= 0 && s[j] < live)
 #pragma unroll
             for (int c = 0; c < CU; ++c) {
-              const int h = h0 + c * 64 * VEC;
+              const int h = h0 + c * LPT * VEC;
               if (h < H) load_row<VEC>(rows + int64_t(s[j]) * H + h, v[j][c]);
             }
 #pragma unroll
@@ -294,7 +305,7 @@ __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
         if (s[j] < 0) continue;
 #pragma unroll
         for (int c = 0; c < CU; ++c) {
-          const int h = h0 + c * 64 * VEC;
+          const int h = h0 + c * LPT * VEC;
           if (h >= H) continue;
           float o[VEC];
 #pragma unroll
@@ -309,7 +320,7 @@ __global__ __launch_bounds__(kGatherThreads) void unpermute_bwd_kernel(
     if (gw)
 #pragma unroll
       for (int j = 0; j < KU; ++j) {
-        const float d = wave_sum(dot[j]);
+        const float d = lanes_sum<LPT>(dot[j]);
         if (lane == 0 && j0 + j < k) gw[t * k + j0 + j] = d;
       }
   }
@@ -330,33 +341,41 @@ hipError_t order_gather(const OrderArgs &a, hipStream_t s) {
 }
 template <typename T, int VEC>
 hipError_t unpermute(const OrderArgs &a, hipStream_t s) {
-  const int piece = kGatherThreads * VEC * (a.k <= 2 ? kUnpermutePieces<2> : 1);
-  const dim3 grid(uint32_t(a.T), uint32_t((a.H + piece - 1) / piece));
+  const bool narrow = a.H <= kNarrow * VEC;  // a token's row in kNarrow threads
+  const int piece = kGatherThreads * VEC * (a.k <= 2 ? kUnpermutePieces<2> : 1), per = kGatherThreads / kNarrow;
+  const dim3 grid = narrow ? dim3(uint32_t((a.T + per - 1) / per)) : dim3(uint32_t(a.T), uint32_t((a.H + piece - 1) / piece));
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(kGatherThreads), 0, s, static_cast<const T *>(a.x), a.T, a.k, a.H, a.E,
                        a.offsets, a.pos, a.w, static_cast<T *>(a.rows));
   };
-  if (a.k <= 2)
-    go(unpermute_kernel<T, VEC, 2>);
+  if (narrow)
+    go(unpermute_kernel<T, VEC, 8, kNarrow>);
+  else if (a.k <= 2)
+    go(unpermute_kernel<T, VEC, 2, kGatherThreads>);
   else if (a.k <= 4)
-    go(unpermute_kernel<T, VEC, 4>);
+    go(unpermute_kernel<T, VEC, 4, kGatherThreads>);
   else
-    go(unpermute_kernel<T, VEC, 8>);
+    go(unpermute_kernel<T, VEC, 8, kGatherThreads>);
   return hipGetLastError();
 }
 template <typename T, int VEC>
 hipError_t unpermute_bwd(const OrderArgs &a, hipStream_t s) {
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(uint32_t((a.T + 3) / 4)), dim3(kGatherThreads), 0, s, static_cast<const T *>(a.x),
-                       static_cast<const T *>(a.gy), a.T, a.k, a.H, a.E, a.offsets, a.pos, a.w,
-                       static_cast<T *>(a.rows), a.gw);
+  auto go = [&](auto kernel, int ku, int lanes) {
+    const int64_t groups = a.T < 4096 ? (a.k + ku - 1) / ku : 1, items = a.T * groups, per = kGatherThreads / lanes;
+    hipLaunchKernelGGL(kernel, dim3(uint32_t((items + per - 1) / per)), dim3(kGatherThreads), 0, s,
+                       static_cast<const T *>(a.x), static_cast<const T *>(a.gy), a.T, a.k, a.H, a.E, a.offsets, a.pos,
+                       a.w, static_cast<T *>(a.rows), a.gw, uint32_t(groups));
   };
-  if (a.k <= 2)
-    go(unpermute_bwd_kernel<T, VEC, 2>);
+  if (a.H <= kNarrow * VEC)
+    go(unpermute_bwd_kernel<T, VEC, 8, 1, kNarrow>, 8, kNarrow);
+  else if (a.T * ((a.k + 7) / 8) < 1024)  // fewer waves than SIMDs
+    go(unpermute_bwd_kernel<T, VEC, 1, 8, 64>, 1, 64);
+  else if (a.k <= 2)
+    go(unpermute_bwd_kernel<T, VEC, 2, 2, 64>, 2, 64);
   else if (a.k <= 4)
-    go(unpermute_bwd_kernel<T, VEC, 4>);
+    go(unpermute_bwd_kernel<T, VEC, 4, 2, 64>, 4, 64);
   else
-    go(unpermute_bwd_kernel<T, VEC, 8>);
+    go(unpermute_bwd_kernel<T, VEC, 8, 1, 64>, 8, 64);
   return hipGetLastError();
 }
 

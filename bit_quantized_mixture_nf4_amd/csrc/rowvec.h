@@ -122,10 +122,13 @@ struct Raw<float, VEC> {
   }
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
+// the sum over each run of L lanes, on all of them
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  for (int o = L / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
 }  // namespace e4b

@@ -304,3 +304,55 @@ def test_counts_at_which_a_row_tile_of_the_gradient_begins_or_ends(rows, tiles):
     within(gb, gb_ref, gb_mag * (rows + 8) * U, "grad_bias")
     back, _ = e4b.expert_linear_dgrad(stack, gy.flip(0).contiguous())
     assert torch.equal(bits(back.flip(0)), bits(gx))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,H", [(1, 32, 16383), (3, 9, 8192), (17, 17, 2337), (130, 8, 640), (1030, 9, 136), (4096, 9, 24),
+                                   (5000, 3, 1), (999, 32, 16), (333, 5, 17), (700, 2, 128), (4097, 17, 8)])
+def test_way_back_of_few_tokens_and_of_narrow_rows(T, k, H, dt):
+    """The gradients against 64 bits however a token's slots are spread over waves, and y."""
+    announce(f"way back T={T} k={k} H={H} {dt}")
+    rng = np.random.default_rng(T + H)
+    ids = rng.integers(-1, 6, (T, k)).astype(np.int32)
+    _, perm = e4b.moe_permute(torch.from_numpy(ids).to(DEV), 6)
+    offsets, pos = perm.offsets.cpu().numpy(), perm.pos.cpu().numpy()
+    live = int(offsets[-1])
+    rows, gy = dev(rng.standard_normal((T * k, H)), dt), dev(rng.standard_normal((T, H)), dt)
+    rows[live:] = float("nan")
+    w = dev(rng.random((T, k)), torch.float32)
+    rh = np.nan_to_num(host(rows))
+    on = pos < live
+    place = np.where(on, pos, 0)
+    at = rh[place] * on[..., None]
+    y = e4b.moe_unpermute(perm, rows, w)
+    within(y, (at * host(w)[..., None]).sum(1), (np.abs(at) * host(w)[..., None]).sum(1) * (k + 1) * U, "y")
+    gr, gw = e4b.moe_unpermute_backward(perm, rows, gy, w)
+    gyh = host(gy)[:, None, :]
+    within(gw, (at * gyh).sum(2), (np.abs(at * gyh)).sum(2) * (H + 2) * U, "grad_w")
+    ref = np.zeros((T * k, H))
+    ref[pos[on]] = (host(w)[..., None] * gyh)[on]
+    within(gr, ref, np.abs(ref) * U, "grad_rows")
+    gr2, _ = e4b.moe_unpermute_backward(perm, None, gy, w, grad_w=False)
+    assert torch.equal(bits(gr2), bits(gr))
+
+
+def test_way_back_spreads_over_the_chip():
+    """A gradient of one token with many slots, and narrow rows of many tokens, against the same pairs as
+    tokens of one slot and as wide rows (1200 us against 12 and 211 against 10 where a wave takes
+    a token and a workgroup a row; 25 and 26 now). Ten times bounds the spread, not the speed."""
+    announce("time of the way back")
+
+    def args(T, k, H):
+        ids = torch.randint(0, 64, (T, k), device=DEV, dtype=torch.int32)
+        return e4b.moe_permute(ids, 64)[1], torch.randn(T * k, H, device=DEV), torch.rand(T, k, device=DEV), torch.randn(T, H, device=DEV)
+
+    def back(T, k, H):
+        p, rows, w, gy = args(T, k, H)
+        return _time(lambda: e4b.moe_unpermute_backward(p, rows, gy, w))
+
+    def forth(T, k, H):
+        p, rows, w, _ = args(T, k, H)
+        return _time(lambda: e4b.moe_unpermute(p, rows, w))
+
+    assert back(1, 32, 16383) < 10 * back(32, 1, 16383)
+    assert forth(48482, 27, 3) < 10 * forth(190, 27, 768)
