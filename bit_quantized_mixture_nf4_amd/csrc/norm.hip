@@ -25,6 +25,8 @@ namespace e4b {
 namespace {
 
 constexpr int kNormThreads = 512;
+constexpr int kLongThreads = 1024;  // norm_bwd_threads of a row beyond 4096 columns
+static_assert(kNormMaxH == 16 * kLongThreads, "16 elements a thread hold the longest row");
 
 // Sum of N values over each group of TPR threads (whole waves), the same on
 // every thread. `red` holds N floats per wave and is free again on return.
@@ -129,15 +131,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
 // v = the factor of dr in the gate / post-norm products (u for a token gate,
 // else s g u), dr = grad_r + rstd_r (c - n m1) gives
 //   sum dr v = sum (grad_r + rstd_r c) v - rstd_r m1 sum n v,   m1 = mean(c n).
-// A workgroup walks rows blockIdx.x R, + gridDim.x R, ... with tpr threads to a
-// row (R = NT / tpr rows at a time) and 8 elements to a thread (16 beyond 8192
-// columns): each thread keeps its columns' weights and its share of the column
-// gradients in registers, and the next rows' pieces, as stored, while it works
-// on these. 32 elements to a thread spilled 150 registers and took 59.6 us at
-// 4096 x 2048 bf16 and 326 us at 8191 x 4096 fp32. At the end the workgroup
-// adds its rows' shares through LDS and writes one partial row;
-// norm_cols_kernel adds those in order. The grid depends on T alone, so results
-// are the same on every run.
+// Rows of up to 4096 columns: a workgroup walks rows blockIdx.x R, + gridDim.x R, ...
+// with tpr threads to a row (R = NT / tpr rows at a time) and 8 elements to a thread:
+// each thread keeps its columns' weights and its share of the column gradients
+// in registers, and the next rows' pieces, as stored, while it works on these. 32
+// elements to a thread spilled 150 registers and took 59.6 us at 4096 x 2048
+// bf16 and 326 us at 8191 x 4096 fp32. At the end the workgroup adds its rows' shares
+// through LDS and writes one partial row; norm_cols_kernel adds those in order. The
+// grid depends on the descriptor alone, so results are the same on every run.
 template <typename X, int NT, int VEC, int C, bool CHANNEL>
 __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
   constexpr int kE = VEC * C;
@@ -278,6 +279,306 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
   if (CHANNEL) put(s_gate, a.part_gate);
 }
 
+// The same for rows beyond 4096 columns: the whole workgroup takes one row, 8 elements to
+// a thread, 16 beyond 8192. A lane of 1024 threads has 128 registers, too few for what
+// the kernel above holds (it spilled up to 473 here, and some calls were slower than
+// elementary operations), so
+//   * the row is kept as stored, and m, n, d are computed from it twice, before and
+//     after the row sums (hide() keeps the compiler from holding them instead);
+//   * column sums that registers have no room for lie in LDS, each column its own
+//     thread's: 8 elements with a channel gate all three, 16 elements two;
+//   * rows are addressed as buffers of their own length, which return zeros and drop
+//     stores past it: no guards, and an offset in place of an address a tensor;
+//   * at 16 elements the weights are read again from L2 for each row and half, and the
+//     next row is not fetched ahead.
+// Forward and backward in us, in parentheses with the kernel above: 1024 x 16384 bf16
+// token gate 102 (202), fp32 channel gate 173 (423), 4096 x 8192 fp32 channel gate 229
+// (331), bf16 token gate 156 (161), 1024 x 16383 fp32 channel gate 227 (733), 13931 x
+// 9634 fp32 without weights 1378 (3319).
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+
+// `n` elements from p as a buffer; without p an empty one
+template <typename T>
+__device__ __forceinline__ buffer_t buffer_of(const T *p, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, p ? n * int(sizeof(T)) : 0, 0x00027000);
+}
+// the VEC elements from h
+template <int VEC>
+__device__ __forceinline__ void buffer_row(buffer_t b, int h, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, h * 4 + 16 * i, 0, 0));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[4 * i + q] = v[q];
+    }
+  } else {
+    f[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, h * 4, 0, 0));
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<float, VEC> &r) {
+  buffer_row<VEC>(b, h, r.v);
+}
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 8> &r) {
+  r.v = __builtin_amdgcn_raw_buffer_load_b128(b, h * 2, 0, 0);
+}
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 1> &r) {
+  r.v = __builtin_amdgcn_raw_buffer_load_b16(b, h * 2, 0, 0);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void buffer_store(buffer_t b, int h, const float (&f)[VEC]) {
+  if constexpr (sizeof(T) == 2 && VEC == 8) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                                 pack_bf16x2(f[6], f[7])},
+                                           b, h * 2, 0, 0);
+  } else if constexpr (sizeof(T) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(f[0]), b, h * 2, 0, 0);
+  } else if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_buffer_store_b128(
+          __builtin_bit_cast(u32x4, f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}), b, h * 4 + 16 * i, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f[0]), b, h * 4, 0, 0);
+  }
+}
+
+// VEC elements of x, y, grad_r and grad_h as stored; single bf16 elements two to a register
+template <typename X, int VEC>
+struct Stored {
+  Raw<X, VEC> x, gr;
+  Raw<bf16_t, VEC> y, gh;
+  __device__ __forceinline__ void fetch(buffer_t bx, buffer_t by, buffer_t br, buffer_t bh, int h) {
+    buffer_fetch(bx, h, x);
+    buffer_fetch(by, h, y);
+    buffer_fetch(br, h, gr);
+    buffer_fetch(bh, h, gh);
+    if constexpr (VEC == 1) {
+      y.v |= gh.v << 16;
+      if constexpr (sizeof(X) == 2) x.v |= gr.v << 16;
+    }
+  }
+  __device__ __forceinline__ void hide() {
+    x.hide();
+    y.hide();
+    if (VEC > 1 || sizeof(X) > 2) gr.hide();
+    if (VEC > 1) gh.hide();
+  }
+  __device__ __forceinline__ void get(float (&fx)[VEC], float (&fy)[VEC], float (&fr)[VEC], float (&fh)[VEC]) const {
+    if constexpr (VEC == 1) {
+      fy[0] = bf16_lo(y.v);
+      fh[0] = bf16_hi(y.v);
+      if constexpr (sizeof(X) == 2) {
+        fx[0] = bf16_lo(x.v);
+        fr[0] = bf16_hi(x.v);
+        return;
+      }
+    } else {
+      y.get(fy);
+      gh.get(fh);
+    }
+    if constexpr (VEC > 1 || sizeof(X) > 2) {
+      x.get(fx);
+      gr.get(fr);
+    }
+  }
+};
+
+// the same value, from which the compiler makes its offsets here and does not hold them
+// from elsewhere
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+template <typename X, int VEC, int C, bool CHANNEL>
+__global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs a) {
+  constexpr int NT = kLongThreads, kE = VEC * C;
+  constexpr bool kAhead = kE <= 8;  // weights held, the next row fetched ahead
+  // where the column sums are: in LDS where that is not one of the two
+  constexpr bool kPreLds = CHANNEL ? kE <= 8 : kE > 8, kPostLds = CHANNEL || kE > 8;
+  __shared__ float red[2][NT / 64][3];
+  __shared__ __attribute__((aligned(16))) float s_gate[CHANNEL ? NT * kE : 1], s_post[kPostLds ? NT * kE : 1],
+      s_pre[kPreLds ? NT * kE : 1];
+  const int th = threadIdx.x, wave = threadIdx.x >> 6, H = a.H;
+  const float inv = 1.0f / float(H);
+  const bool pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  const buffer_t b_post = buffer_of(a.w_post, H), b_pre = buffer_of(a.w_pre, H);
+  const buffer_t b_gate = buffer_of(a.gate_channel, H);
+  struct Weights {
+    float p[VEC], q[VEC], g[VEC];  // post, pre, gate
+  };
+  auto weights = [&](int h, Weights &w) {
+    buffer_row<VEC>(b_post, h, w.p);
+    buffer_row<VEC>(b_pre, h, w.q);
+    if (CHANNEL) buffer_row<VEC>(b_gate, h, w.g);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      w.p[q] = post ? w.p[q] : 1.0f;
+      if (!CHANNEL) w.g[q] = 1.0f;
+    }
+  };
+  Weights held[kAhead ? C : 1];
+  float r_pre[kPreLds ? 1 : C][VEC], r_post[kPostLds ? 1 : C][VEC];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int h = (c * NT + th) * VEC;
+    if constexpr (kAhead) weights(h, held[c]);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      if constexpr (CHANNEL) s_gate[h + q] = 0.0f;
+      if constexpr (kPostLds)
+        s_post[h + q] = 0.0f;
+      else
+        r_post[c][q] = 0.0f;
+      if constexpr (kPreLds)
+        s_pre[h + q] = 0.0f;
+      else
+        r_pre[c][q] = 0.0f;
+    }
+  }
+  struct Row {
+    Stored<X, VEC> e[C];
+    float rs_y, rs_r, gt;
+  };
+  // element t H of a tensor, or nothing
+  auto row_of = [&](const void *p, auto type, int64_t t, bool in) {
+    typedef decltype(type) T;
+    return buffer_of(in && p ? static_cast<const T *>(p) + t * H : static_cast<const T *>(nullptr), H);
+  };
+  auto fetch = [&](int64_t t, Row &f) {
+    const bool on = t < a.T;
+    f.rs_y = post && on ? a.rstd_y[t] : 1.0f;
+    f.rs_r = pre && on ? a.rstd_r[t] : 0.0f;
+    f.gt = !CHANNEL && a.gate_token && on ? a.gate_token[t] : 1.0f;
+    const buffer_t bx = row_of(a.x, X{}, t, on && pre), by = row_of(a.y, bf16_t{}, t, on);
+    const buffer_t br = row_of(a.grad_r, X{}, t, on), bh = row_of(a.grad_h, bf16_t{}, t, on && pre);
+    const int tv = here(th);
+#pragma unroll
+    for (int c = 0; c < C; ++c) f.e[c].fetch(bx, by, br, bh, (c * NT + tv) * VEC);
+  };
+  // (the weights of 4 single elements at a time are on their way, not those of 16)
+  auto apart = [](int c) {
+    if (kE > 8 && VEC == 1 && c % 4 == 3) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  Row cur, nxt;
+  if constexpr (kAhead) fetch(blockIdx.x, nxt);
+  const bool reduce = pre || post || (!CHANNEL && a.grad_gate);  // what needs the row sums
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    if constexpr (kAhead)
+      cur = nxt;
+    else
+      fetch(t, cur);
+    const float rs_y = cur.rs_y, rs_r = cur.rs_r, sg = a.scale * cur.gt;
+    // element q of piece c: m = N(y) (or y), n = N(r), d = grad_r + rstd_r c, v = u or g u, cc = c
+    struct Piece {
+      float m[VEC], n[VEC], d[VEC], v[VEC], cc[VEC], gh[VEC];
+    };
+    auto piece = [&](int c, const Weights &w, Piece &e) {
+      cur.e[c].get(e.n, e.m, e.d, e.gh);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        e.m[q] *= rs_y;
+        e.v[q] = e.m[q] * w.p[q] * (CHANNEL ? w.g[q] : 1.0f);
+        // (without a pre-norm nothing of r reaches a gradient, not even as 0 times an infinity)
+        e.n[q] = pre ? (e.n[q] + sg * e.v[q]) * rs_r : 0.0f;
+        e.cc[q] = e.gh[q] * w.q[q];
+        e.d[q] += rs_r * e.cc[q];
+      }
+    };
+    float sums[3] = {0.0f, 0.0f, 0.0f};
+    int tv = here(th);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * NT + tv) * VEC;
+      Piece e;
+      Weights w;
+      if constexpr (kAhead)
+        w = held[c];
+      else
+        weights(h, w);
+      piece(c, w, e);
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        sums[0] += e.cc[q] * e.n[q];
+        sums[2] += pre ? e.n[q] * e.v[q] : 0.0f;
+        if constexpr (!kPreLds)
+          r_pre[c][q] += e.gh[q] * e.n[q];
+        else
+          s_pre[h + q] += e.gh[q] * e.n[q];
+        sums[1] += e.d[q] * e.v[q];
+      }
+      apart(c);
+    }
+    if constexpr (kAhead) fetch(t + gridDim.x, nxt);
+    if (reduce) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) sums[i] = wave_sum(sums[i]);
+      // two buffers in turn: one barrier orders both the writes and the next turn's
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) red[turn][wave][i] = sums[i];
+      __syncthreads();
+      sums[0] = sums[1] = sums[2] = 0.0f;
+      for (int q = 0; q < NT / 64; ++q)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) sums[i] += red[turn][q][i];
+    }
+    const float m1 = rs_r * sums[0] * inv;    // times n: what dr loses
+    const float dv = sums[1] - m1 * sums[2];  // sum over the row of dr v
+    if (!CHANNEL && a.gate_token && a.grad_gate && th == 0) a.grad_gate[t] = a.scale * dv;
+    const float m2 = post ? sg * dv * inv : 0.0f;  // mean of b m: b m = s g_t (dr v)
+    const buffer_t bx = row_of(a.grad_x, X{}, t, true), by = row_of(a.grad_y, bf16_t{}, t, a.y != nullptr);
+    tv = here(th);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int h = (c * NT + tv) * VEC;
+      cur.e[c].hide();
+      Piece e;
+      Weights w;
+      if constexpr (kAhead)
+        w = held[c];
+      else
+        weights(h, w);
+      piece(c, w, e);
+      float o[VEC];
+#pragma unroll
+      for (int q = 0; q < VEC; ++q) {
+        const float dr = e.d[q] - m1 * e.n[q];
+        const float du = sg * dr * (CHANNEL ? w.g[q] : 1.0f);
+        if constexpr (CHANNEL)
+          s_gate[h + q] += a.scale * dr * (e.m[q] * w.p[q]);
+        if constexpr (!kPostLds)
+          r_post[c][q] += du * e.m[q];
+        else
+          s_post[h + q] += du * e.m[q];
+        e.d[q] = dr;
+        o[q] = post ? rs_y * (du * w.p[q] - e.m[q] * m2) : du;
+      }
+      buffer_store<X, VEC>(bx, h, e.d);
+      buffer_store<bf16_t, VEC>(by, h, o);
+      apart(c);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+      const int h = (c * NT + th) * VEC + q;
+      if (h >= H) continue;
+      const int64_t at = int64_t(blockIdx.x) * H + h;
+      if (a.part_pre) a.part_pre[at] = kPreLds ? s_pre[kPreLds ? h : 0] : r_pre[kPreLds ? 0 : c][q];
+      if (a.part_post) a.part_post[at] = kPostLds ? s_post[kPostLds ? h : 0] : r_post[kPostLds ? 0 : c][q];
+      if constexpr (CHANNEL)
+        if (a.part_gate) a.part_gate[at] = s_gate[h];
+    }
+}
+
 // out[h] = sum over the n partial rows, 16 interleaved runs added in a fixed order.
 __global__ __launch_bounds__(1024) void norm_cols_kernel(const float *__restrict__ p0, const float *__restrict__ p1,
                                                          const float *__restrict__ p2, float *__restrict__ o0,
@@ -334,13 +635,20 @@ hipError_t backward(const NormArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename X, int VEC, int C>
+hipError_t backward_long(const NormArgs &a, hipStream_t s) {
+  if (a.gate_channel)
+    hipLaunchKernelGGL((norm_bwd_long_kernel<X, VEC, C, true>), dim3(uint32_t(a.groups)), dim3(kLongThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_bwd_long_kernel<X, VEC, C, false>), dim3(uint32_t(a.groups)), dim3(kLongThreads), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename X>
 hipError_t backward_by_length(const NormArgs &a, hipStream_t s) {
   if (a.H % 8 == 0)
-    return a.H <= 4096 ? backward<X, 512, 8, 1>(a, s)
-                       : a.H <= 8192 ? backward<X, 1024, 8, 1>(a, s) : backward<X, 1024, 8, 2>(a, s);
-  return a.H <= 4096 ? backward<X, 512, 1, 8>(a, s)
-                     : a.H <= 8192 ? backward<X, 1024, 1, 8>(a, s) : backward<X, 1024, 1, 16>(a, s);
+    return a.H <= 4096 ? backward<X, 512, 8, 1>(a, s) : a.H <= 8192 ? backward_long<X, 8, 1>(a, s) : backward_long<X, 8, 2>(a, s);
+  return a.H <= 4096 ? backward<X, 512, 1, 8>(a, s) : a.H <= 8192 ? backward_long<X, 1, 8>(a, s) : backward_long<X, 1, 16>(a, s);
 }
 
 }  // namespace

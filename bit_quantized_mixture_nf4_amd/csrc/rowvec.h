@@ -81,7 +81,8 @@ __device__ __forceinline__ void store_row(float *p, const float (&f)[VEC]) {
 }
 
 // A piece as it is stored, for rows fetched ahead of their use; zeros when `in`
-// is false.
+// is false. hide() makes it another value to the compiler, which then computes what
+// is made from it again instead of holding that.
 template <typename T, int VEC>
 struct Raw;
 template <>
@@ -91,6 +92,7 @@ struct Raw<bf16_t, 8> {
     v = u32x4{0u, 0u, 0u, 0u};
     if (in) v = *reinterpret_cast<const u32x4 *>(p);
   }
+  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -101,12 +103,13 @@ struct Raw<bf16_t, 8> {
 };
 template <>
 struct Raw<bf16_t, 1> {
-  uint16_t v;
+  uint32_t v;
   __device__ __forceinline__ void fetch(const bf16_t *p, bool in) {
     v = 0;
     if (in) v = p->v;
   }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = bf16_to_f32(v); }
+  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(v)); }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = bf16_to_f32(uint16_t(v)); }
 };
 template <int VEC>
 struct Raw<float, VEC> {
@@ -115,6 +118,10 @@ struct Raw<float, VEC> {
 #pragma unroll
     for (int q = 0; q < VEC; ++q) v[q] = 0.0f;
     if (in) load_row<VEC>(p, v);
+  }
+  __device__ __forceinline__ void hide() {
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) asm volatile("" : "+v"(v[q]));
   }
   __device__ __forceinline__ void get(float (&f)[VEC]) const {
 #pragma unroll

@@ -16,7 +16,7 @@ import bit_quantized_mixture_nf4_amd as e4b
 from gpu_util import DEV, announce
 from oracle import block
 from plan_util import ROWS, T128, T256, TALL, linear_plan
-from test_gpu_block import U, _stack, bits, dev, host, within
+from test_gpu_block import U, _norm_inputs, _stack, bits, dev, host, within
 
 pytestmark = pytest.mark.gpu
 
@@ -356,3 +356,59 @@ def test_way_back_spreads_over_the_chip():
 
     assert back(1, 32, 16383) < 10 * back(32, 1, 16383)
     assert forth(48482, 27, 3) < 10 * forth(190, 27, 768)
+
+
+@pytest.mark.parametrize("H", [4097, 5120, 8191, 8192, 8200, 9634, 12288, 16383, 16384])
+@pytest.mark.parametrize("dt,has_y,post,gate,pre", [("bf16", True, True, "token", True), ("fp32", True, True, "channel", True),
+                                                    ("fp32", True, False, None, False), ("bf16", True, True, "channel", False),
+                                                    ("fp32", False, False, None, True), ("bf16", True, False, "token", False)])
+def test_long_rows(H, dt, has_y, post, gate, pre):
+    """Rows beyond 4096 columns, more of them than workgroups, with guards behind every output: the
+    gradients against differentiation in 64 bits, to the steps that test_block_norm_and_its_gradient
+    derives (H + 24 of a row's sums, four of them; T + 16 of a column's)."""
+    T = 300
+    announce(f"long rows H={H} {dt} y={has_y} post={post} gate={gate} pre={pre}")
+    x, kw, gr, gh = _norm_inputs(T, H, dt, has_y, post, gate, pre)
+    f = e4b.block_norm(x, scale=0.5, **kw)
+    g = e4b.block_norm_backward(f, x, gr, gh, scale=0.5, **kw)
+    leaf = {n: v.double().cpu().requires_grad_(True) for n, v in [("x", x)] + list(kw.items())}
+
+    def rms(v, w):
+        return v * torch.rsqrt(v.square().mean(-1, keepdim=True) + 1e-6) * w
+
+    r = leaf["x"] * 1.0
+    if has_y:
+        u = rms(leaf["y"], leaf["w_post"]) if post else leaf["y"]
+        gv = {"token": lambda: leaf["gate_token"][:, None], "channel": lambda: leaf["gate_channel"], None: lambda: 1.0}[gate]()
+        r = r + 0.5 * gv * u
+    loss = (r * gr.double().cpu()).sum()
+    if pre:
+        loss = loss + (rms(r, leaf["w_pre"]) * gh.double().cpu()).sum()
+    names = list(leaf)
+    ref = dict(zip(names, torch.autograd.grad(loss, [leaf[n] for n in names])))
+    for name, got in (("x", g.grad_x), ("y", g.grad_y), ("w_post", g.grad_w_post), ("w_pre", g.grad_w_pre),
+                      ("gate_" + str(gate), g.grad_gate)):
+        if name not in ref:
+            assert got is None
+            continue
+        want = ref[name].numpy()
+        if name in ("x", "y"):  # each row by its own magnitude (row 1, of zeros, has a far larger gradient)
+            mag = np.sqrt((want ** 2).mean(axis=1, keepdims=True))
+        else:
+            mag = np.sqrt((want ** 2).mean())
+        steps = 4 * (H + 24) + (T + 16 if name in ("w_post", "w_pre", "gate_channel") else 0)
+        within(got, want, 16 * mag * steps * U, name)
+
+
+def test_long_rows_take_no_multiple_of_short_ones():
+    """The gradient of 4 M elements in rows of 16383 against rows of 4096: 5 times is a bound on scratch
+    and idle lanes, not on speed (8 with a kernel that spilled)."""
+    announce("time of long rows")
+
+    def back(T, H):
+        x, kw, gr, gh = _norm_inputs(T, H, "fp32", True, True, "channel", True)
+        f = e4b.block_norm(x, **kw)
+        return _time(lambda: e4b.block_norm_backward(f, x, gr, gh, **kw))
+
+    short, long = back(4096, 4096), back(1024, 16383)
+    assert long < 5 * short, (long, short)
