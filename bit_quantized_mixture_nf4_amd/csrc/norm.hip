@@ -52,25 +52,105 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[N]) {
   }
 }
 
+// Rows addressed as buffers of their own length, which return zeros and drop stores past it.
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+
+// `n` elements from p as a buffer; without p an empty one
+template <typename T>
+__device__ __forceinline__ buffer_t buffer_of(const T *p, int n) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, p ? n * int(sizeof(T)) : 0, 0x00027000);
+}
+// the VEC elements from h
+template <int VEC>
+__device__ __forceinline__ void buffer_row(buffer_t b, int h, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, h * 4 + 16 * i, 0, 0));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f[4 * i + q] = v[q];
+    }
+  } else {
+    f[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, h * 4, 0, 0));
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<float, VEC> &r) {
+  buffer_row<VEC>(b, h, r.v);
+}
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 8> &r) {
+  r.v = __builtin_amdgcn_raw_buffer_load_b128(b, h * 2, 0, 0);
+}
+__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 1> &r) {
+  r.v = __builtin_amdgcn_raw_buffer_load_b16(b, h * 2, 0, 0);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void buffer_store(buffer_t b, int h, const float (&f)[VEC]) {
+  if constexpr (sizeof(T) == 2 && VEC == 8) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                                 pack_bf16x2(f[6], f[7])},
+                                           b, h * 2, 0, 0);
+  } else if constexpr (sizeof(T) == 2) {
+    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(f[0]), b, h * 2, 0, 0);
+  } else if constexpr (VEC == 8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_buffer_store_b128(
+          __builtin_bit_cast(u32x4, f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}), b, h * 4 + 16 * i, 0, 0);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f[0]), b, h * 4, 0, 0);
+  }
+}
+
+// the same value, from which the compiler makes its offsets here and does not hold them
+// from elsewhere
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // One group of TPR threads per row; piece c of a thread is the VEC elements
 // from (c TPR + thread) VEC on, so a wave's accesses are consecutive.
+// Single elements (lengths that no 16-byte access divides), 32 to a thread, come from the
+// rows as buffers, piece by piece as far as the row goes: a guard and an address for
+// each took 141 registers, so one workgroup a CU (10860 x 12358 fp32 without weights
+// 852 us, 492 so; 4096 x 8191 bf16 206 and 98).
 template <typename X, int TPR, int VEC, int C>
 __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
   __shared__ float red[kNormThreads / 64][1];
   constexpr int R = kNormThreads / TPR;
+  constexpr bool kBuffer = VEC == 1 && C > 8;
   const int th = threadIdx.x % TPR;
-  const int64_t t = int64_t(blockIdx.x) * R + threadIdx.x / TPR;
+  const int64_t t = int64_t(blockIdx.x) * R + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const bool on = t < a.T;
   const int64_t row = on ? t * a.H : 0;
+  // a row of a tensor, or nothing; the VEC elements from h of it
+  auto row_of = [&](auto *p) { return buffer_of(on && p ? p + row : p, on ? a.H : 0); };
+  auto load = [&](auto *p, buffer_t b, int h, float(&f)[VEC]) {
+    if constexpr (!kBuffer)
+      load_row<VEC>(p + h, f);
+    else if constexpr (sizeof(*p) == 4)
+      buffer_row<VEC>(b, h, f);
+    else
+      f[0] = bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(b, h * 2, 0, 0));
+  };
+  const X *px = static_cast<const X *>(a.x);
+  const bf16_t *py = static_cast<const bf16_t *>(a.y);
+  X *pr = static_cast<X *>(a.r);
+  bf16_t *ph = static_cast<bf16_t *>(a.h);
+  const buffer_t bx = row_of(px), by = row_of(py), br = row_of(pr), bh = row_of(ph);
+  const buffer_t b_post = buffer_of(a.w_post, a.H), b_pre = buffer_of(a.w_pre, a.H);
+  const buffer_t b_gate = buffer_of(a.gate_channel, a.H);
   float x[C][VEC], y[C][VEC];
+  int tv = kBuffer ? here(th) : th;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int h = (c * TPR + th) * VEC;
+    const int h = (c * TPR + tv) * VEC;
 #pragma unroll
     for (int q = 0; q < VEC; ++q) x[c][q] = y[c][q] = 0.0f;
-    if (on && h < a.H) {
-      load_row<VEC>(static_cast<const X *>(a.x) + row + h, x[c]);
-      if (a.y) load_row<VEC>(static_cast<const bf16_t *>(a.y) + row + h, y[c]);
+    if (kBuffer ? c * TPR < a.H : on && h < a.H) {
+      load(px + row, bx, h, x[c]);
+      if (a.y) load(py + row, by, h, y[c]);
     }
   }
   const float inv = 1.0f / float(a.H);
@@ -88,13 +168,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
       f *= rs;
     }
     if (a.gate_token && on) f *= a.gate_token[t];
+    if (kBuffer) tv = here(th);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + th) * VEC;
-      if (!on || h >= a.H) continue;
+      const int h = (c * TPR + tv) * VEC;
+      if (kBuffer ? c * TPR >= a.H : !on || h >= a.H) continue;
       float w[VEC], g[VEC];
-      if (a.w_post) load_row<VEC>(a.w_post + h, w);
-      if (a.gate_channel) load_row<VEC>(a.gate_channel + h, g);
+      if (a.w_post) load(a.w_post, b_post, h, w);
+      if (a.gate_channel) load(a.gate_channel, b_gate, h, g);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
         float u = f * y[c][q];
@@ -102,7 +183,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
         if (a.gate_channel) u *= g[q];
         x[c][q] += u;
       }
-      store_row<VEC>(static_cast<X *>(a.r) + row + h, x[c]);
+      if constexpr (kBuffer)
+        buffer_store<X, VEC>(br, h, x[c]);
+      else
+        store_row<VEC>(pr + row + h, x[c]);
     }
   }
   if (a.w_pre) {
@@ -114,15 +198,19 @@ __global__ __launch_bounds__(kNormThreads) void norm_fwd_kernel(NormArgs a) {
     row_sums<TPR, 1>(ss, red);
     const float rs = 1.0f / sqrtf(ss[0] * inv + a.eps);
     if (on && th == 0) a.rstd_r[t] = rs;
+    if (kBuffer) tv = here(th);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int h = (c * TPR + th) * VEC;
-      if (!on || h >= a.H) continue;
+      const int h = (c * TPR + tv) * VEC;
+      if (kBuffer ? c * TPR >= a.H : !on || h >= a.H) continue;
       float w[VEC];
-      load_row<VEC>(a.w_pre + h, w);
+      load(a.w_pre, b_pre, h, w);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) w[q] = x[c][q] * rs * w[q];
-      store_row<VEC>(static_cast<bf16_t *>(a.h) + row + h, w);
+      if constexpr (kBuffer)
+        buffer_store<bf16_t, VEC>(bh, h, w);
+      else
+        store_row<VEC>(ph + row + h, w);
     }
   }
 }
@@ -295,55 +383,6 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
 // token gate 102 (202), fp32 channel gate 173 (423), 4096 x 8192 fp32 channel gate 229
 // (331), bf16 token gate 156 (161), 1024 x 16383 fp32 channel gate 227 (733), 13931 x
 // 9634 fp32 without weights 1378 (3319).
-typedef __amdgpu_buffer_rsrc_t buffer_t;
-
-// `n` elements from p as a buffer; without p an empty one
-template <typename T>
-__device__ __forceinline__ buffer_t buffer_of(const T *p, int n) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T *>(p), 0, p ? n * int(sizeof(T)) : 0, 0x00027000);
-}
-// the VEC elements from h
-template <int VEC>
-__device__ __forceinline__ void buffer_row(buffer_t b, int h, float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const f32x4 v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, h * 4 + 16 * i, 0, 0));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) f[4 * i + q] = v[q];
-    }
-  } else {
-    f[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, h * 4, 0, 0));
-  }
-}
-template <int VEC>
-__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<float, VEC> &r) {
-  buffer_row<VEC>(b, h, r.v);
-}
-__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 8> &r) {
-  r.v = __builtin_amdgcn_raw_buffer_load_b128(b, h * 2, 0, 0);
-}
-__device__ __forceinline__ void buffer_fetch(buffer_t b, int h, Raw<bf16_t, 1> &r) {
-  r.v = __builtin_amdgcn_raw_buffer_load_b16(b, h * 2, 0, 0);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void buffer_store(buffer_t b, int h, const float (&f)[VEC]) {
-  if constexpr (sizeof(T) == 2 && VEC == 8) {
-    __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                                 pack_bf16x2(f[6], f[7])},
-                                           b, h * 2, 0, 0);
-  } else if constexpr (sizeof(T) == 2) {
-    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(f[0]), b, h * 2, 0, 0);
-  } else if constexpr (VEC == 8) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_raw_buffer_store_b128(
-          __builtin_bit_cast(u32x4, f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}), b, h * 4 + 16 * i, 0, 0);
-  } else {
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f[0]), b, h * 4, 0, 0);
-  }
-}
-
 // VEC elements of x, y, grad_r and grad_h as stored; single bf16 elements two to a register
 template <typename X, int VEC>
 struct Stored {
@@ -384,13 +423,6 @@ struct Stored {
     }
   }
 };
-
-// the same value, from which the compiler makes its offsets here and does not hold them
-// from elsewhere
-__device__ __forceinline__ int here(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
 
 template <typename X, int VEC, int C, bool CHANNEL>
 __global__ __launch_bounds__(kLongThreads) void norm_bwd_long_kernel(NormArgs a) {

@@ -412,3 +412,16 @@ def test_long_rows_take_no_multiple_of_short_ones():
 
     short, long = back(4096, 4096), back(1024, 16383)
     assert long < 5 * short, (long, short)
+
+
+def test_odd_long_rows_forward_take_no_multiple_of_short_ones():
+    """r = x + y of 74 M elements in rows of 12358 against rows of 4096: 2.4 times bounds the registers that
+    single elements take (2.9 with a guard and an address for each, 1.7 without)."""
+    announce("time of odd long rows, forward")
+
+    def forth(T, H):
+        x, kw, _, _ = _norm_inputs(T, H, "fp32", True, False, None, False)
+        return _time(lambda: e4b.block_norm(x, **kw))
+
+    short, long = forth(18102, 4096), forth(6000, 12358)
+    assert long < 2.4 * short, (long, short)
