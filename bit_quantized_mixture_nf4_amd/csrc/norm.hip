@@ -380,9 +380,8 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs a) {
 //   * at 16 elements the weights are read again from L2 for each row and half, and the
 //     next row is not fetched ahead.
 // Forward and backward in us, in parentheses with the kernel above: 1024 x 16384 bf16
-// token gate 102 (202), fp32 channel gate 173 (423), 4096 x 8192 fp32 channel gate 229
-// (331), bf16 token gate 156 (161), 1024 x 16383 fp32 channel gate 227 (733), 13931 x
-// 9634 fp32 without weights 1378 (3319).
+// token gate 102 (202), fp32 channel gate 175 (423), 4096 x 8192 fp32 channel gate 229
+// (331), bf16 token gate 156 (161), 1024 x 16383 fp32 channel gate 168 (675).
 // VEC elements of x, y, grad_r and grad_h as stored; single bf16 elements two to a register
 template <typename X, int VEC>
 struct Stored {

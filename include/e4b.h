@@ -418,7 +418,7 @@ e4b_status e4b_moe_perm_layout(const e4b_moe_layer *L, int64_t T, int32_t top_k,
  * with a stored stack and an epilogue, and the norms before and after a block.
  * [sdist] Experts4bit.forward takes its routing from outside the module and
  * scales and adds the experts' rows inside it; these calls are for callers who
- * need the pieces (a router that trains, experts with biases or another
+ * need the pieces (gradients through a router, experts with biases or another
  * activation, experts on another rank, dense projections over the same storage
  * modes). They follow the conventions above. All sums, statistics and
  * epilogues are fp32; results are the same on every run. */
@@ -523,8 +523,9 @@ size_t e4b_expert_linear_workspace_bytes(const e4b_stack *st, int64_t rows);
 /* Its gradient, the stack frozen: dz = grad_y act'(z), rounded to bf16 as the
  * product's operand;
  *   grad_x = W[e]^T dz,   grad_bias[e] = sum over e's rows of dz (unrounded)
- * (the residual's gradient is grad_y). act needs z: pre as the forward kept
- * it, or x_bf16 and bias, from which it is computed again, bit for bit.
+ * (the residual's gradient is grad_y; the stack itself gets none). act needs z:
+ * pre as the forward kept it, or x_bf16 and bias, from which it is computed
+ * again, bit for bit.
  * Rows from offsets[E] on get zeros in grad_x; an expert without rows gets a
  * zero bias gradient.
  *   grad_y    : device [rows, out], bf16 or fp32 (gy_dtype)
@@ -567,7 +568,8 @@ typedef struct {
 e4b_status e4b_block_norm(const e4b_norm *n, const void *x, const void *y, void *r, void *h,
                           float *rstd_y, float *rstd_r, hipStream_t stream);
 
-/* Gradients of sum(grad_r r) + sum(grad_h h). r is rebuilt from x and y.
+/* Gradients of sum(grad_r r) + sum(grad_h h). r is rebuilt from x and y; without
+ * w_pre grad_x is grad_r, whatever y holds.
  *   x, y, rstd_y, rstd_r : as in the forward
  *   grad_r      : device [T, H] (dtype), or NULL for zeros (with w_pre only)
  *   grad_h      : device bf16 [T, H], with w_pre
