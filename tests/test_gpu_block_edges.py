@@ -425,3 +425,89 @@ def test_odd_long_rows_forward_take_no_multiple_of_short_ones():
 
     short, long = forth(18102, 4096), forth(6000, 12358)
     assert long < 2.4 * short, (long, short)
+
+
+# products in every tiling (with and without shares of k, foreign rows), forward and gradient
+PRODUCTS = [(4, 90, 0, 256, 192), (1, 300, 0, 2048, 520), (3, 1900, 7, 448, 2304), (2, 3500, 9, 192, 4104), (1, 700, 0, 1024, 2048)]
+
+
+def _product(E, rows, tail, inn, out, seed):
+    rng = np.random.default_rng(seed)
+    R = rows + tail
+    off = torch.linspace(0, rows, E + 1, device=DEV).to(torch.int32) if E > 1 or tail else None
+    return {"off": off, "x": dev(rng.standard_normal((R, inn)), torch.bfloat16),
+            "gy": dev(rng.standard_normal((R, out)), torch.float32), "bias": dev(rng.standard_normal((E, out)), torch.float32)}
+
+
+def _step(stack, s, ws=(None, None)):
+    y, _ = e4b.expert_linear(stack, s["x"], s["off"], s["bias"], "gelu", workspace=ws[0])
+    gx, gb = e4b.expert_linear_dgrad(stack, s["gy"], s["x"], s["off"], s["bias"], "gelu", grad_bias=True, workspace=ws[1])
+    return [y, gx, gb]
+
+
+@pytest.mark.parametrize("E,rows,tail,inn,out", PRODUCTS)
+def test_workspace_contents_do_not_matter(E, rows, tail, inn, out):
+    announce(f"workspaces of NaN, {rows} rows of {inn} -> {out}")
+    stack, _ = _stack(E, out, inn, "nf4", 9)
+    s = _product(E, rows, tail, inn, out, 1)
+    want = _step(stack, s)
+    need = (e4b.expert_linear_workspace_bytes(stack, rows + tail), e4b.expert_linear_dgrad_workspace_bytes(stack, rows + tail, True))
+    ws = [torch.full((n // 4 + 1,), float("nan"), device=DEV) for n in need]
+    for p, q in zip(want, _step(stack, s, ws)):
+        assert torch.equal(bits(p), bits(q))
+
+
+def test_larger_calls_captured_and_replayed():
+    """Every tiling, the order of several passes with rows both ways, and long norms in one graph,
+    replayed on new inputs with eager runs between."""
+    announce("larger calls in a graph")
+    stacks = [_stack(E, out, inn, "nf4", 9)[0] for E, _, _, inn, out in PRODUCTS]
+    norms = [_norm_inputs(300, H, dt, True, True, gate, True) for H, dt, gate in
+             ((8192, "bf16", "token"), (12288, "fp32", "channel"), (4099, "fp32", "token"))]
+    ids = torch.zeros(9000, 4, dtype=torch.int32, device=DEV)
+    rows_in = torch.zeros(9000, 264, dtype=torch.bfloat16, device=DEV)
+    few = torch.zeros(3, 30, dtype=torch.int32, device=DEV)
+    few_in = torch.zeros(3, 1032, dtype=torch.bfloat16, device=DEV)
+    lg = torch.zeros(5000, 300, device=DEV)
+    prods = [_product(*p, 0) for p in PRODUCTS]
+
+    def refresh(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        for t in [s[n] for s in prods for n in ("x", "gy", "bias")] + [rows_in, few_in, lg] + [n[0] for n in norms] + [
+                v for n in norms for v in (n[2], n[3], n[1]["y"])]:
+            t.copy_(torch.randn(t.shape, generator=g, device=DEV))
+        for t in (ids, few):
+            t.copy_(torch.randint(-1, 40, t.shape, generator=g, device=DEV))
+
+    def run():
+        out = [t for stack, s in zip(stacks, prods) for t in _step(stack, s)]
+        for i, x in ((ids, rows_in), (few, few_in)):
+            rows, perm = e4b.moe_permute(i, 40, x)
+            w = torch.full(i.shape, 0.5, device=DEV)
+            out += [rows, perm.offsets, perm.pos, e4b.moe_unpermute(perm, rows, w), *e4b.moe_unpermute_backward(perm, rows, x, w)]
+        idx, w = e4b.moe_route(lg, 7)
+        out += [idx, w, e4b.moe_route_backward(idx, w, w, 300)]
+        for x, kw, gr, gh in norms:
+            f = e4b.block_norm(x, **kw)
+            b = e4b.block_norm_backward(f, x, gr, gh, **kw)
+            out += [f.r, f.h, b.grad_x, b.grad_y, b.grad_gate, b.grad_w_post, b.grad_w_pre]
+        return out
+
+    refresh(0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = run()
+    for rep in range(1, 4):
+        refresh(rep)
+        g.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        for i, (p, q) in enumerate(zip(out, want)):
+            assert torch.equal(p.view(torch.uint8), q.view(torch.uint8)), (rep, i)
