@@ -79,7 +79,7 @@ def activation(act, z):
     if act == "none":
         return z.copy(), np.ones_like(z)
     if act == "relu":
-        return np.maximum(z, 0.0), (z > 0).astype(f64)
+        return np.maximum(z, 0.0), np.where(np.isnan(z), z, z > 0)
     if act == "silu":
         s = 0.5 * (1.0 + np.tanh(0.5 * z))
         return z * s, s + z * s * (1.0 - s)

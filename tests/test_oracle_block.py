@@ -113,3 +113,9 @@ def test_block_norm_gradients_by_differences(has_y, post, gate, pre):
         want = _diff(f, v)
         got = g["grad_gate" if name.startswith("gate") else "grad_" + name]
         np.testing.assert_allclose(got, want, atol=1e-7, err_msg=name)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
+def test_nan_passes_every_activation(act):
+    a, d = block.activation(act, np.array([np.nan, -1.0, 2.0]))
+    assert np.isnan(a[0]) and (act == "none" or np.isnan(d[0])) and np.isfinite(a[1:]).all() and np.isfinite(d[1:]).all()
