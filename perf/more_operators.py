@@ -204,9 +204,10 @@ def _plain_balance(s):
         per_seq = lambda v: v.double().sum(0, keepdim=True)  # noqa: E731
     else:
         seg = torch.searchsorted(cu[1:].contiguous(), torch.arange(T, device=lg.device, dtype=torch.int32), right=True)
-        # long sums in 64 bits
-        member = (seg == torch.arange(S, device=lg.device)[:, None]).double()
-        per_seq = lambda v: member @ v.double()  # noqa: E731
+        # long sums: differences of running ones, in 64 bits, along the side that is contiguous
+        first = cu.to(torch.int64)
+        running = lambda v: torch.nn.functional.pad(v.double().t().contiguous().cumsum(-1), (1, 0))  # noqa: E731
+        per_seq = lambda v: running(v)[..., first].diff(dim=-1).t()  # noqa: E731
     picked = torch.zeros_like(lg).scatter_add_(1, s["idx"].to(torch.int64), used[:, None].expand(T, k).float())
     n, counts, prob = per_seq(used), per_seq(picked), per_seq(p)
     zero = torch.zeros(S, dtype=torch.float64, device=lg.device)
