@@ -70,6 +70,16 @@ __all__ = [
     "block_norm",
     "block_norm_backward",
     "block_norm_workspace_bytes",
+    "Balance",
+    "moe_balance",
+    "moe_balance_backward",
+    "moe_balance_workspace_bytes",
+    "MxRows",
+    "mx4_rows",
+    "mx4_rows_backward",
+    "mx4_values",
+    "mx_linear",
+    "mx_linear_workspace_bytes",
     "E4bError",
 ]
 
@@ -519,6 +529,7 @@ class LayerPrefetcher:
 
 
 from .block import (  # noqa: E402,F401  (block.py uses the helpers above)
+    Balance,
     BlockNorm,
     BlockNormGrads,
     Permutation,
@@ -529,10 +540,21 @@ from .block import (  # noqa: E402,F401  (block.py uses the helpers above)
     expert_linear_dgrad,
     expert_linear_dgrad_workspace_bytes,
     expert_linear_workspace_bytes,
+    moe_balance,
+    moe_balance_backward,
+    moe_balance_workspace_bytes,
     moe_permute,
     moe_permute_backward,
     moe_route,
     moe_route_backward,
     moe_unpermute,
     moe_unpermute_backward,
+)
+from .mx import (  # noqa: E402,F401
+    MxRows,
+    mx4_rows,
+    mx4_rows_backward,
+    mx4_values,
+    mx_linear,
+    mx_linear_workspace_bytes,
 )

@@ -60,6 +60,13 @@ EXPORTS = (
     "e4b_block_norm",
     "e4b_block_norm_backward",
     "e4b_block_norm_workspace_bytes",
+    "e4b_moe_balance",
+    "e4b_moe_balance_workspace_bytes",
+    "e4b_moe_balance_backward",
+    "e4b_mx4_rows",
+    "e4b_mx4_rows_backward",
+    "e4b_mx_linear",
+    "e4b_mx_linear_workspace_bytes",
 )
 
 # bytes of the per-GPU array that e4b_moe_forward_noalloc uses as its workspace
@@ -123,6 +130,17 @@ class E4bNorm(ctypes.Structure):
     ]
 
 
+class E4bBalance(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("E", ctypes.c_int64),
+        ("sequences", ctypes.c_int64),
+        ("top_k", ctypes.c_int32),
+        ("cu_tokens", ctypes.c_void_p),
+        ("token_mask", ctypes.c_void_p),
+    ]
+
+
 class E4bKernelEvents(ctypes.Structure):
     """e4b_kernel_events: start / stop hipEvent_t per kernel id (NULL: not timed)."""
 
@@ -155,7 +173,7 @@ def load():
         )
     lib = ctypes.CDLL(LIB_PATH)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    no = ctypes.POINTER(E4bNorm)
+    no, ba = ctypes.POINTER(E4bNorm), ctypes.POINTER(E4bBalance)
     st, lay, lo = ctypes.POINTER(E4bStack), ctypes.POINTER(E4bLayer), ctypes.POINTER(E4bLora)
     sigs = {
         "e4b_quantize_nf4": (i32, [vp, i64, i64, i64, i32, i32, vp, vp, vp]),
@@ -190,6 +208,13 @@ def load():
         "e4b_block_norm_backward": (
             i32, [no, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "e4b_block_norm_workspace_bytes": (sz, [no]),
+        "e4b_moe_balance": (i32, [ba, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "e4b_moe_balance_workspace_bytes": (sz, [ba]),
+        "e4b_moe_balance_backward": (i32, [ba, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "e4b_mx4_rows": (i32, [vp, i32, i64, i64, i32, vp, vp, vp]),
+        "e4b_mx4_rows_backward": (i32, [vp, i32, vp, i32, i64, i64, vp, vp]),
+        "e4b_mx_linear": (i32, [st, i64, vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp, vp, sz, vp]),
+        "e4b_mx_linear_workspace_bytes": (sz, [st, i64]),
         "e4b_moe_forward_noalloc": (i32, [lay, i64, i32, vp, vp, vp, vp, vp, vp, i32, vp]),
     }
     for name, (res, args) in sigs.items():

@@ -1,6 +1,7 @@
 """What a MoE block needs around its expert MLP: the router with the gradient of
-its logits, tokens into expert order and back, the product of expert rows with a
-stored stack and an epilogue, the norms before and after a block.
+its logits and the losses that keep its experts evenly used, tokens into expert
+order and back, the product of expert rows with a stored stack and an epilogue,
+the norms before and after a block.
 
 Like the rest of the package these functions check torch tensors and marshal
 them into ``libe4b.so``; forwards and gradients are explicit calls. Each runs on
@@ -13,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib, _need, _need_buffer, _vp
-from ._lib import E4bNorm, check, load
+from ._lib import E4bBalance, E4bNorm, check, load
 
 ACTS = {"none": _lib.E4B_ACT_NONE, "relu": _lib.E4B_ACT_RELU, "silu": _lib.E4B_ACT_SILU,
         "gelu": _lib.E4B_ACT_GELU, "gelu_tanh": _lib.E4B_ACT_GELU_TANH}
@@ -110,6 +111,110 @@ def moe_route_backward(topk_idx, topk_w, grad_topk_w, E):
     out = torch.empty(T, max(int(E), 0), dtype=torch.float32, device=dev)
     _run("e4b_route_backward", dev, topk_idx.data_ptr(), topk_w.data_ptr(), grad_topk_w.data_ptr(), T, int(E), k,
          out.data_ptr())
+    return out
+
+
+@dataclass
+class Balance:
+    """``moe_balance``'s results for S sequences: ``counts`` int32 [S, E] (pairs of each
+    expert), ``tokens`` int32 [S] (counted tokens), ``prob`` float32 [S, E] (sums of the
+    router's probabilities), ``loss`` and ``z_loss`` float32 [S], ``lse`` float32 [T]
+    (-inf for a token that is not counted), and the ``top_k`` they were made with."""
+
+    counts: torch.Tensor
+    tokens: torch.Tensor
+    prob: torch.Tensor
+    loss: torch.Tensor
+    z_loss: torch.Tensor
+    lse: torch.Tensor
+    top_k: int
+
+
+def _balance_args(logits, top_k, cu_tokens, token_mask):
+    """(the C descriptor, sequences); what it points to stays the caller's"""
+    _need(logits, "logits", torch.float32)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    dev = logits.device
+    S = 1
+    if cu_tokens is not None:
+        _need(cu_tokens, "cu_tokens", torch.int32, dev)
+        if cu_tokens.dim() != 1 or cu_tokens.shape[0] < 2:
+            raise ValueError("cu_tokens must be [sequences + 1]")
+        S = cu_tokens.shape[0] - 1
+    if token_mask is not None:
+        _need(token_mask, "token_mask", torch.bool, dev, (T,))
+    return E4bBalance(T, E, S, int(top_k), None if cu_tokens is None else cu_tokens.data_ptr(),
+                      None if token_mask is None else token_mask.data_ptr()), S
+
+
+def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=None):
+    """How evenly a router uses its experts, and the losses that keep it even: a ``Balance``.
+
+    ``logits`` float32 [T, E] (entries may be -inf), ``topk_idx`` int32 [T, k] as
+    ``moe_route`` gives them (an id outside [0, E) is no expert's). ``cu_tokens`` int32
+    [S + 1]: sequence s has tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 and losses of its
+    own (None: one sequence of all tokens). ``token_mask`` bool [T], False for tokens that
+    are not counted, as padding; nor are those of no sequence and those with logits of -inf throughout.
+    With N counted tokens and p the softmax of all logits,
+    loss = E / (k N^2) sum_e counts_e prob_e (1 for an even use) and
+    z_loss = 1 / N sum_t (log sum_e exp l_te)^2; both are 0 for a sequence without a token.
+    """
+    _need(logits, "logits", torch.float32)
+    dev = logits.device
+    _need(topk_idx, "topk_idx", torch.int32, dev)
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    b, S = _balance_args(logits, k, cu_tokens, token_mask)
+    T, E = logits.shape
+    if topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must have {T} rows, got {topk_idx.shape[0]}")
+    counts = torch.empty(S, E, dtype=torch.int32, device=dev)
+    tokens = torch.empty(S, dtype=torch.int32, device=dev)
+    prob = torch.empty(S, E, dtype=torch.float32, device=dev)
+    loss = torch.empty(S, dtype=torch.float32, device=dev)
+    z = torch.empty(S, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws, at, nbytes = _workspace(workspace, int(load().e4b_moe_balance_workspace_bytes(ctypes.byref(b))), dev)
+    _run("e4b_moe_balance", dev, ctypes.byref(b), logits.data_ptr(), topk_idx.data_ptr(), counts.data_ptr(),
+         tokens.data_ptr(), prob.data_ptr(), loss.data_ptr(), z.data_ptr(), lse.data_ptr(), at, nbytes)
+    return Balance(counts, tokens, prob, loss, z, lse, k)
+
+
+def moe_balance_workspace_bytes(logits, top_k, cu_tokens=None):
+    """Bytes of ``moe_balance``'s workspace for these arguments."""
+    b, _ = _balance_args(logits, top_k, cu_tokens, None)
+    return int(load().e4b_moe_balance_workspace_bytes(ctypes.byref(b)))
+
+
+def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=None, add=None, out=None):
+    """Gradient [T, E] of the logits of sum(grad_loss loss) + sum(grad_z z_loss), the
+    selection held fixed, plus ``add``.
+
+    ``fwd`` is ``moe_balance``'s result and ``cu_tokens`` its argument; ``grad_loss`` and
+    ``grad_z`` float32 [S] (None: zeros); ``add`` float32 [T, E], as ``moe_route_backward``
+    gives it; ``out`` the result's place, which may be ``add``. Tokens that are not counted
+    get ``add`` alone. With ``fwd.counts`` and ``fwd.tokens`` summed over ranks first, the
+    gradient is that of the loss over all ranks' tokens.
+    """
+    b, S = _balance_args(logits, fwd.top_k, cu_tokens, None)
+    T, E = logits.shape
+    dev = logits.device
+    _need(fwd.counts, "counts", torch.int32, dev, (S, E))
+    _need(fwd.tokens, "tokens", torch.int32, dev, (S,))
+    _need(fwd.lse, "lse", torch.float32, dev, (T,))
+    for t, name, shape in ((grad_loss, "grad_loss", (S,)), (grad_z, "grad_z", (S,)), (add, "add", (T, E)),
+                           (out, "out", (T, E))):
+        if t is not None:
+            _need(t, name, torch.float32, dev, shape)
+    if out is None:
+        out = torch.empty(T, E, dtype=torch.float32, device=dev)
+    elif _overlap(out, logits) or (add is not None and _overlap(out, add) and out.data_ptr() != add.data_ptr()):
+        raise ValueError("out must not overlap logits, nor add unless it is add")
+    _run("e4b_moe_balance_backward", dev, ctypes.byref(b), logits.data_ptr(), fwd.counts.data_ptr(),
+         fwd.tokens.data_ptr(), fwd.lse.data_ptr(), _vp(grad_loss), _vp(grad_z), _vp(add), out.data_ptr())
     return out
 
 

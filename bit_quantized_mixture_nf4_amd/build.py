@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libe4b.so")
 
 SOURCES = ["plan.cpp", "quant.hip", "route.hip", "gemm_wide.hip", "combine.hip", "decode.hip", "lora.hip", "mx.hip",
-           "api.hip", "noalloc.hip", "plan_block.cpp", "order.hip", "norm.hip", "linear.hip"]
+           "api.hip", "noalloc.hip", "plan_block.cpp", "order.hip", "norm.hip", "linear.hip", "balance.hip",
+           "mx4.hip", "mx_linear.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -22,6 +22,7 @@
 #include "gemm_dev.h"
 #include "plan_block.h"
 #include "rowvec.h"
+#include "tiles_dev.h"
 
 namespace e4b {
 
@@ -35,28 +36,6 @@ namespace {
 // Offsets are clamped to [0, rows] and to ascending order, so that no list of
 // offsets leads out of a buffer.
 constexpr int kMapThreads = 1024;
-
-__device__ __forceinline__ int32_t clamped_offset(const int32_t *offsets, int i, int E, int32_t rows) {
-  if (!offsets) return i < E ? 0 : rows;
-  return min(max(offsets[i], 0), rows);
-}
-
-// Zeros to bytes from .. to of p (p 16-byte aligned, from and to even), the work of
-// `threads` threads: 16 bytes a store but for the ends.
-__device__ __forceinline__ void clear_bytes(char *p, int64_t from, int64_t to, int64_t thread, int64_t threads) {
-  const int64_t a = min((from + 15) / 16 * 16, to), b = max(to / 16 * 16, a);
-  if (thread < (a - from) / 2) reinterpret_cast<uint16_t *>(p + from)[thread] = 0;
-  if (thread < (to - b) / 2) reinterpret_cast<uint16_t *>(p + b)[thread] = 0;
-  for (int64_t i = a + thread * 16; i < b; i += threads * 16) *reinterpret_cast<u32x4 *>(p + i) = u32x4{0u, 0u, 0u, 0u};
-}
-
-// Workgroups that clear the rows of no expert, of `bytes` at most (the host does not
-// know how many of the rows those are).
-constexpr int64_t kClearBytes = 1 << 16;  // a workgroup's share
-int64_t clear_groups(int64_t bytes, int64_t most) {
-  const int64_t n = (bytes + kClearBytes - 1) / kClearBytes;
-  return n < most ? n : most;
-}
 
 __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__restrict__ offsets, int E,
                                                                int32_t rows, int bm, int32_t *__restrict__ tile_offsets,
@@ -550,18 +529,6 @@ constexpr int kRowDepth = 4;
 // of bf16 2048 -> 128: 20.4 us with 1 slice, 6.5 with 8)
 constexpr int64_t kRowWaves = 4096;
 
-// inclusive sums over the wave's lanes: shifts by 1, 2, 4, 8 within a row of 16, then
-// the rows' last lanes to the rows behind
-__device__ __forceinline__ int32_t wave_scan(int32_t v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
-
 template <int SK, int MT>
 __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, const int32_t *__restrict__ offsets,
                                                                   int32_t rows, int wk, int32_t blocks,
@@ -586,33 +553,9 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows_kernel(LinearArgs g, 
     if (g.y) clear_bytes(static_cast<char *>(g.y), from * y_bytes, to * y_bytes, i, n);
     return;
   }
-  int e = 0;
-  int32_t r0 = block * kRows, hi = rows;
-  if (offsets) {
-    e = -1;
-    int32_t skip = block;  // blocks before this one
-    // (where most rows are no expert's, most workgroups have no block: they do not look through all experts)
-    const int32_t live = clamped_offset(offsets, g.E, g.E, rows);
-    const int32_t most = (live + (kRows - 1) * min(g.E, live)) / kRows;
-    for (int e0 = 0; e0 < g.E && e < 0; e0 += 64) {
-      const int i = min(e0 + lane, g.E - 1);
-      int32_t a = offsets[i], b = offsets[i + 1];
-      a = min(max(a, 0), rows);
-      b = min(max(b, 0), rows);
-      const int32_t n = e0 + lane < g.E && b > a ? (b - a + kRows - 1) / kRows : 0, incl = wave_scan(n);
-      const int32_t total = __builtin_amdgcn_readlane(incl, 63);
-      if (skip < total) {
-        const int at = __ffsll(static_cast<unsigned long long>(__ballot(incl > skip))) - 1;
-        e = e0 + at;
-        r0 = __builtin_amdgcn_readlane(a + (skip - incl + n) * kRows, at);
-        hi = __builtin_amdgcn_readlane(b, at);
-      } else {
-        skip -= total;
-        if (block >= most) return;
-      }
-    }
-    if (e < 0) return;
-  }
+  int e;
+  int32_t r0, hi;
+  if (!block_of(offsets, g.E, rows, kRows, block, lane, e, r0, hi)) return;
 
   const int col0 = (blockIdx.x * wn + wave / wk) * 16;  // the wave's columns
   const int m = lane & 15, grp = lane >> 4;

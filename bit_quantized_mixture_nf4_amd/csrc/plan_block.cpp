@@ -177,4 +177,51 @@ e4b_status check_route(int64_t T, int64_t E, int32_t top_k) {
   return E4B_OK;
 }
 
+e4b_status plan_balance(const e4b_balance *b, BalanceArgs *a) {
+  *a = BalanceArgs{};
+  if (!b) return E4B_ERR_NULL;
+  const e4b_status s = check_route(b->T, b->E, b->top_k);
+  if (s != E4B_OK) return s;
+  if (b->sequences < 1 || b->sequences > 65536) return E4B_ERR_SHAPE;
+  if (!b->cu_tokens && b->sequences != 1) return E4B_ERR_NULL;
+  if (!aligned16(b->cu_tokens) || !aligned16(b->token_mask)) return E4B_ERR_ALIGN;
+  a->T = b->T;
+  a->E = int32_t(b->E);
+  a->k = b->top_k;
+  a->S = int32_t(b->sequences);
+  a->cu = b->cu_tokens;
+  a->mask = b->token_mask;
+  // two workgroups to a CU where there are tokens for them
+  a->chunk = int32_t((b->T + 511) / 512 + 15) / 16 * 16;
+  if (a->chunk < 16) a->chunk = 16;
+  if (!a->cu && b->T <= kBalanceOne) a->chunk = int32_t(kBalanceOne);
+  a->slots = b->T / a->chunk + a->S;
+  return E4B_OK;
+}
+
+size_t balance_ws_bytes(const BalanceArgs &a) {
+  if (a.T == 0 || (!a.cu && a.T <= kBalanceOne)) return 0;
+  return ((size_t(a.slots) * size_t(a.E) * 8 + 255) / 256 + (size_t(a.slots) * 8 + 255) / 256) * 256;
+}
+
+e4b_status check_mx_rows(int64_t rows, int64_t K) {
+  if (rows < 0 || rows > (int64_t(1) << 30) || K <= 0 || K % kBlock != 0 || K > (int64_t(1) << 20)) return E4B_ERR_SHAPE;
+  // a launch dimension has fewer than 2^32 threads, one for 8 elements
+  if (rows * K >= (int64_t(1) << 35) - 2048) return E4B_ERR_SHAPE;
+  return E4B_OK;
+}
+
+e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool gathered, int32_t act, int32_t dtype,
+                          MxLinearPlan *p) {
+  *p = MxLinearPlan{};
+  // the refusals of the product with bf16 rows, for stacks of this format
+  LinearPlan linear;
+  const e4b_status s = plan_linear(st, rows, act, dtype, &linear);
+  if (s != E4B_OK) return s;
+  if (st->codebook != E4B_CB_MXFP4) return E4B_ERR_CODEBOOK;
+  if (gathered && (top_k < 1 || top_k > kMaxTopK || rows % top_k != 0)) return E4B_ERR_SHAPE;
+  p->rows = rows;
+  return E4B_OK;
+}
+
 }  // namespace e4b

@@ -90,4 +90,42 @@ e4b_status plan_linear(const e4b_stack *st, int64_t rows, int32_t act, int32_t d
 // ---- routing (route.hip) ----
 e4b_status check_route(int64_t T, int64_t E, int32_t top_k);
 
+// ---- balance of a router (balance.hip) ----
+// A sequence's tokens are worked off in chunks. Chunk j of sequence s has slot
+// cu[s] / chunk + s + j: as many slots as chunks at least, told apart without a sum over
+// the sequences before, and fewer than T / chunk + S in all.
+struct BalanceArgs {
+  int64_t T;
+  int32_t E, k, S, chunk;
+  int64_t slots;
+  const int32_t *cu;
+  const uint8_t *mask;
+  const float *logits;
+  const int32_t *idx;
+  int32_t *counts, *tokens;
+  float *prob, *loss, *z, *lse;
+  float *part_prob, *part_z;  // [slots, E], [slots]
+  int32_t *part_counts, *part_tokens;
+  const float *grad_loss, *grad_z, *add;
+  float *grad;
+};
+constexpr int64_t kBalanceOne = 64;  // tokens that one workgroup takes, the result in its own hands
+e4b_status plan_balance(const e4b_balance *b, BalanceArgs *a);
+size_t balance_ws_bytes(const BalanceArgs &a);
+
+// ---- microscaled rows and their product (mx4.hip, mx_linear.hip) ----
+// K a multiple of 64 up to 2^20, rows K below 2^35.
+e4b_status check_mx_rows(int64_t rows, int64_t K);
+struct MxLinearPlan {
+  int64_t rows;
+};
+struct MxLinearArgs {
+  LinearArgs lin;
+  const uint8_t *x, *xs;         // codes [tokens, in / 2], scales [tokens, in / 32]
+  const int32_t *sorted;         // row -> pair, or null: the row itself
+  int32_t top_k, tokens;
+};
+e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool gathered, int32_t act, int32_t dtype,
+                          MxLinearPlan *p);
+
 }  // namespace e4b

@@ -589,6 +589,112 @@ e4b_status e4b_block_norm_backward(const e4b_norm *n, const void *x, const void 
                                    void *ws, size_t ws_bytes, hipStream_t stream);
 size_t e4b_block_norm_workspace_bytes(const e4b_norm *n);
 
+/* ---- Balance of a router ----
+ *
+ * How evenly a router uses its experts, sequence by sequence, and the losses that
+ * keep it even. With lse_t = log sum_e exp l_te and p_te = exp(l_te - lse_t), over
+ * the N_s counted tokens t of sequence s,
+ *   counts_se = pairs (t, j) with topk_idx = e,     prob_se = sum_t p_te,
+ *   loss_s = E / (top_k N_s^2) sum_e counts_se prob_se   (1 for an even use),
+ *   z_loss_s = 1 / N_s sum_t lse_t^2.
+ * A token is counted if token_mask has it, a sequence does, and its logits are not
+ * -inf throughout. A sequence without one has losses of 0. Ids outside [0, E) are
+ * pairs of no expert. */
+typedef struct {
+  int64_t T, E;              /* tokens (fewer than 2^24), experts in [1, 1024] */
+  int64_t sequences;         /* in [1, 65536] */
+  int32_t top_k;             /* in [1, min(E, 32)] */
+  const int32_t *cu_tokens;  /* device int32 [sequences + 1], ascending: sequence s has tokens
+                                cu_tokens[s] .. cu_tokens[s + 1] - 1; those of no sequence are
+                                not counted. NULL for one sequence of all T. Values are not
+                                checked on the host; the kernels clamp them to [0, T]. */
+  const uint8_t *token_mask; /* device [T], 0: a token that is not counted (whatever its logits
+                                hold), or NULL */
+} e4b_balance;
+
+/*   logits   : device fp32 [T, E]; entries may be -inf (probability 0)
+ *   topk_idx : device int32 [T, top_k]
+ *   counts   : device int32 [sequences, E] (written)
+ *   tokens   : device int32 [sequences], N_s (written)
+ *   prob     : device fp32 [sequences, E] (written)
+ *   loss, z_loss : device fp32 [sequences] (written)
+ *   lse      : device fp32 [T] (written; -inf for a token that is not counted)
+ *   ws       : e4b_moe_balance_workspace_bytes() (0 for a few tokens of one sequence, or
+ *              for invalid arguments: then ws may be NULL)
+ * T = 0 writes zeros. Errors: NULL, SHAPE, WORKSPACE, ALIGN, HIP. */
+e4b_status e4b_moe_balance(const e4b_balance *b, const float *logits, const int32_t *topk_idx,
+                           int32_t *counts, int32_t *tokens, float *prob, float *loss,
+                           float *z_loss, float *lse, void *ws, size_t ws_bytes,
+                           hipStream_t stream);
+size_t e4b_moe_balance_workspace_bytes(const e4b_balance *b);
+
+/* Gradient of sum_s (grad_loss_s loss_s + grad_z_s z_loss_s), the selection (the counts)
+ * held fixed:
+ *   grad_logits_te = add_te + grad_loss_s E / (top_k N_s^2) p_te (counts_se - sum_j counts_sj p_tj)
+ *                    + grad_z_s 2 / N_s lse_t p_te
+ * and add_te alone for a token that is not counted.
+ *   b         : as in the forward; token_mask is not read (lse tells)
+ *   counts, tokens, lse : as the forward wrote them; summed over ranks before the
+ *               call, counts and tokens give the gradient of the loss over the tokens of all
+ *   grad_loss, grad_z : device fp32 [sequences], or NULL for zeros
+ *   add       : device fp32 [T, E] (the gradient through the routing weights), or NULL
+ *   grad_logits : device fp32 [T, E] (written whole); may be add itself, in place
+ * Errors: as e4b_moe_balance. */
+e4b_status e4b_moe_balance_backward(const e4b_balance *b, const float *logits, const int32_t *counts,
+                                    const int32_t *tokens, const float *lse, const float *grad_loss,
+                                    const float *grad_z, const float *add, float *grad_logits,
+                                    hipStream_t stream);
+
+/* ---- Rows in microscaled 4-bit floats, and their product with an MXFP4 stack ---- */
+
+/* Rows of activations converted to E2M1 codes with an E8M0 scale for every 32 consecutive
+ * elements, by the rule of e4b_quantize_mxfp4 and in its layout (n rows are a stack of
+ * E = 1, out = n). A block that holds an infinity or a NaN gets the scale 255 (NaN) and
+ * codes of 0: all of it reads as NaN.
+ *   x      : device [rows, K] (dtype), or with `gated` [rows, 2 K] = [g | u], whose
+ *            silu(g) u is converted (as computed without rounding; beyond fp32's range it
+ *            counts as infinite)
+ *   rows   : 0 to 2^30;  K % 64 == 0, at most 2^20;  rows K below 2^35
+ *   codes  : device uint8 [rows, K/2]   (written)
+ *   scales : device uint8 [rows, K/32]  (written)
+ * Errors: NULL, SHAPE, DTYPE, ALIGN, HIP. */
+e4b_status e4b_mx4_rows(const void *x, int32_t dtype, int64_t rows, int64_t K, int32_t gated,
+                        uint8_t *codes, uint8_t *scales, hipStream_t stream);
+
+/* Gradient of the gated rows, straight through their rounding: of [g | u] from that of
+ * silu(g) u. (Rows that are not gated pass their gradient on.)
+ *   x      : device [rows, 2 K] (dtype)
+ *   grad   : device [rows, K], bf16 or fp32 (grad_dtype)
+ *   grad_x : device [rows, 2 K] (dtype)  (written; must not overlap x or grad)
+ * Errors: as e4b_mx4_rows. */
+e4b_status e4b_mx4_rows_backward(const void *x, int32_t dtype, const void *grad, int32_t grad_dtype,
+                                 int64_t rows, int64_t K, void *grad_x, hipStream_t stream);
+
+/* Product of microscaled rows with a stored MXFP4 stack: for a row r of expert e
+ * (offsets[e] <= r < offsets[e + 1]),
+ *   z = W[e] x_row(r) + bias[e],   y_r = act(z) + residual_r
+ * on gfx950's block-scaled MFMA, both operands as they are stored, with fp32 accumulation. row(r) is r,
+ * or with an expert order (sorted_pair, as e4b_permute writes it) the token
+ * sorted_pair[r] / top_k, so that tokens are not copied into expert order first. Rows
+ * from offsets[E] on belong to no expert: y and pre are zeros there.
+ * The gradient of x, its rounding passed straight through, and that of bias are
+ * e4b_expert_linear_dgrad's, with pre as kept here (in expert order:
+ * e4b_unpermute without weights adds up a token's).
+ *   st          : codebook E4B_CB_MXFP4 (CODEBOOK otherwise); sizes, rows, offsets, bias, act,
+ *                 residual, y and pre as in e4b_expert_linear
+ *   sorted_pair : device int32 [rows] or NULL; top_k in [1, 32] is read only with it, and then
+ *                 divides rows. Values are clamped to the rows of x.
+ *   x_codes     : device uint8 [rows, in/2] (with sorted_pair [rows / top_k, in/2])
+ *   x_scales    : device uint8 [rows, in/32] (or [rows / top_k, in/32])
+ *   ws          : e4b_mx_linear_workspace_bytes() (NULL is enough for 0)
+ * Errors: NULL, SHAPE, BLOCKSIZE, CODEBOOK, ACT, DTYPE, WORKSPACE, ALIGN, HIP. */
+e4b_status e4b_mx_linear(const e4b_stack *st, int64_t rows, const int32_t *offsets,
+                         const int32_t *sorted_pair, int32_t top_k, const uint8_t *x_codes,
+                         const uint8_t *x_scales, const float *bias, int32_t act,
+                         const void *residual_bf16, int32_t y_dtype, void *y, float *pre, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
+size_t e4b_mx_linear_workspace_bytes(const e4b_stack *st, int64_t rows);
+
 /* Static, human-readable text for a status code. */
 const char *e4b_status_string(e4b_status status);
 

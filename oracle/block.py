@@ -24,6 +24,64 @@ def route_backward(idx, w, grad_w, E):
     return out
 
 
+def balance(logits, idx, cu=None, mask=None):
+    """How evenly a router uses its experts, sequence by sequence: dict of counts [S, E],
+    tokens [S], prob [S, E], loss [S], z [S] and lse [T] (-inf for a token not counted)."""
+    lg, idx = np.asarray(logits, f64), np.asarray(idx)
+    T, E = lg.shape
+    k = idx.shape[1]
+    cu = [0, T] if cu is None else [min(max(int(c), 0), T) for c in cu]
+    S = len(cu) - 1
+    counts, tokens, prob = np.zeros((S, E), np.int64), np.zeros(S, np.int64), np.zeros((S, E))
+    zsum, lse, loss = np.zeros(S), np.full(T, -np.inf), np.zeros(S)
+    for s in range(S):
+        for t in range(cu[s], cu[s + 1]):
+            if (mask is not None and not mask[t]) or np.all(lg[t] == -np.inf):
+                continue
+            top = lg[t].max()
+            z = np.exp(lg[t] - top)
+            lse[t] = top + np.log(z.sum())
+            prob[s] += z / z.sum()
+            zsum[s] += lse[t] ** 2
+            tokens[s] += 1
+            for e in idx[t]:
+                if 0 <= e < E:
+                    counts[s, e] += 1
+        if tokens[s]:
+            loss[s] = E / (k * float(tokens[s]) ** 2) * (counts[s] * prob[s]).sum()
+            zsum[s] /= tokens[s]
+    return {"counts": counts, "tokens": tokens, "prob": prob, "loss": loss, "z": zsum, "lse": lse}
+
+
+def balance_backward(fwd, logits, k, grad_loss=None, grad_z=None, cu=None, add=None):
+    """d(sum(grad_loss loss) + sum(grad_z z)) / d logits, the counts fixed, plus add."""
+    lg = np.asarray(logits, f64)
+    T, E = lg.shape
+    cu = [0, T] if cu is None else [min(max(int(c), 0), T) for c in cu]
+    out = np.zeros((T, E)) if add is None else np.asarray(add, f64).copy()
+    for s in range(len(cu) - 1):
+        for t in range(cu[s], cu[s + 1]):
+            if fwd["lse"][t] == -np.inf:
+                continue
+            N, c = float(fwd["tokens"][s]), np.asarray(fwd["counts"][s], f64)
+            z = np.exp(lg[t] - lg[t].max())
+            p = z / z.sum()
+            if grad_loss is not None:
+                out[t] += float(grad_loss[s]) * E / (k * N * N) * p * (c - (c * p).sum())
+            if grad_z is not None:
+                out[t] += float(grad_z[s]) * 2.0 / N * fwd["lse"][t] * p
+    return out
+
+
+def swiglu(x):
+    """silu(g) u of rows [g | u], and its derivatives by g and by u."""
+    x = np.asarray(x, f64)
+    g, u = np.split(x, 2, axis=1)
+    e = np.exp(-np.abs(g))
+    s, r = np.where(g < 0, e, 1.0) / (1.0 + e), np.where(g < 0, 1.0, e) / (1.0 + e)  # sigmoid, 1 - sigmoid
+    return g * s * u, s * (1.0 + g * r) * u, g * s
+
+
 def expert_order(idx, E):
     """(offsets [E + 1], sorted_pair [P], pos [T, k]): pairs by expert id, stable; pairs
     whose id lies outside [0, E) last."""

@@ -147,6 +147,34 @@ def dequantize_mx(packed, scales, out, inn):
     return f32.reshape(E, out, inn)
 
 
+def quantize_mx_rows(v):
+    """MXFP4 conversion of float64 rows ``[n, K]``: ``(codes uint8 [n, K/2], scales uint8
+    [n, K/32])``. The rule of ``quantize_mx``; a block that holds an infinity or a NaN takes
+    the scale 255 (NaN) and codes of 0."""
+    v = np.asarray(v, dtype=np.float64)
+    n, K = v.shape
+    if K % MX_BLOCK:
+        raise ValueError("row length must be divisible by 32")
+    b = v.reshape(n, K // MX_BLOCK, MX_BLOCK)
+    live = np.isfinite(b).all(axis=2)
+    b = np.where(live[..., None], b, 0.0)
+    sh = shared_exponent(np.abs(b).max(axis=2))
+    q = round_e2m1_magnitude(np.abs(np.ldexp(b, -sh[..., None]))) + 8 * np.signbit(b)
+    q = np.where(live[..., None], q, 0).reshape(n, K)
+    codes = ((q[:, 0::2] << 4) | q[:, 1::2]).astype(np.uint8)
+    return codes, np.where(live, sh + 127, 255).astype(np.uint8)
+
+
+def mx_rows_values(codes, scales):
+    """float64 ``[n, K]`` of MXFP4 rows; a scale of 255 makes its block NaN."""
+    codes, scales = np.asarray(codes, dtype=np.int64), np.asarray(scales, dtype=np.int64)
+    n = codes.shape[0]
+    q = np.empty((n, codes.shape[1] * 2), dtype=np.int64)
+    q[:, 0::2], q[:, 1::2] = codes >> 4, codes & 15
+    s = np.where(scales == 255, np.nan, np.ldexp(1.0, np.minimum(scales, 254) - 127))
+    return e2m1_value(q) * np.repeat(s, MX_BLOCK, axis=1)
+
+
 def mx_value_exact(code, s):
     """Reference value of one element by Python float arithmetic (exact)."""
     mag = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0][code & 7]
