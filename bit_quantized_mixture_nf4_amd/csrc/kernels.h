@@ -153,6 +153,11 @@ hipError_t launch_combine_dgrad(const uint16_t *rows, const int32_t *pos_of_pair
 // (quant.hip).
 hipError_t launch_dequantize8(const e4b_stack &st, bool bf16, void *out, hipStream_t s);
 
+// The row tiles of bm rows of every expert, into a.tile_offsets and a.tile_map (linear.hip), and zeros
+// to the rows of up to two outputs (bytes a row) that no expert has.
+hipError_t launch_tile_map(const int32_t *offsets, int E, int64_t rows, int bm, const LinearArgs &a, void *zero_a,
+                           int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s);
+
 // The decode forward for T <= 8 (decode.hip): two launches, gate_up (routing
 // when logits is not null, grouping, GEMV, SiLU*up) and down (GEMV and the
 // weighted combine). With logits null the ids and weights in idx / w are

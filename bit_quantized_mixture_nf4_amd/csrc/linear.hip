@@ -90,16 +90,6 @@ __global__ __launch_bounds__(kMapThreads) void tile_map_kernel(const int32_t *__
   }
 }
 
-// The tiles of a call: the map's, or without offsets simply the rows in turn
-// (no map is made then: its launch took 4.7 us of a 2048 x 2048 -> 4096 product's 61).
-__device__ __forceinline__ int tile_count(const LinearArgs &g, int bm) {
-  return g.tile_map ? g.tile_offsets[g.E] : int((g.rows + bm - 1) / bm);
-}
-__device__ __forceinline__ int4 tile_of(const LinearArgs &g, int t, int bm) {
-  if (g.tile_map) return g.tile_map[t];
-  return int4{0, 0, t * bm, int(min(int64_t(bm), g.rows - int64_t(t) * bm))};
-}
-
 // ---- the tiled product ----
 
 // 128 rows x 128 columns x 64: 4 waves of 64 x 64 (2 x 2 MFMA 32x32x16 bf16),
@@ -247,22 +237,10 @@ __global__ __launch_bounds__(Tile<WM>::kThreads, WM == 2 ? 2 : 1) void linear_ti
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 
-  // real tiles, one share of k after the other, split evenly over the 8 XCDs (block b
-  // runs on XCD b % 8), in groups of 1024 rows so that an XCD's L2 sees both operands
-  // again; the workgroups without a tile come last
-  const int n_mt = tile_count(g, kM);
   const int N = NN ? g.in : g.out;
-  const uint32_t n_nt = uint32_t((N + kTN - 1) / kTN), W = uint32_t(n_mt) * n_nt;
-  const uint32_t per = (W * g.splits + 7) / 8, xi = blockIdx.x / 8;
-  uint32_t L = (blockIdx.x % 8) * per + xi;
-  if (xi >= per || L >= W * g.splits) return;
-  const int share = int(L / W);
-  L -= share * W;
-  constexpr uint32_t kGroup = 16 / WM;
-  const uint32_t grp = L / (kGroup * n_nt), rem = L % (kGroup * n_nt), m0 = grp * kGroup;
-  const uint32_t gm = min(kGroup, uint32_t(n_mt) - m0);
-  const int nt = int(rem / gm);
-  const int4 tm = tile_of(g, int(m0 + rem % gm), kM);
+  int mt, nt, share;
+  if (!place_of(tile_count(g, kM), (N + kTN - 1) / kTN, g.splits, 16 / WM, mt, nt, share)) return;
+  const int4 tm = tile_of(g, mt, kM);
   const int64_t e = tm.x, row0 = int64_t(tm.y) + tm.z;
   const int valid = tm.w;
 
@@ -816,20 +794,28 @@ hipError_t launch_forward(const LinearPlan &p, const LinearArgs &a, const int32_
   return launch_grouped_gemm(GEMM_LINEAR, wide_args(p, a, false), s);
 }
 
+}  // namespace
+
+hipError_t launch_tile_map(const int32_t *offsets, int E, int64_t rows, int bm, const LinearArgs &a, void *zero_a,
+                           int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
+  // without offsets every row belongs to an expert: nothing to clear
+  const int64_t bytes = rows * ((zero_a ? bytes_a : 0) + (zero_b ? bytes_b : 0));
+  const uint32_t grid = 1 + uint32_t(offsets ? clear_groups(bytes, 256) : 0);
+  hipLaunchKernelGGL(tile_map_kernel, dim3(grid), dim3(kMapThreads), 0, s, offsets, E, int32_t(rows), bm,
+                     const_cast<int32_t *>(a.tile_offsets), const_cast<int4 *>(a.tile_map), tiles_at_most(E, rows, bm),
+                     static_cast<char *>(zero_a), bytes_a, static_cast<char *>(zero_b), bytes_b);
+  return hipGetLastError();
+}
+
+namespace {
+
 // Makes the map for a kind of tiles where they need one, in `a`'s place for it.
 hipError_t launch_map(const LinearPlan &p, LinearArgs &a, const int4 *place, const int32_t *offsets, int tiles,
                       void *zero_a, int64_t bytes_a, void *zero_b, int64_t bytes_b, hipStream_t s) {
   const int bm = a.bm = tiles == TILE_128 ? kLinearM : kBM;
-  const int64_t bound = tiles_at_most(a.E, p.rows, bm);
   a.tile_map = offsets || tiles == TILE_256 ? place : nullptr;
   if (!a.tile_map) return hipSuccess;
-  // without offsets every row belongs to an expert: nothing to clear
-  const int64_t bytes = p.rows * ((zero_a ? bytes_a : 0) + (zero_b ? bytes_b : 0));
-  const uint32_t grid = 1 + uint32_t(offsets ? clear_groups(bytes, 256) : 0);
-  hipLaunchKernelGGL(tile_map_kernel, dim3(grid), dim3(kMapThreads), 0, s, offsets, int(a.E), int32_t(p.rows), bm,
-                     const_cast<int32_t *>(a.tile_offsets), const_cast<int4 *>(a.tile_map), bound,
-                     static_cast<char *>(zero_a), bytes_a, static_cast<char *>(zero_b), bytes_b);
-  return hipGetLastError();
+  return launch_tile_map(offsets, a.E, p.rows, bm, a, zero_a, bytes_a, zero_b, bytes_b, s);
 }
 
 template <typename G, int VEC>

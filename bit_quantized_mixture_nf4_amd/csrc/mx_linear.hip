@@ -151,6 +151,589 @@ hipError_t launch_rows_mt(const MxLinearPlan &p, const MxLinearArgs &m, const in
   return hipGetLastError();
 }
 
+// ---- the tiled product ----
+
+// Tiles of 64 TM rows x 64 TN columns x 128: 4 waves (2 x 2), each of 32 TM x 32 TN as TM x TN
+// v_mfma_scale_f32_32x32x64_f8f6f4 for each half of a K-step. Weights are the A operand: lane (row
+// r = l % 32, half h = l / 32) gives the 32 k of block h of its row and that block's scale, and
+// its results are runs of 4 columns of one row (register 4 q + t: column 8 q + 4 h + t). A row of
+// a K-step is 64 bytes of codes and 4 scales, one word, staged as it is and shifted by 8: bytes 0
+// and 2 of word h are the scales of the two halves (op_sel).
+//
+// While K-step ks runs from one LDS stage, ks + 1 goes from registers to the other and ks + 3 is
+// asked for (ks + 2 is on its way). The wave's instructions are cut into 2 TM TN slots of one MFMA (32 cycles) and a
+// share of that work, each closed by a scheduling barrier. The 16-byte pieces of a row lie at
+// piece ^ (row / 2 % 4), so that eight rows of one piece fill all banks.
+// HALF: the last K-step is half (in % 128 = 64).
+template <int I, typename F>
+__device__ __forceinline__ void each_slot(F &&f) {
+  if constexpr (I > 0) {
+    each_slot<I - 1>(f);
+    f(std::integral_constant<int, I - 1>{});
+  }
+}
+
+// memory from p on as a buffer of 2^32 - 1 bytes
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t whole_buffer(const uint8_t *p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, -1, 0x00027000);
+}
+
+template <int TM, int TN>
+struct MxTile {
+  static constexpr int kM = 64 * TM, kN = 64 * TN, kStage = (kM + kN) * 64, kScales = 2 * (kM + kN);  // (words of a K-step)
+  static constexpr int kOutLd = 32 * TN + 4;                 // a wave's 32 rows on their way out, fp32
+  static constexpr int kOut = 4 * 32 * kOutLd * 4, kIn = 2 * (kStage + 4 * kScales * 4);
+  static constexpr int kBytes = kOut > kIn ? kOut : kIn;
+};
+
+template <int TM, int TN, bool HALF>
+__global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLinearArgs m) {
+  using T = MxTile<TM, TN>;
+  constexpr int kM = T::kM, kN = T::kN, R = TM + TN, MN = TM * TN, D = 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kBytes];
+  const LinearArgs &g = m.lin;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, h = lane >> 5;
+  int mt, nt, share;
+  if (!place_of(tile_count(g, kM), (g.out + kN - 1) / kN, 1, 1024 / kM, mt, nt, share)) return;
+  const int4 tm = tile_of(g, mt, kM);
+  const int64_t e = tm.x, row0 = int64_t(tm.y) + tm.z;
+  const int valid = tm.w;
+
+  // 16-byte piece tid % 4 of rows tid / 4 + 64 i; rows past the last repeat it (their results are not
+  // stored). Operands are read as buffers, by 32-bit offsets and a uniform one for the K-step: rows by
+  // place from the tile's first one (gathered ones from x's, which is checked to fit), weight rows from
+  // the expert's first one.
+  const int piece = tid & 3, prow = tid >> 2;
+  const uint32_t kb = g.in / 2, sb = g.in / 32;
+  const int64_t skip = m.sorted ? 0 : row0;
+  const buffer_t xb = whole_buffer(m.x + skip * kb), xsb = whole_buffer(m.xs + skip * sb);
+  const buffer_t wb = whole_buffer(g.packed + e * g.out * int64_t(kb)), wsb = whole_buffer(g.scales + e * g.out * int64_t(sb));
+  const auto x_row = [&](int r) -> uint32_t {
+    r = min(r, valid - 1);
+    return m.sorted ? uint32_t(source_row(m, row0 + r)) : uint32_t(r);
+  };
+  const auto w_row = [&](int r) -> uint32_t { return min(nt * kN + r, g.out - 1); };
+  uint32_t src[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    src[i] = (i < TM ? x_row(prow + 64 * i) : w_row(prow + 64 * (i - TM))) * kb + piece * 16;
+  // the scale words of row tid % kM of x and row tid % kN of the weights (some threads repeat others'),
+  // or, where a thread has one row, of either
+  constexpr bool kOneRow = kM + kN <= 256;
+  constexpr int kWords = kOneRow ? 1 : 2;
+  uint32_t ssrc[kWords];
+  int sdst[kWords];
+  const bool mine_x = tid % (kM + kN) < kM;
+  if constexpr (kOneRow) {
+    sdst[0] = tid % (kM + kN);
+    ssrc[0] = (mine_x ? x_row(sdst[0]) : w_row(sdst[0] - kM)) * sb;
+  } else {
+    sdst[0] = tid % kM;
+    sdst[1] = kM + tid % kN;
+    ssrc[0] = x_row(sdst[0]) * sb;
+    ssrc[1] = w_row(sdst[1] - kM) * sb;
+  }
+  const int nK = (g.in + 127) / 128, last = nK - 1;
+
+  u32x4 in[D][R];  // of the next D K-steps
+  u32x4 in_s[kWords];  // of the next four, one load a row: a line of scales is read for 4 K-steps
+  auto load = [&](int set, int ks, int i) {
+    // (HALF: pieces 2 and 3 of the last K-step lie behind the row, and are not multiplied)
+    const uint32_t at = HALF && ks == last && piece >= 2 ? src[i] - 32 : src[i];
+    in[set % D][i] = __builtin_amdgcn_raw_buffer_load_b128(i < TM ? xb : wb, at, ks * 64, 0);
+  };
+  auto load_scales = [&](int panel) {
+    const int first = 4 * panel;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      // (one row a thread: whole waves have x's or the weights')
+      const buffer_t of = i == 0 && (!kOneRow || __builtin_amdgcn_readfirstlane(mine_x)) ? xsb : wsb;
+      if (!HALF && first + 4 <= nK) {
+        in_s[i] = __builtin_amdgcn_raw_buffer_load_b128(of, ssrc[i], first * 4, 0);
+      } else {
+        // words past the row's end repeat the last one
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int ks = min(first + w, last);
+          if (HALF) {
+            const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(of, ssrc[i], ks * 4, 0);
+            const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(of, ssrc[i], ks * 4 + (ks == last ? 0 : 2), 0);
+            in_s[i][w] = lo | hi << 16;
+          } else {
+            in_s[i][w] = __builtin_amdgcn_raw_buffer_load_b32(of, ssrc[i], ks * 4, 0);
+          }
+        }
+      }
+    }
+  };
+  auto stage = [&](int st) { return lds + st * T::kStage; };
+  // the scales of K-step ks: two panels of four
+  auto scales = [&](int ks) { return reinterpret_cast<uint32_t *>(lds + 2 * T::kStage) + (ks & 7) * T::kScales; };
+  auto store = [&](int st, int i) {
+    const int row = prow + 64 * i;
+    *reinterpret_cast<u32x4 *>(stage(st) + row * 64 + (piece ^ (row >> 1 & 3)) * 16) = in[st % D][i];
+  };
+  auto store_scales = [&](int panel) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        *reinterpret_cast<u32x2 *>(scales(4 * panel + w) + 2 * sdst[i]) = u32x2{in_s[i][w], in_s[i][w] >> 8};
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  u32x4 f[2][R];
+  int sc[2][R];  // by the K-step's parity
+  // fragment i of half kh: 0 .. TM - 1 the wave's rows of x, then its weight rows
+  auto row_of = [&](int i) { return i < TM ? wm * 32 * TM + i * 32 + r32 : kM + wn * 32 * TN + (i - TM) * 32 + r32; };
+  auto frag = [&](int st, int kh, int i) {
+    const int row = row_of(i);
+    f[kh][i] = *reinterpret_cast<const u32x4 *>(stage(st) + row * 64 + ((2 * kh + h) ^ (row >> 1 & 3)) * 16);
+  };
+  auto frag_scale = [&](int st, int ks, int i) { sc[st][i] = int(scales(ks)[2 * row_of(i) + h]); };
+
+  // the first stage; loads past the last K-step repeat it
+  auto load_step = [&](int set, int ks) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) load(set, ks, i);
+  };
+  load_scales(0);
+  load_step(0, 0);
+  if constexpr (D == 2) load_step(1, min(1, last));
+#pragma unroll
+  for (int i = 0; i < R; ++i) store(0, i);
+  store_scales(0);
+  load_scales(1);
+  load_step(0, min(D, last));
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    frag_scale(0, 0, i);
+    frag(0, 0, i);
+  }
+
+  // fragments in the order in which the MFMAs (rows outside, columns inside) need them: the first
+  // rows', all columns', the other rows'
+  constexpr auto nth = [](int q) { return q == 0 ? 0 : q <= TN ? TM + q - 1 : q - TN; };
+  auto kstep = [&](auto cur_c, int ks) {
+    constexpr int CUR = decltype(cur_c)::value, NXT = CUR ^ 1;
+    const int ahead = min(ks + 1 + D, last);
+    if ((ks & 3) == 3) {  // the next four K-steps' scales, and those behind them
+      store_scales((ks >> 2) + 1);
+      load_scales((ks >> 2) + 2);
+    }
+    each_slot<2 * MN>([&](auto slot) {
+      constexpr int s = decltype(slot)::value, kh = s / MN, i = s % MN / TN, j = s % TN;
+      if constexpr (kh == 0)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[0][TM + j]), operand(f[0][i]), acc[i][j],
+                                                                    MX_E2M1, MX_E2M1, 0, sc[CUR][TM + j], 0, sc[CUR][i]);
+      else if (!HALF || ks < last)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[1][TM + j]), operand(f[1][i]), acc[i][j],
+                                                                    MX_E2M1, MX_E2M1, 2, sc[CUR][TM + j], 2, sc[CUR][i]);
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        if (s == q * MN / R) {
+          frag(CUR, 1, nth(q));
+          store(NXT, q);
+          load(NXT, ahead, q);
+        }
+        if (s == MN + q * MN / R) {
+          frag_scale(NXT, ks + 1, nth(q));
+          frag(NXT, 0, nth(q));
+        }
+      }
+      // every wave has filled its share of the next stage, and read its last fragment of this one
+      if constexpr (s == MN - 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  int ks = 0;
+  for (; ks + 1 < nK; ks += 2) {
+    kstep(std::integral_constant<int, 0>{}, ks);
+    kstep(std::integral_constant<int, 1>{}, ks + 1);
+  }
+  if (ks < nK) kstep(std::integral_constant<int, 0>{}, ks);
+  __syncthreads();  // the last stage's fragments are read
+
+  // ---- epilogue: 32 rows of the wave at a time through its own part of LDS, so that every global
+  // access is a run of a row; all rows of a lane side by side, so that their accesses overlap ----
+  float *tile = reinterpret_cast<float *>(lds) + wave * 32 * T::kOutLd;
+  const int col0 = nt * kN + wn * 32 * TN;
+  auto turn = [&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16 &c = acc[i][j];
+        *reinterpret_cast<f32x4 *>(tile + r32 * T::kOutLd + j * 32 + 8 * q + 4 * h) =
+            f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      }
+    const int first = wm * 32 * TM + i * 32;
+    if (g.out % 8 == 0) {
+      constexpr int kL = 4 * TN, kRows = 64 / kL, kN8 = 32 / kRows;  // lanes a row, rows at once, turns
+      const int cl = lane % kL * 8, col = col0 + cl, r0 = first + lane / kL;
+      if (col >= g.out) return;
+      const int64_t at = (row0 + r0) * g.out + col;
+      float v[8 * kN8], b[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) b[q] = 0.0f;
+      if (g.bias) load_row<8>(g.bias + e * g.out + col, b);
+      Raw<bf16_t, 8> res[kN8];
+      if (g.residual) {
+#pragma unroll
+        for (int n = 0; n < kN8; ++n)
+          res[n].fetch(reinterpret_cast<const bf16_t *>(g.residual) + at + int64_t(n * kRows) * g.out, r0 + n * kRows < valid);
+      }
+#pragma unroll
+      for (int n = 0; n < kN8; ++n)
+        load_row<8>(tile + (lane / kL + n * kRows) * T::kOutLd + cl, reinterpret_cast<float(&)[8]>(v[8 * n]));
+#pragma unroll
+      for (int q = 0; q < 8 * kN8; ++q) v[q] += b[q % 8];
+      if (g.pre) {
+#pragma unroll
+        for (int n = 0; n < kN8; ++n)
+          if (r0 + n * kRows < valid)
+            store_row<8>(g.pre + at + int64_t(n * kRows) * g.out, reinterpret_cast<float(&)[8]>(v[8 * n]));
+      }
+      act_values<8 * kN8>(g.act, v);
+      if (g.residual) {
+#pragma unroll
+        for (int n = 0; n < kN8; ++n) {
+          float r[8];
+          res[n].get(r);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[8 * n + q] += r[q];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kN8; ++n) {
+        if (r0 + n * kRows >= valid) continue;
+        const int64_t to = at + int64_t(n * kRows) * g.out;
+        if (g.y_f32)
+          store_row<8>(static_cast<float *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
+        else
+          store_row<8>(static_cast<bf16_t *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
+      }
+    } else {
+      for (int c = lane % (32 * TN); c < 32 * TN && col0 + c < g.out; c += 64) {
+        const float b[1] = {g.bias ? g.bias[e * g.out + col0 + c] : 0.0f};
+        for (int r = lane / (32 * TN); r < 32 && first + r < valid; r += TN == 1 ? 2 : 1) {
+          float v[1] = {tile[r * T::kOutLd + c]};
+          linear_epilogue<1>(g, (row0 + first + r) * g.out + col0 + c, b, v);
+        }
+      }
+    }
+  };
+  each_slot<TM>(turn);
+}
+
+// ---- large products ----
+
+// 16 bytes a lane from a buffer straight into LDS, 1 KB from `lds` on in the order of the lanes. The
+// compiler does not see that LDS is written: every reader is behind a wait for the vector memory counter and
+// a barrier written out here. (No register is written, so none can be taken for free while the load flies.)
+__device__ __forceinline__ void load_to_lds(buffer_t b, uint32_t offset, uint32_t step, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(offset), "s"(b), "s"(step), "s"(lds)
+               : "memory", "m0");
+}
+// waits until at most N vector memory operations of the wave are under way
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+// Tiles of 128 TM rows x 256 columns x 128: 8 waves (4 x 2), each of 32 TM x 128; one workgroup per CU that
+// stays for all its tiles.
+template <int TM>
+struct MxStream {
+  static constexpr int kM = 128 * TM, kN = 256, kThreads = 512, kRows = kM + kN;
+  static constexpr int kStage = kRows * 64, kStages = 3, kPanel = kRows * 16, kPanels = 3;
+  static constexpr int kOutLd = 36;  // a wave's 32 x 32 results on their way out, fp32
+  static constexpr int kOutAt = kStages * kStage + kPanels * kPanel;
+  static constexpr int kBytes = kOutAt + 8 * 32 * kOutLd * 4;
+};
+
+template <int TM>
+__global__ __launch_bounds__(512, 2) void mx_stream_kernel(MxLinearArgs m) {
+  using T = MxStream<TM>;
+  constexpr int kM = T::kM, kN = T::kN, TN = 4, R = TM + TN, MN = TM * TN;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kBytes];
+  const LinearArgs &g = m.lin;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, h = lane >> 5;
+  const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds));
+  const uint32_t kb = g.in / 2, sb = g.in / 32;
+  const int nK = g.in / 128;
+
+  // this workgroup's tiles: every so-many-th of its XCD's share
+  const int n_mt = tile_count(g, kM), n_nt = (g.out + kN - 1) / kN;
+  const uint32_t W = uint32_t(n_mt) * uint32_t(n_nt), per = (W + 7) / 8, each = gridDim.x / 8;
+  const uint32_t begin = (blockIdx.x % 8) * per, end = min(begin + per, W);
+  uint32_t L = begin + blockIdx.x / 8;
+  if (L >= end) return;
+  struct Tile {
+    int e, valid, nt;
+    int64_t row0;
+  };
+  auto tile_of_L = [&](uint32_t l) {
+    int mt, nt;
+    tile_at(l, n_mt, n_nt, 1024 / kM, mt, nt);
+    const int4 t = tile_of(g, mt, kM);
+    return Tile{t.x, t.w, nt, int64_t(t.y) + t.z};
+  };
+  // what a thread fetches of a tile: pieces of 16 bytes of TM rows of x and two weight rows, and the
+  // scales of one row of either. A row's piece p lies at p ^ (row / 2 % 4), so a lane's place in LDS
+  // fixes which piece it asks for. Rows past the tile's last repeat it.
+  struct Source {
+    buffer_t x, w, s;
+    uint32_t xo[TM], wo[2], so;
+  };
+  const int srow = tid < T::kRows ? tid : tid - T::kRows;
+  const bool s_of_x = wave * 64 < kM, has_scales = wave * 64 < T::kRows;
+  auto offsets_of = [&](const Tile &t, Source &s) {
+    const auto x_row = [&](int r) -> uint32_t {
+      r = min(r, t.valid - 1);
+      return m.sorted ? uint32_t(source_row(m, t.row0 + r)) : uint32_t(r);
+    };
+    const auto w_row = [&](int r) -> uint32_t { return min(t.nt * kN + r, g.out - 1); };
+    const int r = lane >> 2, piece = (lane & 3) ^ (lane >> 3 & 3);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) s.xo[i] = x_row(16 * (TM * wave + i) + r) * kb + piece * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s.wo[i] = w_row(16 * (2 * wave + i) + r) * kb + piece * 16;
+    s.so = (s_of_x ? x_row(srow) : w_row(max(srow - kM, 0))) * sb;
+  };
+  auto buffers_of = [&](const Tile &t, Source &s) {
+    const int64_t skip = m.sorted ? 0 : t.row0, first = int64_t(t.e) * g.out;
+    s.x = whole_buffer(m.x + skip * kb);
+    s.w = whole_buffer(g.packed + first * kb);
+    s.s = whole_buffer(s_of_x ? m.xs + skip * sb : g.scales + first * sb);
+  };
+
+  Tile cur = tile_of_L(L), next = L + each < end ? tile_of_L(L + each) : cur;
+  Source src, ahead;
+  offsets_of(cur, src);
+  buffers_of(cur, src);
+  offsets_of(next, ahead);
+
+  // the stream of K-steps of all tiles: step by step into a ring of three stages, three steps ahead; the
+  // scales of four steps at a time (the last four of a row where fewer are left) into a ring of three panels
+  int f_ks = 0, f_stage = 0, f_panel = 0;
+  bool f_next = L + each < end;  // the stream goes on behind the tile it is in
+  auto fetch = [&] {
+    const uint32_t at = lds0 + f_stage * T::kStage;
+    if ((f_ks & 3) == 0) {
+      if (has_scales)
+        load_to_lds(src.s, src.so, min(f_ks, nK - 4) * 4, lds0 + T::kStages * T::kStage + f_panel * T::kPanel + wave * 1024);
+      f_panel = f_panel == T::kPanels - 1 ? 0 : f_panel + 1;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) load_to_lds(src.x, src.xo[i], f_ks * 64, at + (TM * wave + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_to_lds(src.w, src.wo[i], f_ks * 64, at + kM * 64 + (2 * wave + i) * 1024);
+    f_stage = f_stage == T::kStages - 1 ? 0 : f_stage + 1;
+    if (++f_ks == nK) {
+      f_ks = 0;
+      if (f_next) {
+        const Source s = ahead;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) src.xo[i] = s.xo[i];
+        src.wo[0] = s.wo[0];
+        src.wo[1] = s.wo[1];
+        src.so = s.so;
+        buffers_of(next, src);
+      }  // (behind the last tile it repeats that, and nobody reads it)
+    }
+  };
+
+  f32x16 acc[TM][TN];
+  u32x4 f[2][R];
+  uint32_t sc[R], sc_next[R];
+  // fragment i of half t of the K-step: 0 .. TM - 1 the wave's rows of x, then its weight rows. Lane half h
+  // has the 32 k of block 2 h + t, and both blocks' scales in one 16-bit word.
+  auto row_of = [&](int i) { return i < TM ? (wm * TM + i) * 32 + r32 : kM + (wn * TN + i - TM) * 32 + r32; };
+  auto frag = [&](int stage, int t, int i) {
+    const int row = row_of(i);
+    f[t][i] = *reinterpret_cast<const u32x4 *>(lds + stage * T::kStage + row * 64 + ((2 * h + t) ^ (row >> 1 & 3)) * 16);
+  };
+  auto frag_scale = [&](int at, int i) { sc_next[i] = *reinterpret_cast<const uint16_t *>(lds + at + row_of(i) * 16 + 2 * h); };
+  constexpr auto nth = [](int q) { return q == 0 ? 0 : q <= TN ? TM + q - 1 : q - TN; };
+
+  int c_stage = 0, c_panel = 0;  // of the K-step under way
+  fetch();
+  fetch();
+  fetch();
+  wait_loads<0>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    frag_scale(T::kStages * T::kStage, i);
+    frag(0, 0, i);
+  }
+  int landed = 2;  // K-steps behind this one that have landed whatever the counter says
+
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+    for (int ks = 0; ks < nK; ++ks) {
+      const int n_stage = c_stage == T::kStages - 1 ? 0 : c_stage + 1, n_ks = ks + 1 < nK ? ks + 1 : 0;
+      if ((n_ks & 3) == 0) c_panel = c_panel == T::kPanels - 1 ? 0 : c_panel + 1;
+      const int s_at = T::kStages * T::kStage + c_panel * T::kPanel + (n_ks - min(n_ks & ~3, nK - 4)) * 4;
+#pragma unroll
+      for (int i = 0; i < R; ++i) sc[i] = sc_next[i];
+      each_slot<2 * MN>([&](auto slot) {
+        constexpr int s = decltype(slot)::value, t = s / MN, i = s % MN / TN, j = s % TN;
+        if constexpr (t == 0)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[0][TM + j]), operand(f[0][i]), acc[i][j],
+                                                                      MX_E2M1, MX_E2M1, 0, sc[TM + j], 0, sc[i]);
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[1][TM + j]), operand(f[1][i]), acc[i][j],
+                                                                      MX_E2M1, MX_E2M1, 1, sc[TM + j], 1, sc[i]);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          if (s == q * (MN - 2) / R) frag(c_stage, 1, nth(q));
+          if (s == MN + q * MN / R) {
+            frag_scale(s_at, nth(q));
+            frag(n_stage, 0, nth(q));
+          }
+        }
+        // every wave has read its last fragment of this stage, and its share of the next one has landed
+        if constexpr (s == MN - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (landed)
+            --landed;
+          else
+            wait_loads<TM + 2>();
+          __syncthreads();
+          fetch();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      c_stage = n_stage;
+    }
+
+    // ---- epilogue: 32 x 32 results of the wave at a time through its own part of LDS ----
+    float *tile = reinterpret_cast<float *>(lds + T::kOutAt) + wave * 32 * T::kOutLd;
+    const bool more = L + each < end, after = L + 2 * each < end;
+    const Tile was = cur;
+    cur = next;
+    if (after) {  // the addresses of the tile behind the next
+      next = tile_of_L(L + 2 * each);
+      offsets_of(next, ahead);
+    }
+    f_next = after;
+    each_slot<TM * TN>([&](auto ic) {
+      constexpr int i = decltype(ic)::value / TN, j = decltype(ic)::value % TN;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16 &c = acc[i][j];
+        *reinterpret_cast<f32x4 *>(tile + r32 * T::kOutLd + 8 * q + 4 * h) =
+            f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      }
+      const int first = (wm * TM + i) * 32, col0 = was.nt * kN + (wn * TN + j) * 32;
+      if (g.out % 8 == 0) {
+        const int cl = lane % 4 * 8, col = col0 + cl, r0 = first + lane / 4;
+        const int64_t at = (was.row0 + r0) * g.out + col;
+        float v[16], b[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) b[q] = 0.0f;
+        if (g.bias && col < g.out) load_row<8>(g.bias + int64_t(was.e) * g.out + col, b);
+        Raw<bf16_t, 8> res[2];
+        if (g.residual) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            res[n].fetch(reinterpret_cast<const bf16_t *>(g.residual) + at + int64_t(n * 16) * g.out,
+                         col < g.out && r0 + n * 16 < was.valid);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          load_row<8>(tile + (lane / 4 + n * 16) * T::kOutLd + cl, reinterpret_cast<float(&)[8]>(v[8 * n]));
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] += b[q % 8];
+        if constexpr (i == 0 && j == 0) wait_loads<0>();  // three K-steps have landed: nothing counts the stores
+        if (g.pre) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            if (col < g.out && r0 + n * 16 < was.valid)
+              store_row<8>(g.pre + at + int64_t(n * 16) * g.out, reinterpret_cast<float(&)[8]>(v[8 * n]));
+        }
+        act_values<16>(g.act, v);
+        if (g.residual) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float r[8];
+            res[n].get(r);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[8 * n + q] += r[q];
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (col >= g.out || r0 + n * 16 >= was.valid) continue;
+          const int64_t to = at + int64_t(n * 16) * g.out;
+          if (g.y_f32)
+            store_row<8>(static_cast<float *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
+          else
+            store_row<8>(static_cast<bf16_t *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
+        }
+      } else {
+        if constexpr (i == 0 && j == 0) wait_loads<0>();
+        const int col = col0 + r32;
+        if (col < g.out) {
+          const float b[1] = {g.bias ? g.bias[int64_t(was.e) * g.out + col] : 0.0f};
+          for (int r = h; r < 32 && first + r < was.valid; r += 2) {
+            float v[1] = {tile[r * T::kOutLd + r32]};
+            linear_epilogue<1>(g, (was.row0 + first + r) * g.out + col, b, v);
+          }
+        }
+      }
+    });
+    if (!more) break;
+    L += each;
+    landed = 2;
+  }
+  wait_loads<0>();  // nothing flies into LDS behind the end
+}
+
+template <int TM>
+hipError_t launch_stream(const MxLinearPlan &p, const MxLinearArgs &m, hipStream_t s) {
+  const int64_t tiles = tiles_at_most(m.lin.E, p.rows, MxStream<TM>::kM) * ((m.lin.out + 255) / 256);
+  const int64_t grid = tiles < 256 ? (tiles + 7) / 8 * 8 : 256;
+  hipLaunchKernelGGL(mx_stream_kernel<TM>, dim3(uint32_t(grid)), dim3(512), 0, s, m);
+  return hipGetLastError();
+}
+
+template <int TM, int TN>
+hipError_t launch_tiles(const MxLinearPlan &p, const MxLinearArgs &m, hipStream_t s) {
+  using T = MxTile<TM, TN>;
+  const LinearArgs &a = m.lin;
+  const int64_t tiles = tiles_at_most(a.E, p.rows, T::kM) * ((a.out + T::kN - 1) / T::kN);
+  const dim3 grid(uint32_t((tiles + 7) / 8 * 8)), block(256);
+  if (a.in % 128)
+    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, true>), grid, block, 0, s, m);
+  else
+    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, false>), grid, block, 0, s, m);
+  return hipGetLastError();
+}
+
 }  // namespace
 }  // namespace e4b
 
@@ -158,7 +741,7 @@ using namespace e4b;
 
 extern "C" size_t e4b_mx_linear_workspace_bytes(const e4b_stack *st, int64_t rows) {
   MxLinearPlan p;
-  return plan_mx_linear(st, rows, 1, false, E4B_ACT_NONE, E4B_BF16, &p) == E4B_OK ? 0 : 0;
+  return plan_mx_linear(st, rows, 1, false, E4B_ACT_NONE, E4B_BF16, &p) == E4B_OK ? p.ws_bytes : 0;
 }
 
 extern "C" e4b_status e4b_mx_linear(const e4b_stack *st, int64_t rows, const int32_t *offsets,
@@ -171,11 +754,11 @@ extern "C" e4b_status e4b_mx_linear(const e4b_stack *st, int64_t rows, const int
   if (s != E4B_OK) return s;
   if (!offsets && st->E != 1) return E4B_ERR_NULL;
   if (rows == 0) return E4B_OK;
-  if (!x_codes || !x_scales || !y) return E4B_ERR_NULL;
+  if (!x_codes || !x_scales || !y || (p.ws_bytes && !ws)) return E4B_ERR_NULL;
+  if (ws_bytes < p.ws_bytes) return E4B_ERR_WORKSPACE;
   if (!aligned16(offsets) || !aligned16(sorted_pair) || !aligned16(x_codes) || !aligned16(x_scales) ||
       !aligned16(bias) || !aligned16(residual_bf16) || !aligned16(y) || !aligned16(pre) || !aligned16(ws))
     return E4B_ERR_ALIGN;
-  (void)ws_bytes;
   MxLinearArgs m{};
   m.x = x_codes;
   m.xs = x_scales;
@@ -195,9 +778,24 @@ extern "C" e4b_status e4b_mx_linear(const e4b_stack *st, int64_t rows, const int
   a.y = y;
   a.y_f32 = y_dtype == E4B_F32;
   a.pre = pre;
-  const int64_t mean = (rows + st->E - 1) / st->E;
-  const hipError_t err = mean <= 16   ? launch_rows_mt<1>(p, m, offsets, stream)
-                         : mean <= 32 ? launch_rows_mt<2>(p, m, offsets, stream)
-                                      : launch_rows_mt<4>(p, m, offsets, stream);
+  hipError_t err;
+  if (p.tiles == MX_ROWS) {
+    const int64_t mean = (rows + st->E - 1) / st->E;
+    err = mean <= 16   ? launch_rows_mt<1>(p, m, offsets, stream)
+          : mean <= 32 ? launch_rows_mt<2>(p, m, offsets, stream)
+                       : launch_rows_mt<4>(p, m, offsets, stream);
+    return err == hipSuccess ? E4B_OK : E4B_ERR_HIP;
+  }
+  if (offsets) {
+    a.tile_offsets = reinterpret_cast<const int32_t *>(ws);
+    a.tile_map = reinterpret_cast<const int4 *>(static_cast<char *>(ws) + p.off_tile_map);
+    err = launch_tile_map(offsets, a.E, rows, mx_tile_rows(p.tiles), a, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4,
+                          stream);
+    if (err != hipSuccess) return E4B_ERR_HIP;
+  }
+  err = p.tiles == MX_256    ? launch_stream<2>(p, m, stream)
+        : p.tiles == MX_TALL ? launch_stream<1>(p, m, stream)
+        : p.tiles == MX_128  ? launch_tiles<2, 2>(p, m, stream)
+                             : launch_tiles<1, 1>(p, m, stream);
   return err == hipSuccess ? E4B_OK : E4B_ERR_HIP;
 }

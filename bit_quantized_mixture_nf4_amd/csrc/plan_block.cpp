@@ -211,6 +211,14 @@ e4b_status check_mx_rows(int64_t rows, int64_t K) {
   return E4B_OK;
 }
 
+static int mx_tiles(const e4b_stack *st, int64_t rows, int64_t tokens) {
+  // (the tiles address gathered rows of x in 32 bits)
+  if (tokens * (st->in / 2) >= (int64_t(1) << 32)) return MX_ROWS;
+  if (rows <= 32 * st->E) return MX_ROWS;
+  const int64_t wide = row_tiles(st, rows, 256) * ((st->out + 255) / 256);
+  return st->in % 128 == 0 && st->in >= 512 && wide >= 512 ? MX_256 : MX_128;
+}
+
 e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool gathered, int32_t act, int32_t dtype,
                           MxLinearPlan *p) {
   *p = MxLinearPlan{};
@@ -221,6 +229,10 @@ e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool
   if (st->codebook != E4B_CB_MXFP4) return E4B_ERR_CODEBOOK;
   if (gathered && (top_k < 1 || top_k > kMaxTopK || rows % top_k != 0)) return E4B_ERR_SHAPE;
   p->rows = rows;
+  p->tiles = mx_tiles(st, rows, gathered ? rows / top_k : 0);
+  if (p->tiles == MX_ROWS || rows == 0) return E4B_OK;  // (the kernel for few rows reads the offsets itself)
+  p->off_tile_map = (size_t(st->E + 1) * 4 + 255) / 256 * 256;
+  p->ws_bytes = p->off_tile_map + size_t(tiles_at_most(st->E, rows, mx_tile_rows(p->tiles))) * 16;
   return E4B_OK;
 }
 
