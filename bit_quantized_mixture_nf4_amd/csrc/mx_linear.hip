@@ -38,6 +38,14 @@ __device__ __forceinline__ int64_t source_row(const MxLinearArgs &g, int64_t r) 
   return min(t, uint32_t(g.tokens - 1));
 }
 
+// zeros for the rows of no expert, by thread i of n
+__device__ __forceinline__ void clear_tail(const LinearArgs &g, const int32_t *__restrict__ offsets, int64_t i, int64_t n) {
+  const int64_t from = clamped_offset(offsets, g.E, g.E, int32_t(g.rows)) * int64_t(g.out), to = g.rows * int64_t(g.out);
+  if (g.pre) clear_bytes(reinterpret_cast<char *>(g.pre), from * 4, to * 4, i, n);
+  const int y_bytes = g.y_f32 ? 4 : 2;
+  clear_bytes(static_cast<char *>(g.y), from * y_bytes, to * y_bytes, i, n);
+}
+
 // One workgroup per block of 16 MT rows of an expert (found from the offsets) and 8 / wk
 // groups of 16 columns; wk waves share a column group's k and join their sums in order.
 constexpr int kRowThreads = 512;
@@ -51,15 +59,10 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(MxLinearArgs m, co
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = 8 / wk, slice = wave % wk;
   const int32_t block = int32_t(blockIdx.z * gridDim.y + blockIdx.y);
-  if (block >= blocks) {  // the rows of no expert
+  if (block >= blocks) {
     const int32_t z = block - blocks;
     if (z >= zeros) return;
-    const int64_t from = clamped_offset(offsets, g.E, g.E, rows) * int64_t(g.out), to = rows * int64_t(g.out);
-    const int64_t i = (int64_t(z) * gridDim.x + blockIdx.x) * kRowThreads + tid;
-    const int64_t n = int64_t(zeros) * gridDim.x * kRowThreads;
-    if (g.pre) clear_bytes(reinterpret_cast<char *>(g.pre), from * 4, to * 4, i, n);
-    const int y_bytes = g.y_f32 ? 4 : 2;
-    clear_bytes(static_cast<char *>(g.y), from * y_bytes, to * y_bytes, i, n);
+    clear_tail(g, offsets, (int64_t(z) * gridDim.x + blockIdx.x) * kRowThreads + tid, int64_t(zeros) * gridDim.x * kRowThreads);
     return;
   }
   int e;
@@ -163,7 +166,7 @@ hipError_t launch_rows_mt(const MxLinearPlan &p, const MxLinearArgs &m, const in
 // While K-step ks runs from one LDS stage, ks + 1 goes from registers to the other and ks + 3 is
 // asked for (ks + 2 is on its way). The wave's instructions are cut into 2 TM TN slots of one MFMA (32 cycles) and a
 // share of that work, each closed by a scheduling barrier. The 16-byte pieces of a row lie at
-// piece ^ (row / 2 % 4), so that eight rows of one piece fill all banks.
+// piece ^ (row / 4 % 4), so that sixteen rows of one piece fill all banks.
 // HALF: the last K-step is half (in % 128 = 64).
 template <int I, typename F>
 __device__ __forceinline__ void each_slot(F &&f) {
@@ -178,6 +181,10 @@ typedef __amdgpu_buffer_rsrc_t buffer_t;
 __device__ __forceinline__ buffer_t whole_buffer(const uint8_t *p) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, -1, 0x00027000);
 }
+// of `bytes` bytes, or as far as a lane's offset goes: loads from behind them give zeros
+__device__ __forceinline__ buffer_t sized_buffer(const uint8_t *p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, int(min(bytes, int64_t(0xFFFFFFFFll))), 0x00027000);
+}
 
 template <int TM, int TN>
 struct MxTile {
@@ -188,7 +195,8 @@ struct MxTile {
 };
 
 template <int TM, int TN, bool HALF>
-__global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLinearArgs m) {
+__global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxLinearArgs m, const int32_t *__restrict__ offsets,
+                                                         int32_t tiles) {
   using T = MxTile<TM, TN>;
   constexpr int kM = T::kM, kN = T::kN, R = TM + TN, MN = TM * TN, D = 2;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::kBytes];
@@ -196,25 +204,44 @@ __global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLin
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, h = lane >> 5;
   int mt, nt, share;
-  if (!place_of(tile_count(g, kM), (g.out + kN - 1) / kN, 1, 1024 / kM, mt, nt, share)) return;
-  const int4 tm = tile_of(g, mt, kM);
-  const int64_t e = tm.x, row0 = int64_t(tm.y) + tm.z;
-  const int valid = tm.w;
+  int64_t e = 0, row0;
+  int valid;
+  if (offsets) {
+    // found from the offsets: a map of the tiles would cost a launch. How many there are is not known then: the
+    // workgroups without one come last, and an XCD takes every eighth column tile.
+    if (int32_t(blockIdx.x) >= tiles) {
+      clear_tail(g, offsets, int64_t(blockIdx.x - tiles) * 256 + tid, int64_t(gridDim.x - tiles) * 256);
+      return;
+    }
+    const uint32_t n_nt = (g.out + kN - 1) / kN;
+    nt = int(blockIdx.x % n_nt);
+    int32_t at, r0, hi;
+    if (!block_of(offsets, g.E, int32_t(g.rows), kM, int32_t(blockIdx.x / n_nt), lane, at, r0, hi)) return;
+    e = at;
+    row0 = r0;
+    valid = min(kM, hi - r0);
+  } else {
+    if (!place_of(tile_count(g, kM), (g.out + kN - 1) / kN, 1, 1024 / kM, mt, nt, share)) return;
+    const int4 tm = tile_of(g, mt, kM);
+    e = tm.x;
+    row0 = int64_t(tm.y) + tm.z;
+    valid = tm.w;
+  }
 
   // 16-byte piece tid % 4 of rows tid / 4 + 64 i; rows past the last repeat it (their results are not
   // stored). Operands are read as buffers, by 32-bit offsets and a uniform one for the K-step: rows by
-  // place from the tile's first one (gathered ones from x's, which is checked to fit), weight rows from
-  // the expert's first one.
+  // place and weight rows from the tile's first one (gathered ones from x's, which is checked to fit).
   const int piece = tid & 3, prow = tid >> 2;
   const uint32_t kb = g.in / 2, sb = g.in / 32;
   const int64_t skip = m.sorted ? 0 : row0;
   const buffer_t xb = whole_buffer(m.x + skip * kb), xsb = whole_buffer(m.xs + skip * sb);
-  const buffer_t wb = whole_buffer(g.packed + e * g.out * int64_t(kb)), wsb = whole_buffer(g.scales + e * g.out * int64_t(sb));
+  const int64_t w_first = e * g.out + nt * kN;
+  const buffer_t wb = whole_buffer(g.packed + w_first * kb), wsb = whole_buffer(g.scales + w_first * sb);
   const auto x_row = [&](int r) -> uint32_t {
     r = min(r, valid - 1);
     return m.sorted ? uint32_t(source_row(m, row0 + r)) : uint32_t(r);
   };
-  const auto w_row = [&](int r) -> uint32_t { return min(nt * kN + r, g.out - 1); };
+  const auto w_row = [&](int r) -> uint32_t { return min(r, g.out - 1 - nt * kN); };
   uint32_t src[R];
 #pragma unroll
   for (int i = 0; i < R; ++i)
@@ -273,7 +300,7 @@ __global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLin
   auto scales = [&](int ks) { return reinterpret_cast<uint32_t *>(lds + 2 * T::kStage) + (ks & 7) * T::kScales; };
   auto store = [&](int st, int i) {
     const int row = prow + 64 * i;
-    *reinterpret_cast<u32x4 *>(stage(st) + row * 64 + (piece ^ (row >> 1 & 3)) * 16) = in[st % D][i];
+    *reinterpret_cast<u32x4 *>(stage(st) + row * 64 + (piece ^ (row >> 2 & 3)) * 16) = in[st % D][i];
   };
   auto store_scales = [&](int panel) {
 #pragma unroll
@@ -296,7 +323,7 @@ __global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLin
   auto row_of = [&](int i) { return i < TM ? wm * 32 * TM + i * 32 + r32 : kM + wn * 32 * TN + (i - TM) * 32 + r32; };
   auto frag = [&](int st, int kh, int i) {
     const int row = row_of(i);
-    f[kh][i] = *reinterpret_cast<const u32x4 *>(stage(st) + row * 64 + ((2 * kh + h) ^ (row >> 1 & 3)) * 16);
+    f[kh][i] = *reinterpret_cast<const u32x4 *>(stage(st) + row * 64 + ((2 * kh + h) ^ (row >> 2 & 3)) * 16);
   };
   auto frag_scale = [&](int st, int ks, int i) { sc[st][i] = int(scales(ks)[2 * row_of(i) + h]); };
 
@@ -441,6 +468,12 @@ __global__ __launch_bounds__(256, TM * TN > 8 ? 1 : 2) void mx_tile_kernel(MxLin
 
 // ---- large products ----
 
+// waits until at most N vector memory operations of the wave are under way
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
 // 16 bytes a lane from a buffer straight into LDS, 1 KB from `lds` on in the order of the lanes. The
 // compiler does not see that LDS is written: every reader is behind a wait for the vector memory counter and
 // a barrier written out here. (No register is written, so none can be taken for free while the load flies.)
@@ -448,39 +481,47 @@ __device__ __forceinline__ void load_to_lds(buffer_t b, uint32_t offset, uint32_
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
                : "v"(offset), "s"(b), "s"(step), "s"(lds)
-               : "memory", "m0");
+               : "memory");
 }
-// waits until at most N vector memory operations of the wave are under way
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+// The same if `go`, without a branch that the compiler sees: the step around it stays one basic block (behind
+// a branch the compiler gathered the matrix instructions, and copied the fragments).
+__device__ __forceinline__ void load_to_lds_if(int go, buffer_t b, uint32_t offset, uint32_t lds) {
+  asm volatile(
+      "s_cmp_eq_u32 %3, 0\n\ts_cbranch_scc1 .Lmx_no_load%=\n\t"
+      "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds\n"
+      ".Lmx_no_load%=:"
+      :
+      : "v"(offset), "s"(b), "s"(lds), "s"(go)
+      : "memory", "scc");
 }
 
-// Tiles of 128 TM rows x 256 columns x 128: 8 waves (4 x 2), each of 32 TM x 128; one workgroup per CU that
-// stays for all its tiles.
-template <int TM>
-struct MxStream {
-  static constexpr int kM = 128 * TM, kN = 256, kThreads = 512, kRows = kM + kN;
-  static constexpr int kStage = kRows * 64, kStages = 3, kPanel = kRows * 16, kPanels = 3;
-  static constexpr int kOutLd = 36;  // a wave's 32 x 32 results on their way out, fp32
-  static constexpr int kOutAt = kStages * kStage + kPanels * kPanel;
-  static constexpr int kBytes = kOutAt + 8 * 32 * kOutLd * 4;
-};
+// the lane's number, counted where it is needed: no register holds it meanwhile
+__device__ __forceinline__ int lane_again() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
 
-template <int TM>
+// Tiles of 256 rows x 256 columns x 256: 8 waves (4 x 2) of 64 x 128, one workgroup per CU that stays for all
+// its tiles, whose steps are one stream: while one of two LDS stages is multiplied, the other takes the next
+// step's operands, of the next tile too. Operands go to LDS without registers, in whole 128-byte lines: in
+// half lines (steps of 128) a step needed twice the requests, and the L1 held all eight waves up. The
+// scales of four steps come together, 32 bytes a row, into two panels in turn.
+constexpr int kStreamM = 256, kStreamN = 256, kStreamK = 256;
+constexpr int kStreamRows = kStreamM + kStreamN, kStreamStage = kStreamRows * 128, kStreamPanel = kStreamRows * 32;
+
 __global__ __launch_bounds__(512, 2) void mx_stream_kernel(MxLinearArgs m) {
-  using T = MxStream<TM>;
-  constexpr int kM = T::kM, kN = T::kN, TN = 4, R = TM + TN, MN = TM * TN;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kBytes];
+  constexpr int TM = 2, TN = 4, R = TM + TN, MN = TM * TN, kPanels = 2 * kStreamStage;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kPanels + 2 * kStreamPanel];
   const LinearArgs &g = m.lin;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, h = lane >> 5;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds));
   const uint32_t kb = g.in / 2, sb = g.in / 32;
-  const int nK = g.in / 128;
+  const int steps = g.in / kStreamK;
 
   // this workgroup's tiles: every so-many-th of its XCD's share
-  const int n_mt = tile_count(g, kM), n_nt = (g.out + kN - 1) / kN;
+  const int n_mt = __builtin_amdgcn_readfirstlane(tile_count(g, kStreamM)), n_nt = (g.out + kStreamN - 1) / kStreamN;
   const uint32_t W = uint32_t(n_mt) * uint32_t(n_nt), per = (W + 7) / 8, each = gridDim.x / 8;
   const uint32_t begin = (blockIdx.x % 8) * per, end = min(begin + per, W);
   uint32_t L = begin + blockIdx.x / 8;
@@ -491,246 +532,339 @@ __global__ __launch_bounds__(512, 2) void mx_stream_kernel(MxLinearArgs m) {
   };
   auto tile_of_L = [&](uint32_t l) {
     int mt, nt;
-    tile_at(l, n_mt, n_nt, 1024 / kM, mt, nt);
-    const int4 t = tile_of(g, mt, kM);
-    return Tile{t.x, t.w, nt, int64_t(t.y) + t.z};
+    tile_at(l, n_mt, n_nt, 1024 / kStreamM, mt, nt);
+    if (!g.tile_map) return Tile{0, int(min(int64_t(kStreamM), g.rows - int64_t(mt) * kStreamM)), nt, int64_t(mt) * kStreamM};
+    // (by the scalar cache: the entry is the same for all lanes, and an earlier launch wrote it)
+    const auto *t = reinterpret_cast<const __attribute__((address_space(4))) int32_t *>(reinterpret_cast<uintptr_t>(g.tile_map)) +
+                    mt * 4;
+    return Tile{t[0], t[3], nt, int64_t(t[1]) + t[2]};
   };
-  // what a thread fetches of a tile: pieces of 16 bytes of TM rows of x and two weight rows, and the
-  // scales of one row of either. A row's piece p lies at p ^ (row / 2 % 4), so a lane's place in LDS
-  // fixes which piece it asks for. Rows past the tile's last repeat it.
-  struct Source {
-    buffer_t x, w, s;
-    uint32_t xo[TM], wo[2], so;
+
+  // What a lane fetches of a step: 16 bytes of four rows of x and of four weight rows, eight lanes a row; and of
+  // four steps' scales 16 bytes of two rows, x's by waves 0 .. 3 and the weights' by the others. Piece p of a
+  // row lies at p ^ row / 2 % 8 (scales: at p ^ row / 8 % 2), so that the sixteen lanes of a cycle meet all
+  // banks; a lane's place is fixed, so that says which piece it asks for. Rows past the tile's last
+  // repeat it (their results are not stored).
+  const bool s_of_x = wave < 4;
+  const int d_row = wave * 32 + (lane >> 3), s_row = (wave & 3) * 64 + (lane >> 1);
+  struct Rows {  // of x, by tile
+    uint32_t x[4], s[2];
   };
-  const int srow = tid < T::kRows ? tid : tid - T::kRows;
-  const bool s_of_x = wave * 64 < kM, has_scales = wave * 64 < T::kRows;
-  auto offsets_of = [&](const Tile &t, Source &s) {
+  auto rows_of = [&](const Tile &t) {
+    Rows q;
     const auto x_row = [&](int r) -> uint32_t {
       r = min(r, t.valid - 1);
       return m.sorted ? uint32_t(source_row(m, t.row0 + r)) : uint32_t(r);
     };
-    const auto w_row = [&](int r) -> uint32_t { return min(t.nt * kN + r, g.out - 1); };
-    const int r = lane >> 2, piece = (lane & 3) ^ (lane >> 3 & 3);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) s.xo[i] = x_row(16 * (TM * wave + i) + r) * kb + piece * 16;
+    for (int i = 0; i < 4; ++i) q.x[i] = x_row(d_row + 8 * i);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) s.wo[i] = w_row(16 * (2 * wave + i) + r) * kb + piece * 16;
-    s.so = (s_of_x ? x_row(srow) : w_row(max(srow - kM, 0))) * sb;
+    for (int i = 0; i < 2; ++i) q.s[i] = s_of_x ? x_row(s_row + 32 * i) : 0;
+    return q;
   };
-  auto buffers_of = [&](const Tile &t, Source &s) {
-    const int64_t skip = m.sorted ? 0 : t.row0, first = int64_t(t.e) * g.out;
-    s.x = whole_buffer(m.x + skip * kb);
-    s.w = whole_buffer(g.packed + first * kb);
-    s.s = whole_buffer(s_of_x ? m.xs + skip * sb : g.scales + first * sb);
+  const auto word = [](uint32_t v) {  // as it stands here: products taken before the steps cost registers in all of them
+    asm volatile("" : "+v"(v));
+    return v;
+  };
+  buffer_t xb, wb, ssb;
+  uint32_t xo[4], so[2];
+  // (pieces 0 and 1 of `i`; the rows of i + 2 lie 16 further down)
+  const auto piece_of = [&](int l, int i) { return uint32_t((l & 7) ^ ((l >> 4) + 4 * (i & 1))) * 16; };
+  const uint32_t wo[2] = {d_row * kb + piece_of(lane, 0), (d_row + 8) * kb + piece_of(lane, 1)};
+  // The weights' rows behind the expert's last one are the next expert's, and behind the stack's end zeros by the
+  // buffer's size: no store takes their results.
+  auto source_w = [&](const Tile &t) {
+    const int64_t first = int64_t(t.e) * g.out + t.nt * kStreamN, left = (int64_t(g.E) * g.out - first) * kb;
+    wb = sized_buffer(g.packed + first * kb, left);
+  };
+  auto source_x = [&](const Tile &t, const Rows &q) {  // and of the scales
+    const int64_t skip = m.sorted ? 0 : t.row0, first = int64_t(t.e) * g.out + t.nt * kStreamN;
+    xb = whole_buffer(m.x + skip * kb);
+    ssb = s_of_x ? whole_buffer(m.xs + skip * sb) : sized_buffer(g.scales + first * sb, (int64_t(g.E) * g.out - first) * sb);
+    const int l = lane_again();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xo[i] = word(__umul24(word(q.x[i]), kb) + piece_of(l, i));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) so[i] = word(__umul24(word(s_of_x ? q.s[i] : (wave & 3) * 64 + (l >> 1) + 32 * i), sb));
   };
 
   Tile cur = tile_of_L(L), next = L + each < end ? tile_of_L(L + each) : cur;
-  Source src, ahead;
-  offsets_of(cur, src);
-  buffers_of(cur, src);
-  offsets_of(next, ahead);
+  bool more = L + each < end;
+  Rows ahead = rows_of(next);
+  source_x(cur, rows_of(cur));
+  source_w(cur);
 
-  // the stream of K-steps of all tiles: step by step into a ring of three stages, three steps ahead; the
-  // scales of four steps at a time (the last four of a row where fewer are left) into a ring of three panels
-  int f_ks = 0, f_stage = 0, f_panel = 0;
-  bool f_next = L + each < end;  // the stream goes on behind the tile it is in
-  auto fetch = [&] {
-    const uint32_t at = lds0 + f_stage * T::kStage;
-    if ((f_ks & 3) == 0) {
-      if (has_scales)
-        load_to_lds(src.s, src.so, min(f_ks, nK - 4) * 4, lds0 + T::kStages * T::kStage + f_panel * T::kPanel + wave * 1024);
-      f_panel = f_panel == T::kPanels - 1 ? 0 : f_panel + 1;
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) load_to_lds(src.x, src.xo[i], f_ks * 64, at + (TM * wave + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) load_to_lds(src.w, src.wo[i], f_ks * 64, at + kM * 64 + (2 * wave + i) * 1024);
-    f_stage = f_stage == T::kStages - 1 ? 0 : f_stage + 1;
-    if (++f_ks == nK) {
-      f_ks = 0;
-      if (f_next) {
-        const Source s = ahead;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) src.xo[i] = s.xo[i];
-        src.wo[0] = s.wo[0];
-        src.wo[1] = s.wo[1];
-        src.so = s.so;
-        buffers_of(next, src);
-      }  // (behind the last tile it repeats that, and nobody reads it)
-    }
+  // load n of ten that ask for step ks of the tile that `source_x` and `source_w` were told: the scales of its four
+  // steps (the last 16 bytes of a row where fewer are left) with the first of them, then x, then the weights
+  int f_panel = 1;
+  struct Fetch {
+    int panel;
+    uint32_t s_lds, step, lds;
+  };
+  auto fetch_of = [&](int ks, int stage) {
+    const int panel = ((ks & 3) - 1) >> 31 & 1;  // (integers: a comparison would go by way of the lanes)
+    f_panel ^= panel;
+    return Fetch{panel,
+                 lds0 + kPanels + f_panel * kStreamPanel + wave * 2048, uint32_t(ks) * 128,
+                 lds0 + stage * kStreamStage + wave * 4096};
+  };
+  auto load_nth = [&](const Fetch &q, int n) {
+    if (n < 2) {
+      const int l = lane_again();
+      load_to_lds_if(q.panel, ssb, so[n] + min(int(q.step / 16) + ((l ^ l >> 4) & 1) * 16, int(sb) - 16), q.s_lds + n * 1024);
+    } else if (n < 6)
+      load_to_lds(xb, xo[n - 2], q.step, q.lds + (n - 2) * 1024);
+    else
+      // (the whole offset in the lane's part, which is what the buffer's size is held against)
+      load_to_lds(wb, wo[n & 1] + (q.step + (n - 6) / 2 * 16 * kb), 0, q.lds + kStreamM * 128 + (n - 6) * 1024);
   };
 
+  // Fragment i of quarter t of the step: 0 .. TM - 1 the wave's rows of x, then its weight rows. Lane half h has
+  // the 32 k of block 4 h + t, so that one word holds its four scales, byte t for quarter t (op_sel).
+  // A lane's own part of the addresses (rows 32 further on lie alike):
   f32x16 acc[TM][TN];
   u32x4 f[2][R];
   uint32_t sc[R], sc_next[R];
-  // fragment i of half t of the K-step: 0 .. TM - 1 the wave's rows of x, then its weight rows. Lane half h
-  // has the 32 k of block 2 h + t, and both blocks' scales in one 16-bit word.
-  auto row_of = [&](int i) { return i < TM ? (wm * TM + i) * 32 + r32 : kM + (wn * TN + i - TM) * 32 + r32; };
+  const int f_lane = r32 * 128 + (4 * h ^ (r32 >> 1 & 7)) * 16;
+  const int x_first = wm * TM * 32, w_first = kStreamM + wn * TN * 32;
   auto frag = [&](int stage, int t, int i) {
-    const int row = row_of(i);
-    f[t][i] = *reinterpret_cast<const u32x4 *>(lds + stage * T::kStage + row * 64 + ((2 * h + t) ^ (row >> 1 & 3)) * 16);
+    const int wave_at = stage * kStreamStage + (i < TM ? x_first : w_first) * 128;
+    f[t & 1][i] = *reinterpret_cast<const u32x4 *>(lds + (wave_at + (f_lane ^ t * 16)) + (i < TM ? i : i - TM) * 4096);
   };
-  auto frag_scale = [&](int at, int i) { sc_next[i] = *reinterpret_cast<const uint16_t *>(lds + at + row_of(i) * 16 + 2 * h); };
-  constexpr auto nth = [](int q) { return q == 0 ? 0 : q <= TN ? TM + q - 1 : q - TN; };
+  int c_panel = 0;  // of the step whose scales were read last
+  auto scales_at = [&](int ks) {
+    const int q = ks >> 1 & 1;  // the 16 bytes of a row's 32 that hold the step's
+    return (kPanels + c_panel * kStreamPanel + ks * 8 - min((ks & ~1) * 8, int(sb) - 16)) | q << 24;
+  };
+  int s_lane = 0;
+  auto frag_scale = [&](int at, int i) {
+    if (i == 0) {
+      const int l = lane_again();
+      s_lane = ((l & 31) * 32 + (l >> 3 & 1) * 16 + (l >> 5) * 4) ^ at >> 24 << 4;
+    }
+    const int wave_at = (at & 0xFFFFFF) + (i < TM ? x_first : w_first) * 32;
+    sc_next[i] = *reinterpret_cast<const uint32_t *>(lds + (wave_at + s_lane) + (i < TM ? i : i - TM) * 1024);
+  };
+  constexpr auto nth = [](int q) { return q == 0 ? 0 : q <= TN ? TM + q - 1 : q - TN; };  // in the order of their use
 
-  int c_stage = 0, c_panel = 0;  // of the K-step under way
-  fetch();
-  fetch();
-  fetch();
-  wait_loads<0>();
-  __syncthreads();
+  Fetch ask_w;  // the step whose weights are asked for next
+  {
+    const Fetch q = fetch_of(0, 0);
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    frag_scale(T::kStages * T::kStage, i);
-    frag(0, 0, i);
+    for (int n = 0; n < 10; ++n) load_nth(q, n);
+    wait_loads<0>();
+    ask_w = fetch_of(1, 1);
+#pragma unroll
+    for (int n = 0; n < 6; ++n) load_nth(ask_w, n);
   }
-  int landed = 2;  // K-steps behind this one that have landed whatever the counter says
+  __syncthreads();
+  int stage = 0;
+  const bool simple = !g.act && !g.residual && !g.pre && !g.y_f32;  // (an epilogue without the branches: 9K cycles a tile, not 16K)
 
   for (;;) {
+    // (read here and not by the tile before, whose epilogue needs the registers)
+    {
+      const int at = scales_at(0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        frag_scale(at, i);
+        frag(stage, 0, i);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-    for (int ks = 0; ks < nK; ++ks) {
-      const int n_stage = c_stage == T::kStages - 1 ? 0 : c_stage + 1, n_ks = ks + 1 < nK ? ks + 1 : 0;
-      if ((n_ks & 3) == 0) c_panel = c_panel == T::kPanels - 1 ? 0 : c_panel + 1;
-      const int s_at = T::kStages * T::kStage + c_panel * T::kPanel + (n_ks - min(n_ks & ~3, nK - 4)) * 4;
+    // the slots of a step: one MFMA each (two waves of a SIMD in turn, 64 cycles) and a fragment of the next
+    // quarter. Behind slot 23 the one barrier: every wave has read its last fragment of this stage, and its loads
+    // of the next step have landed. From there on the stage takes the step after the next one: scales and x in
+    // slots 24 .. 31, the weights in the first slots of the next step.
+#pragma unroll 1
+    for (int ks = 0; ks < steps; ++ks) {
+      const int n_ks = ks + 1 < steps ? ks + 1 : 0, n2_ks = n_ks + 1 < steps ? n_ks + 1 : 0;
+      // (behind the last tile it is asked for again, and nobody reads it)
+      if (more) {
+        if (n2_ks == 0) source_x(next, ahead);
+        if (n_ks == 0) source_w(next);
+      }
+      const Fetch ask_x = fetch_of(n2_ks, stage);
+      c_panel ^= ((n_ks & 3) - 1) >> 31 & 1;
+      const int s_at = scales_at(n_ks);
 #pragma unroll
       for (int i = 0; i < R; ++i) sc[i] = sc_next[i];
-      each_slot<2 * MN>([&](auto slot) {
+      each_slot<4 * MN>([&](auto slot) {
         constexpr int s = decltype(slot)::value, t = s / MN, i = s % MN / TN, j = s % TN;
-        if constexpr (t == 0)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[0][TM + j]), operand(f[0][i]), acc[i][j],
-                                                                      MX_E2M1, MX_E2M1, 0, sc[TM + j], 0, sc[i]);
-        else
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[1][TM + j]), operand(f[1][i]), acc[i][j],
-                                                                      MX_E2M1, MX_E2M1, 1, sc[TM + j], 1, sc[i]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(f[t & 1][TM + j]), operand(f[t & 1][i]), acc[i][j],
+                                                                    MX_E2M1, MX_E2M1, t, sc[TM + j], t, sc[i]);
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-          if (s == q * (MN - 2) / R) frag(c_stage, 1, nth(q));
-          if (s == MN + q * MN / R) {
-            frag_scale(s_at, nth(q));
-            frag(n_stage, 0, nth(q));
+        for (int q = 0; q < R; ++q)
+          if (s % MN == q) {
+            if constexpr (t < 3) {
+              frag(stage, t + 1, nth(q));
+            } else {
+              frag_scale(s_at, nth(q));
+              frag(stage ^ 1, 0, nth(q));
+            }
           }
-        }
-        // every wave has read its last fragment of this stage, and its share of the next one has landed
-        if constexpr (s == MN - 1) {
+#pragma unroll
+        for (int n = 0; n < 10; ++n)
+          if (s == (n < 2 ? 24 : n < 6 ? 21 + 2 * n : 2 * (n - 6))) load_nth(n < 6 ? ask_x : ask_w, n);
+        if constexpr (s == 3 * MN - 1) {
           __builtin_amdgcn_sched_barrier(0);
-          if (landed)
-            --landed;
-          else
-            wait_loads<TM + 2>();
-          __syncthreads();
-          fetch();
+          __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
         }
         __builtin_amdgcn_sched_barrier(0);
       });
-      c_stage = n_stage;
+      stage ^= 1;
+      ask_w = ask_x;
     }
 
-    // ---- epilogue: 32 x 32 results of the wave at a time through its own part of LDS ----
-    float *tile = reinterpret_cast<float *>(lds + T::kOutAt) + wave * 32 * T::kOutLd;
-    const bool more = L + each < end, after = L + 2 * each < end;
+    // ---- epilogue, without LDS: 32 x 32 results at a time, lane (row r32, half h) with columns 8 q + 4 h .. of
+    // group q; lanes swap until 16 rows have their 32 columns in one register's four lane groups ----
+    const bool last = !more;
     const Tile was = cur;
+    L += each;
     cur = next;
-    if (after) {  // the addresses of the tile behind the next
-      next = tile_of_L(L + 2 * each);
-      offsets_of(next, ahead);
-    }
-    f_next = after;
-    each_slot<TM * TN>([&](auto ic) {
-      constexpr int i = decltype(ic)::value / TN, j = decltype(ic)::value % TN;
+    more = L + each < end;
+    if (more) next = tile_of_L(L + each);
+    const int l = lane_again(), e_row = l & 15, e_col = (l & 16) + (l >> 5) * 8;
+    const int64_t down = int64_t(16) * g.out;
+    const auto col_of = [&](int part) { return was.nt * kStreamN + (wn * TN + part % TN) * 32 + e_col; };
+    const auto row_of = [&](int part) { return (wm * TM + part / TN) * 32 + e_row; };
+    // w[8 n ..]: columns e_col .. of row e_row + 16 n
+    const auto arrange = [&](float(&w)[16]) {
+      uint32_t v[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x16 &c = acc[i][j];
-        *reinterpret_cast<f32x4 *>(tile + r32 * T::kOutLd + 8 * q + 4 * h) =
-            f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+      for (int q = 0; q < 16; ++q) v[q] = __float_as_uint(w[q]);
+      const auto swap32 = [&](int a, int b) {
+        const auto t = __builtin_amdgcn_permlane32_swap(v[a], v[b], false, false);
+        v[a] = t[0], v[b] = t[1];
+      };
+      const auto swap16 = [&](int a, int b) {
+        const auto t = __builtin_amdgcn_permlane16_swap(v[a], v[b], false, false);
+        v[a] = t[0], v[b] = t[1];
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) swap32(q, 4 + q), swap32(8 + q, 12 + q);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) swap16(q, 8 + q);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) w[q] = __uint_as_float(v[q]);
+    };
+    if (simple) {
+      float b[TN][8];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) b[j][q] = 0.0f;
+        if (g.bias && col_of(j) < g.out) load_row<8>(g.bias + int64_t(was.e) * g.out + col_of(j), b[j]);
       }
-      const int first = (wm * TM + i) * 32, col0 = was.nt * kN + (wn * TN + j) * 32;
-      if (g.out % 8 == 0) {
-        const int cl = lane % 4 * 8, col = col0 + cl, r0 = first + lane / 4;
-        const int64_t at = (was.row0 + r0) * g.out + col;
-        float v[16], b[8];
+      bf16_t *y = static_cast<bf16_t *>(g.y) + (was.row0 + row_of(0)) * g.out + col_of(0);
+      each_slot<MN>([&](auto part) {
+        constexpr int i = decltype(part)::value / TN, j = decltype(part)::value % TN;
+        float w[16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) b[q] = 0.0f;
-        if (g.bias && col < g.out) load_row<8>(g.bias + int64_t(was.e) * g.out + col, b);
-        Raw<bf16_t, 8> res[2];
-        if (g.residual) {
+        for (int q = 0; q < 16; ++q) w[q] = acc[i][j][q];
+        arrange(w);
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-            res[n].fetch(reinterpret_cast<const bf16_t *>(g.residual) + at + int64_t(n * 16) * g.out,
-                         col < g.out && r0 + n * 16 < was.valid);
-        }
+        for (int q = 0; q < 16; ++q) w[q] += b[j][q % 8];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          load_row<8>(tile + (lane / 4 + n * 16) * T::kOutLd + cl, reinterpret_cast<float(&)[8]>(v[8 * n]));
+          if (col_of(j) < g.out && row_of(i * TN) + 16 * n < was.valid)
+            store_row<8>(y + (2 * i + n) * down + j * 32, reinterpret_cast<float(&)[8]>(w[8 * n]));
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+      struct Extra {  // what a part reads
+        float b[8];
+        Raw<bf16_t, 8> res[2];
+      } extra;
+      auto fetch_extra = [&](int part) {
+        const int col = col_of(part), r = row_of(part);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q] += b[q % 8];
-        if constexpr (i == 0 && j == 0) wait_loads<0>();  // three K-steps have landed: nothing counts the stores
+        for (int q = 0; q < 8; ++q) extra.b[q] = 0.0f;
+        if (g.bias && col < g.out) load_row<8>(g.bias + int64_t(was.e) * g.out + col, extra.b);
+        if (g.residual) {
+          const bf16_t *from = reinterpret_cast<const bf16_t *>(g.residual) + (was.row0 + r) * g.out + col;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) extra.res[n].fetch(from + n * down, col < g.out && r + 16 * n < was.valid);
+        }
+      };
+      fetch_extra(0);
+      // (one body for all parts: unrolled, the activations' code did not fit the instruction cache)
+#pragma unroll 1
+      for (int part = 0; part < MN; ++part) {
+        float w[16];
+        each_slot<MN>([&](auto n) {
+          constexpr int i = decltype(n)::value / TN, j = decltype(n)::value % TN;
+          if (part == decltype(n)::value) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) w[q] = acc[i][j][q];
+          }
+        });
+        arrange(w);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) w[q] += extra.b[q % 8];
+        Raw<bf16_t, 8> res[2] = {extra.res[0], extra.res[1]};
+        if (part + 1 < MN) fetch_extra(part + 1);
+        const int col = col_of(part), r = row_of(part);
+        const int64_t at = (was.row0 + r) * g.out + col;
+        const bool in[2] = {col < g.out && r < was.valid, col < g.out && r + 16 < was.valid};
         if (g.pre) {
 #pragma unroll
           for (int n = 0; n < 2; ++n)
-            if (col < g.out && r0 + n * 16 < was.valid)
-              store_row<8>(g.pre + at + int64_t(n * 16) * g.out, reinterpret_cast<float(&)[8]>(v[8 * n]));
+            if (in[n]) store_row<8>(g.pre + at + n * down, reinterpret_cast<float(&)[8]>(w[8 * n]));
         }
-        act_values<16>(g.act, v);
+        act_values<16>(g.act, w);
         if (g.residual) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float r[8];
-            res[n].get(r);
+            float f[8];
+            res[n].get(f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[8 * n + q] += r[q];
+            for (int q = 0; q < 8; ++q) w[8 * n + q] += f[q];
           }
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          if (col >= g.out || r0 + n * 16 >= was.valid) continue;
-          const int64_t to = at + int64_t(n * 16) * g.out;
+          if (!in[n]) continue;
           if (g.y_f32)
-            store_row<8>(static_cast<float *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
+            store_row<8>(static_cast<float *>(g.y) + at + n * down, reinterpret_cast<float(&)[8]>(w[8 * n]));
           else
-            store_row<8>(static_cast<bf16_t *>(g.y) + to, reinterpret_cast<float(&)[8]>(v[8 * n]));
-        }
-      } else {
-        if constexpr (i == 0 && j == 0) wait_loads<0>();
-        const int col = col0 + r32;
-        if (col < g.out) {
-          const float b[1] = {g.bias ? g.bias[int64_t(was.e) * g.out + col] : 0.0f};
-          for (int r = h; r < 32 && first + r < was.valid; r += 2) {
-            float v[1] = {tile[r * T::kOutLd + r32]};
-            linear_epilogue<1>(g, (was.row0 + first + r) * g.out + col, b, v);
-          }
+            store_row<8>(static_cast<bf16_t *>(g.y) + at + n * down, reinterpret_cast<float(&)[8]>(w[8 * n]));
         }
       }
-    });
-    if (!more) break;
-    L += each;
-    landed = 2;
+    }
+    if (last) break;
+    if (more) ahead = rows_of(next);  // (the rows of the tile behind the one whose steps come now)
   }
-  wait_loads<0>();  // nothing flies into LDS behind the end
+  wait_loads<0>();
 }
 
-template <int TM>
 hipError_t launch_stream(const MxLinearPlan &p, const MxLinearArgs &m, hipStream_t s) {
-  const int64_t tiles = tiles_at_most(m.lin.E, p.rows, MxStream<TM>::kM) * ((m.lin.out + 255) / 256);
+  const int64_t tiles = tiles_at_most(m.lin.E, p.rows, kStreamM) * ((m.lin.out + kStreamN - 1) / kStreamN);
   const int64_t grid = tiles < 256 ? (tiles + 7) / 8 * 8 : 256;
-  hipLaunchKernelGGL(mx_stream_kernel<TM>, dim3(uint32_t(grid)), dim3(512), 0, s, m);
+  hipLaunchKernelGGL(mx_stream_kernel, dim3(uint32_t(grid)), dim3(512), 0, s, m);
   return hipGetLastError();
 }
 
 template <int TM, int TN>
-hipError_t launch_tiles(const MxLinearPlan &p, const MxLinearArgs &m, hipStream_t s) {
+hipError_t launch_tiles(const MxLinearPlan &p, const MxLinearArgs &m, const int32_t *offsets, hipStream_t s) {
   using T = MxTile<TM, TN>;
   const LinearArgs &a = m.lin;
-  const int64_t tiles = tiles_at_most(a.E, p.rows, T::kM) * ((a.out + T::kN - 1) / T::kN);
-  const dim3 grid(uint32_t((tiles + 7) / 8 * 8)), block(256);
+  int64_t tiles = tiles_at_most(a.E, p.rows, T::kM) * ((a.out + T::kN - 1) / T::kN);
+  if (!offsets) tiles = (tiles + 7) / 8 * 8;
+  const int64_t bytes = p.rows * a.out * ((a.y_f32 ? 4 : 2) + (a.pre ? 4 : 0));
+  const dim3 grid(uint32_t(tiles + (offsets ? clear_groups(bytes, 1024) : 0))), block(256);
   if (a.in % 128)
-    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, true>), grid, block, 0, s, m);
+    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, true>), grid, block, 0, s, m, offsets, int32_t(tiles));
   else
-    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, false>), grid, block, 0, s, m);
+    hipLaunchKernelGGL((mx_tile_kernel<TM, TN, false>), grid, block, 0, s, m, offsets, int32_t(tiles));
   return hipGetLastError();
 }
 
@@ -780,22 +914,20 @@ extern "C" e4b_status e4b_mx_linear(const e4b_stack *st, int64_t rows, const int
   a.pre = pre;
   hipError_t err;
   if (p.tiles == MX_ROWS) {
-    const int64_t mean = (rows + st->E - 1) / st->E;
-    err = mean <= 16   ? launch_rows_mt<1>(p, m, offsets, stream)
-          : mean <= 32 ? launch_rows_mt<2>(p, m, offsets, stream)
-                       : launch_rows_mt<4>(p, m, offsets, stream);
+    // (more than 16 rows an expert: only where x is too long for the tiles)
+    err = rows <= 16 * st->E ? launch_rows_mt<1>(p, m, offsets, stream) : launch_rows_mt<4>(p, m, offsets, stream);
     return err == hipSuccess ? E4B_OK : E4B_ERR_HIP;
   }
-  if (offsets) {
+  if (offsets && !p.by_offsets) {
     a.tile_offsets = reinterpret_cast<const int32_t *>(ws);
     a.tile_map = reinterpret_cast<const int4 *>(static_cast<char *>(ws) + p.off_tile_map);
     err = launch_tile_map(offsets, a.E, rows, mx_tile_rows(p.tiles), a, y, st->out * (a.y_f32 ? 4 : 2), pre, st->out * 4,
                           stream);
     if (err != hipSuccess) return E4B_ERR_HIP;
   }
-  err = p.tiles == MX_256    ? launch_stream<2>(p, m, stream)
-        : p.tiles == MX_TALL ? launch_stream<1>(p, m, stream)
-        : p.tiles == MX_128  ? launch_tiles<2, 2>(p, m, stream)
-                             : launch_tiles<1, 1>(p, m, stream);
+  if (!p.by_offsets) offsets = nullptr;
+  err = p.tiles == MX_256   ? launch_stream(p, m, stream)
+        : p.tiles == MX_128 ? launch_tiles<2, 2>(p, m, offsets, stream)
+                             : launch_tiles<1, 1>(p, m, offsets, stream);
   return err == hipSuccess ? E4B_OK : E4B_ERR_HIP;
 }

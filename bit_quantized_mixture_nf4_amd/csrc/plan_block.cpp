@@ -211,12 +211,27 @@ e4b_status check_mx_rows(int64_t rows, int64_t K) {
   return E4B_OK;
 }
 
+// How a microscaled product is tiled: by the kernel for few rows, or in tiles of 64 x 64, 128 x 128 or
+// 256 x 256. In us on one MI355X:
+//   few rows / 64 / 128, one expert of 2048 -> 4096: 1 row 3.8 / 6.3 / 8.9, 16 rows 4.7 / 6.6 / 9.2, 48 rows
+//     7.6 / 6.9 / 9.5; 8 experts of 768 -> 2048, 16 rows each 4.9 / 4.7 / 6.4; 8 of 4096 -> 4096, one row each
+//     20.6 / 15.8 / 17.8: it wins where the larger tiles leave most CUs idle
+//   64 / 128, 8 experts of 4096 -> 4096, rows each: 32 16.9 / 17.4, 64 18.7 / 18.4, 96 30.0 / 19.5; 64 experts of
+//     1024 -> 2816: 32 27.9 / 28.5, 64 34.2 / 32.1; 256 rows of 2048 -> 4096: 7.6 / 10.0
+//   128 / 256, 8 experts of 4096 -> 4096, rows each: 256 33.3 / 38.3, 512 59.9 / 44.4, 2048 225 / 146; 64
+//     experts of 1024 -> 2816: 128 38.7 / 44.9, 192 54.7 / 49.0: a tile of 256 costs what three of 128 do
+//     (2.8 to 3.2), and less than one a CU costs the same
 static int mx_tiles(const e4b_stack *st, int64_t rows, int64_t tokens) {
   // (the tiles address gathered rows of x in 32 bits)
   if (tokens * (st->in / 2) >= (int64_t(1) << 32)) return MX_ROWS;
-  if (rows <= 32 * st->E) return MX_ROWS;
-  const int64_t wide = row_tiles(st, rows, 256) * ((st->out + 255) / 256);
-  return st->in % 128 == 0 && st->in >= 512 && wide >= 512 ? MX_256 : MX_128;
+  const auto tiles = [&](int64_t bm) { return row_tiles(st, rows, bm) * ((st->out + bm - 1) / bm); };
+  if (rows <= 16 * st->E && tiles(64) <= 128) return MX_ROWS;
+  // (a launch dimension has fewer than 2^32 threads)
+  const bool fits = tiles_at_most(st->E, rows, 64) * ((st->out + 63) / 64) < (int64_t(1) << 24) - 8;
+  if (fits && (rows <= 48 * st->E || tiles(64) <= 512)) return MX_64;
+  if (st->in % 256 != 0 || st->in < 512 || st->out % 8 != 0) return MX_128;
+  const int64_t wide = tiles(256);
+  return 3 * (wide > 224 ? wide : 224) < tiles(128) ? MX_256 : MX_128;
 }
 
 e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool gathered, int32_t act, int32_t dtype,
@@ -230,9 +245,13 @@ e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool
   if (gathered && (top_k < 1 || top_k > kMaxTopK || rows % top_k != 0)) return E4B_ERR_SHAPE;
   p->rows = rows;
   p->tiles = mx_tiles(st, rows, gathered ? rows / top_k : 0);
-  if (p->tiles == MX_ROWS || rows == 0) return E4B_OK;  // (the kernel for few rows reads the offsets itself)
+  // Each workgroup finds its tile by itself where that is cheaper than a launch that maps them (3.4 us; 8 experts of
+  // 4096 -> 4096, one row each: 15.8 us, with a map 19.2; 64 of 1024 -> 2816, 48 rows each 30.8 / 33.0, 96 each 35.3 / 36.5,
+  // 192 each 59.5 / 54.7: the map knows how many there are).
+  p->by_offsets = p->tiles != MX_256 && rows <= 4096 && st->E <= 512;
+  // (of a call's rows and experts alone: enough for any tiling)
   p->off_tile_map = (size_t(st->E + 1) * 4 + 255) / 256 * 256;
-  p->ws_bytes = p->off_tile_map + size_t(tiles_at_most(st->E, rows, mx_tile_rows(p->tiles))) * 16;
+  if (rows > 0) p->ws_bytes = p->off_tile_map + size_t(tiles_at_most(st->E, rows, 64)) * 16;
   return E4B_OK;
 }
 

@@ -116,11 +116,12 @@ size_t balance_ws_bytes(const BalanceArgs &a);
 // ---- microscaled rows and their product (mx4.hip, mx_linear.hip) ----
 // K a multiple of 64 up to 2^20, rows K below 2^35.
 e4b_status check_mx_rows(int64_t rows, int64_t K);
-// how it is tiled: few rows, or tiles of rows x columns 64 x 64, 128 x 128, 256 x 128, 256 x 256
-enum { MX_ROWS = 0, MX_64, MX_128, MX_TALL, MX_256 };
+// how it is tiled: few rows, or tiles of rows x columns 64 x 64, 128 x 128, 256 x 256
+enum { MX_ROWS = 0, MX_64, MX_128, MX_256 };
 inline int mx_tile_rows(int tiles) { return tiles == MX_64 ? 64 : tiles == MX_256 ? 256 : 128; }
 struct MxLinearPlan {
   int tiles;
+  bool by_offsets;  // each workgroup finds its tile from the offsets
   int64_t rows;
   size_t off_tile_map, ws_bytes;
 };

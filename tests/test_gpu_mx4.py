@@ -273,6 +273,77 @@ def test_product(E, rows, tail, inn, out, act, with_bias, with_res, yt):
     assert none is None and torch.equal(bits(y2), bits(y))
 
 
+# Products in every tiling, with rows enough for it: 128 x 128 tiles found by a map, 64 x 64 ones of many experts, and
+# 256 x 256 ones, one a workgroup and several in turn, of 2 to 9 K-steps of 256 (whose scales come for 4 at a time).
+LARGE = [
+    (1024, 2990, 5, 128, 520, "relu", True, True, "bf16"), (700, 2500, 0, 192, 264, "none", False, False, "fp32"),
+    (1, 4100, 0, 512, 2816, "none", False, False, "bf16"), (3, 5000, 0, 1280, 2312, "none", True, False, "bf16"),
+    (5, 12000, 33, 768, 2048, "none", True, False, "bf16"), (2, 9000, 0, 512, 2504, "silu", True, True, "bf16"),
+    (7, 9500, 130, 2304, 2056, "gelu", True, False, "fp32"), (300, 40000, 1, 1024, 2048, "none", False, True, "bf16"),
+]
+
+
+@pytest.mark.parametrize("E,rows,tail,inn,out,act,with_bias,with_res,yt", LARGE)
+def test_product_in_every_tiling(E, rows, tail, inn, out, act, with_bias, with_res, yt):
+    """The reference is summed by torch in 64 bits, on the GPU: numpy would take minutes."""
+    announce(f"mx product E={E} rows={rows}+{tail} {inn}->{out} {act} bias={with_bias} res={with_res} {yt}")
+    rng = np.random.default_rng(rows + out)
+    stack, w = _stack(E, out, inn, out + inn)
+    R, f64 = rows + tail, torch.float64
+    offsets = np.concatenate([[0], np.cumsum(_counts(E, rows, rng, (0, E - 1) if E > 2 else ()))]).astype(np.int32)
+    off_d = torch.from_numpy(offsets).to(DEV) if E > 1 or tail else None
+    q = e4b.mx4_rows(dev(rng.standard_normal((R, inn)) * np.exp(rng.standard_normal((R, 1))), torch.bfloat16))
+    x = torch.from_numpy(np.float32(mx.mx_rows_values(q.codes.cpu().numpy(), q.scales.cpu().numpy()))).to(DEV)
+    bias = dev(rng.standard_normal((E, out)) * 0.1, torch.float32) if with_bias else None
+    res = dev(rng.standard_normal((R, out)), torch.bfloat16) if with_res else None
+    y, pre = e4b.mx_linear(stack, q, offsets=off_d, bias=bias, act=act, residual=res, out_dtype=DT[yt], save=True)
+    y2, none = e4b.mx_linear(stack, q, offsets=off_d, bias=bias, act=act, residual=res, out_dtype=DT[yt])
+    assert none is None and torch.equal(bits(y2), bits(y))
+    assert not bits(y[rows:]).any() and not bits(pre[rows:]).any()
+    for e in range(E):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if a == b:
+            continue
+        we, xe = torch.from_numpy(np.float32(w[e])).to(DEV).to(f64).t().contiguous(), x[a:b].to(f64)
+        be = torch.zeros(out, device=DEV, dtype=f64) if bias is None else bias[e].to(f64)
+        z = host(xe @ we + be)
+        z_err = 2 * (inn + 4) * U * host(xe.abs() @ we.abs() + be.abs())
+        within(pre[a:b], z, z_err, f"pre of expert {e}")
+        ye, r = block.activation(act, z)[0], 0.0 if res is None else host(res[a:b])
+        within(y[a:b], ye + r, _act_errors(act, z, z_err) + 2 * U * (np.abs(ye + r) + np.abs(r)), f"y of expert {e}")
+
+
+@pytest.mark.parametrize("T,k,E,inn,out", [(3000, 4, 5, 768, 2048), (1200, 8, 300, 128, 2048)])
+def test_gathered_in_large_tiles(T, k, E, inn, out):
+    test_product_gathered_by_token(T, k, E, inn, out, 0.1)
+
+
+def test_lists_that_lead_nowhere_in_large_tiles():
+    test_lists_that_lead_nowhere_stay_inside(4, 12000, 512, 2048)
+
+
+def test_tokens_beyond_32_bits():
+    """Gathered rows of more than 2^32 bytes of codes."""
+    announce("mx product gathered beyond 32 bits")
+    T, inn, out = 8200, 2 ** 20, 64
+    codes = torch.zeros(T, inn // 2, device=DEV, dtype=torch.uint8)
+    scales = torch.full((T, inn // 32), 127, device=DEV, dtype=torch.uint8)
+    stack, _ = _stack(1, out, inn, 12)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    some = [0, 1, 4095, 4096, 8191, 8192, 8199]
+    for t in some:
+        codes[t] = torch.randint(0, 256, (inn // 2,), generator=g, device=DEV, dtype=torch.uint8)
+    q = e4b.MxRows(codes, scales)
+    perm = e4b.moe_permute(torch.zeros(T, 1, dtype=torch.int32, device=DEV), 1, torch.zeros(T, 8, device=DEV, dtype=torch.bfloat16))[1]
+    y, _ = e4b.mx_linear(stack, q, perm=perm, out_dtype=torch.float32)
+    alone, _ = e4b.mx_linear(stack, e4b.MxRows(codes[some], scales[some]), out_dtype=torch.float32)
+    mag = 6 * 2.0 ** -5 * 6 * inn  # of the terms
+    assert (y[some] - alone).abs().max().item() <= 4 * inn * U * mag
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[some] = False
+    assert not y[rest].any() and alone.abs().max(dim=1).values.gt(0).all()
+
+
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 513])
 @pytest.mark.parametrize("inn,out", [(128, 64), (192, 300)])
 def test_product_row_counts(rows, inn, out):
