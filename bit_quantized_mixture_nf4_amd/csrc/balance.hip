@@ -226,46 +226,65 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
   }
 }
 
-// One workgroup per sequence: its chunks' sums, in order.
-constexpr int kJoinThreads = 1024;
+// One workgroup per sequence: its chunks' sums, in order. A thread takes VEC experts of every so-many-th chunk,
+// kJoinAhead chunks at a time: waiting for one row after the other took 28 us for 512 chunks of 128
+// experts (16384 tokens, whose own sums take 7), so it takes 9.
+constexpr int kJoinThreads = 1024, kJoinAhead = 8;
+template <int VEC>
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs g, int cols) {
-  __shared__ float s_prob[kJoinThreads];
-  __shared__ int32_t s_counts[kJoinThreads];
+  __shared__ __attribute__((aligned(16))) float s_prob[kJoinThreads * VEC];
+  __shared__ __attribute__((aligned(16))) int32_t s_counts[kJoinThreads * VEC];
   __shared__ double s_dot[kJoinThreads / 64];
   __shared__ float s_z[kJoinThreads / 64];
   __shared__ int32_t s_n[kJoinThreads / 64];
+  typedef float values __attribute__((ext_vector_type(VEC)));
+  typedef int32_t numbers __attribute__((ext_vector_type(VEC)));
   const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t a = first_token(g, s), b = first_token(g, s + 1);
-  const int64_t w0 = a / g.chunk + s, chunks = b > a ? (int64_t(b) - a + g.chunk - 1) / g.chunk : 0;
-  // cols threads to a row of E sums (cols a power of two, at least E)
-  const int e = tid & (cols - 1), rows = kJoinThreads / cols;
-  float p = 0.0f;
-  int32_t c = 0;
+  const int64_t w0 = a / g.chunk + s;
+  const int32_t chunks = b > a ? (b - a + g.chunk - 1) / g.chunk : 0;
+  // cols threads to a row of E sums (cols a power of two, cols VEC at least E)
+  const int e = (tid & (cols - 1)) * VEC, rows = kJoinThreads / cols;
+  values p = 0.0f;
+  numbers c = 0;
   if (e < g.E) {
-#pragma unroll 8
-    for (int64_t i = tid / cols; i < chunks; i += rows) {
-      p += g.part_prob[(w0 + i) * g.E + e];
-      c += g.part_counts[(w0 + i) * g.E + e];
+    for (int32_t i0 = tid / cols; i0 < chunks; i0 += kJoinAhead * rows) {
+      values dp[kJoinAhead];
+      numbers dc[kJoinAhead];
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u) {
+        const int64_t at = (w0 + min(i0 + u * rows, chunks - 1)) * g.E + e;
+        dp[u] = *reinterpret_cast<const values *>(g.part_prob + at);
+        dc[u] = *reinterpret_cast<const numbers *>(g.part_counts + at);
+      }
+#pragma unroll
+      for (int u = 0; u < kJoinAhead; ++u)
+        if (i0 + u * rows < chunks) {
+          p += dp[u];
+          c += dc[u];
+        }
     }
   }
   float z = 0.0f;
   int32_t n = 0;
-  for (int64_t i = tid; i < chunks; i += kJoinThreads) {
+  for (int32_t i = tid; i < chunks; i += kJoinThreads) {
     z += g.part_z[w0 + i];
     n += g.part_tokens[w0 + i];
   }
-  s_prob[tid] = p;
-  s_counts[tid] = c;
+  *reinterpret_cast<values *>(&s_prob[tid * VEC]) = p;
+  *reinterpret_cast<numbers *>(&s_counts[tid * VEC]) = c;
   __syncthreads();
   double dot = 0.0;
   if (tid < g.E) {
-    for (int r = 1; r < rows; ++r) {
-      p += s_prob[r * cols + tid];
-      c += s_counts[r * cols + tid];
+    float sum = 0.0f;
+    int32_t count = 0;
+    for (int r = 0; r < rows; ++r) {
+      sum += s_prob[r * cols * VEC + tid];
+      count += s_counts[r * cols * VEC + tid];
     }
-    g.prob[int64_t(s) * g.E + tid] = p;
-    g.counts[int64_t(s) * g.E + tid] = c;
-    dot = double(p) * double(c);
+    g.prob[int64_t(s) * g.E + tid] = sum;
+    g.counts[int64_t(s) * g.E + tid] = count;
+    dot = double(sum) * double(count);
   }
   z = wave_sum(z);
 #pragma unroll
@@ -439,9 +458,13 @@ extern "C" e4b_status e4b_moe_balance(const e4b_balance *b, const float *logits,
   E4B_TRY(by_experts(a.E, [&](auto l, auto per, auto vec) {
     hipLaunchKernelGGL((balance_kernel<l(), per(), vec(), false>), dim3(uint32_t(grid)), dim3(256), 0, stream, a);
   }));
-  int cols = 64;
-  while (cols < a.E) cols *= 2;
-  hipLaunchKernelGGL(balance_join_kernel, dim3(uint32_t(a.S)), dim3(kJoinThreads), 0, stream, a, cols);
+  const int vec = a.E % 4 == 0 ? 4 : 1;
+  int cols = 1;
+  while (cols * vec < a.E) cols *= 2;
+  if (vec == 4)
+    hipLaunchKernelGGL(balance_join_kernel<4>, dim3(uint32_t(a.S)), dim3(kJoinThreads), 0, stream, a, cols);
+  else
+    hipLaunchKernelGGL(balance_join_kernel<1>, dim3(uint32_t(a.S)), dim3(kJoinThreads), 0, stream, a, cols);
   E4B_TRY(hipGetLastError());
   return E4B_OK;
 }

@@ -65,20 +65,21 @@ __device__ __forceinline__ uint32_t magnitude(const float (&v)[8]) {
   return m;
 }
 
-// silu(g) u in fp32, with e^-|g| of full relative precision: the product |g| log2 e is off by half a
-// step of its own, which the second term adds back. Right to 2^-21 of itself for |g| below kFar.
+// e^a of full relative precision, |a| up to kFar: the product a log2 e is off by half a step of its own, which
+// the second term adds back.
 constexpr float kFar = 64.0f;
-__device__ __forceinline__ float exp_minus(float a) {
-  const float t = a * -1.4426950408889634f;
-  const float r = fmaf(a, -1.4426950408889634f, -t) + a * -1.9259629911266175e-8f;
+__device__ __forceinline__ float exponential(float a) {
+  const float t = a * 1.4426950408889634f;
+  const float r = fmaf(a, 1.9259629911266175e-8f, fmaf(a, 1.4426950408889634f, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * 0.6931471805599453f, e);
 }
-__device__ __forceinline__ float silu(float g) {
-  const float e = exp_minus(fabsf(g));
-  return g * ((g < 0.0f ? e : 1.0f) * __builtin_amdgcn_rcpf(1.0f + e));
-}
+// silu(g) for g above -kFar, off by 2^-21 of itself at most (steps of 2^-24: two of the power, one each of its
+// correction, the sum and the product, two of the quotient).
 constexpr float kOff = 0x1p-20f;
+__device__ __forceinline__ float silu(float g) {
+  return g * __builtin_amdgcn_rcpf(1.0f + exponential(fmaxf(-g, -kFar)));
+}
 __device__ __forceinline__ double silu64(double g) {
   const double e = exp(-fabs(g));
   const double s = (g < 0.0 ? e : 1.0) / (1.0 + e);
@@ -114,16 +115,25 @@ __global__ __launch_bounds__(256) void mx4_gated_kernel(const T *__restrict__ x,
   float g[8], u[8], v[8];
   load_row<8>(p, g);
   load_row<8>(p + int64_t(per.d) * 8, u);
-  uint32_t unsure = 0;
+  float low = 0.0f, least = INFINITY, top = 0.0f;
+  bool nan = false;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float gs = silu(g[q]);
-    v[q] = gs * u[q];
-    // e^-|g| leaves fp32's range before its products do; a subnormal has lost bits, as has one beyond
-    const float least = fminf(fabsf(gs), fabsf(v[q]));
-    if (g[q] < -kFar || !(fabsf(v[q]) < 0x1p127f) || (least < 0x1p-100f && g[q] != 0.0f && u[q] != 0.0f)) unsure = 1;
+  for (int q = 0; q < 8; q += 2) {
+    v[q] = silu(g[q]) * u[q];
+    v[q + 1] = silu(g[q + 1]) * u[q + 1];
+    low = fminf(fminf(low, g[q]), g[q + 1]);
+    least = fminf(fminf(least, fabsf(g[q])), fabsf(g[q + 1]));
+    top = fmaxf(fmaxf(top, fabsf(v[q])), fabsf(v[q + 1]));
+    nan |= __builtin_isunordered(v[q], v[q + 1]);
   }
-  const float most = __uint_as_float(block_max(magnitude(v)));
+  // Not to be had in fp32: far below zero; a block near either end of fp32's range (in one that is not, a value
+  // that lost bits as a subnormal has the code 0), and a g that lost some.
+  const uint32_t amax = block_max(nan ? 0x7FC00000u : __float_as_uint(top));
+  uint32_t unsure = low < -kFar || amax >= 0x7F000000u /* 2^127 */ || (amax < 0x0D800000u /* 2^-100 */ && amax != 0);
+  if (least < 0x1p-100f)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) unsure |= fabsf(g[q]) < 0x1p-100f && g[q] != 0.0f && u[q] != 0.0f;
+  const float most = __uint_as_float(amax);
   uint32_t byte = scale_byte(__float_as_uint(fmaf(most, -kOff, most)));
   unsure |= byte ^ scale_byte(__float_as_uint(fmaf(most, kOff, most)));
   float lo[8], hi[8];
@@ -167,7 +177,7 @@ __global__ __launch_bounds__(256) void mx4_gated_bwd_kernel(const T *__restrict_
       u[q] = float(double(ga[q]) * silu64(gd));
       continue;
     }
-    const float e = exp_minus(fabsf(g[q])), r = __builtin_amdgcn_rcpf(1.0f + e);
+    const float e = exponential(-fabsf(g[q])), r = __builtin_amdgcn_rcpf(1.0f + e);
     const float s = neg ? e * r : r, rest = neg ? r : e * r;  // 1 - s, without a difference
     gs = g[q] * s;
     slope = e == 0.0f ? s : s * fmaf(g[q], rest, 1.0f);  // (an infinite g times 0)
