@@ -249,9 +249,10 @@ e4b_status plan_mx_linear(const e4b_stack *st, int64_t rows, int32_t top_k, bool
   // 4096 -> 4096, one row each: 15.8 us, with a map 19.2; 64 of 1024 -> 2816, 48 rows each 30.8 / 33.0, 96 each 35.3 / 36.5,
   // 192 each 59.5 / 54.7: the map knows how many there are).
   p->by_offsets = p->tiles != MX_256 && rows <= 4096 && st->E <= 512;
-  // (of a call's rows and experts alone: enough for any tiling)
+  // (rows in place and gathered ones agree about the map, but that the longest gathered ones have none)
+  if (rows == 0 || p->tiles == MX_ROWS || p->by_offsets) return E4B_OK;
   p->off_tile_map = (size_t(st->E + 1) * 4 + 255) / 256 * 256;
-  if (rows > 0) p->ws_bytes = p->off_tile_map + size_t(tiles_at_most(st->E, rows, 64)) * 16;
+  p->ws_bytes = p->off_tile_map + size_t(tiles_at_most(st->E, rows, mx_tile_rows(p->tiles))) * 16;
   return E4B_OK;
 }
 

@@ -13,8 +13,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _need, _vp, QuantStack
-from ._lib import load
+from . import CODEBOOKS, _need, _vp
+from ._lib import E4bStack, load
 from .block import ACTS, _DTYPES, _linear_args, _overlap, _rows, _run, _workspace
 
 
@@ -40,11 +40,14 @@ class MxRows:
         return self.codes.device
 
     def check(self):
-        _need(self.codes, "codes", torch.uint8)
-        if self.codes.dim() != 2 or self.K % 64 or self.K == 0:
-            raise ValueError(f"codes must be [n, K/2] with K % 64 == 0, got {tuple(self.codes.shape)}")
-        _need(self.scales, "scales", torch.uint8, self.codes.device, (self.rows, self.K // 32))
-        return self.codes.device
+        codes = self.codes
+        _need(codes, "codes", torch.uint8)
+        shape = codes.shape
+        if len(shape) != 2 or shape[1] % 32 or shape[1] == 0:
+            raise ValueError(f"codes must be [n, K/2] with K % 64 == 0, got {tuple(shape)}")
+        dev = codes.device
+        _need(self.scales, "scales", torch.uint8, dev, (shape[0], shape[1] // 16))
+        return dev
 
 
 def mx4_rows(x, gated=False):
@@ -84,8 +87,8 @@ def mx4_values(q, dtype=torch.bfloat16):
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
     out = torch.empty(q.rows, q.K, dtype=dtype, device=dev)
-    if q.rows:
-        c = QuantStack(q.codes, None, 1, q.rows, q.K, "mxfp4", q.scales).as_c()
+    if q.rows:  # (as a stack of one expert)
+        c = E4bStack(q.codes.data_ptr(), None, 1, q.rows, q.K, 32, CODEBOOKS["mxfp4"], q.scales.data_ptr())
         _run("e4b_dequantize_nf4", dev, ctypes.byref(c), _DTYPES[dtype], out.data_ptr())
     return out
 
