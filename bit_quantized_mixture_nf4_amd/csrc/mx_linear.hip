@@ -765,18 +765,23 @@ __global__ __launch_bounds__(512, 2) void mx_stream_kernel(MxLinearArgs m) {
         if (g.bias && col_of(j) < g.out) load_row<8>(g.bias + int64_t(was.e) * g.out + col_of(j), b[j]);
       }
       bf16_t *y = static_cast<bf16_t *>(g.y) + (was.row0 + row_of(0)) * g.out + col_of(0);
-      each_slot<MN>([&](auto part) {
-        constexpr int i = decltype(part)::value / TN, j = decltype(part)::value % TN;
-        float w[16];
+      each_slot<MN / 2>([&](auto pair) {  // (two parts at a time: their 64 bytes of a row are one line)
+        constexpr int i = decltype(pair)::value * 2 / TN, j0 = decltype(pair)::value * 2 % TN;
+        float w[2][16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) w[q] = acc[i][j][q];
-        arrange(w);
+        for (int m = 0; m < 2; ++m) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) w[q] += b[j][q % 8];
+          for (int q = 0; q < 16; ++q) w[m][q] = acc[i][j0 + m][q];
+          arrange(w[m]);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) w[m][q] += b[j0 + m][q % 8];
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          if (col_of(j) < g.out && row_of(i * TN) + 16 * n < was.valid)
-            store_row<8>(y + (2 * i + n) * down + j * 32, reinterpret_cast<float(&)[8]>(w[8 * n]));
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            if (col_of(j0 + m) < g.out && row_of(i * TN) + 16 * n < was.valid)
+              store_row<8>(y + (2 * i + n) * down + (j0 + m) * 32, reinterpret_cast<float(&)[8]>(w[m][8 * n]));
         __builtin_amdgcn_sched_barrier(0);
       });
     } else {
