@@ -46,8 +46,14 @@ __device__ __forceinline__ void clear_tail(const LinearArgs &g, const int32_t *_
   clear_bytes(static_cast<char *>(g.y), from * y_bytes, to * y_bytes, i, n);
 }
 
+// ---- few rows ----
+
 // One workgroup per block of 16 MT rows of an expert (found from the offsets) and 8 / wk
-// groups of 16 columns; wk waves share a column group's k and join their sums in order.
+// groups of 16 columns; wk waves share a column group's k, step by step in turn, and join their sums in
+// order. Operands go from memory to registers: the weights' latency decides, and how many waves wait
+// for it at a time (one row of 2048 -> 4096: 3.8 us, 3.6 of them a launch's). Four steps asked for ahead, of
+// two column groups a wave, were slower (8 experts of 4096 -> 4096, one row each, 27 us against 21): the L1 takes
+// one request for each row's 64 bytes of codes, and as many for its scales.
 constexpr int kRowThreads = 512;
 template <int MT>
 __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(MxLinearArgs m, const int32_t *__restrict__ offsets,
@@ -83,7 +89,6 @@ __global__ __launch_bounds__(kRowThreads) void mx_rows_kernel(MxLinearArgs m, co
     acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   const int blocks_k = g.in / 32;
-#pragma unroll 2
   for (int b0 = slice * 4; b0 < blocks_k; b0 += wk * 4) {
     const int b = b0 + q;
     // past the row's end (half a step): codes of 0 and scales of 1
@@ -168,6 +173,11 @@ hipError_t launch_rows_mt(const MxLinearPlan &p, const MxLinearArgs &m, const in
 // share of that work, each closed by a scheduling barrier. The 16-byte pieces of a row lie at
 // piece ^ (row / 4 % 4), so that sixteen rows of one piece fill all banks.
 // HALF: the last K-step is half (in % 128 = 64).
+//
+// 64 x 64 is for experts of few rows and reads their weights at 5.5 to 6 TB/s (128 experts of 2048 -> 1536, one
+// row each: 213 MB in 37.5 us). 128 x 128 takes 620 cycles a K-step with two workgroups on a CU (2.5 PFLOP/s at
+// 8 x 4096 rows of 4096 -> 4096), twice the time of its MFMA alone: half lines of operands, and twice the requests a
+// product that the 256 x 256 tile has. Four waves alone on a CU take 1100 cycles, most of it latency.
 template <int I, typename F>
 __device__ __forceinline__ void each_slot(F &&f) {
   if constexpr (I > 0) {
@@ -507,6 +517,11 @@ __device__ __forceinline__ int lane_again() {
 // step's operands, of the next tile too. Operands go to LDS without registers, in whole 128-byte lines: in
 // half lines (steps of 128) a step needed twice the requests, and the L1 held all eight waves up. The
 // scales of four steps come together, 32 bytes a row, into two panels in turn.
+//
+// A step's 64 MFMAs a SIMD take 2410 cycles when nothing else is done (37.7 each; 1.7 to 1.8 GHz under this load).
+// It takes 3320 to 3430 (16384 rows of 4096 -> 28672: 3.15 PFLOP/s; MFMAs alone reach 5.5 to 6.2): 360 are
+// the scales' requests, 450 operands that are not in the XCD's L2, the rest the stores of other CUs' tiles. A tile's
+// epilogue takes 10000 besides.
 constexpr int kStreamM = 256, kStreamN = 256, kStreamK = 256;
 constexpr int kStreamRows = kStreamM + kStreamN, kStreamStage = kStreamRows * 128, kStreamPanel = kStreamRows * 32;
 
