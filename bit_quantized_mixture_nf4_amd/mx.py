@@ -87,8 +87,8 @@ def mx4_values(q, dtype=torch.bfloat16):
     if dtype not in _DTYPES:
         raise ValueError("dtype must be float32 or bfloat16")
     out = torch.empty(q.rows, q.K, dtype=dtype, device=dev)
-    if q.rows:  # (as a stack of one expert)
-        c = E4bStack(q.codes.data_ptr(), None, 1, q.rows, q.K, 32, CODEBOOKS["mxfp4"], q.scales.data_ptr())
+    if q.rows:  # (as a stack of so many experts of one row, of which there may be as many as rows)
+        c = E4bStack(q.codes.data_ptr(), None, q.rows, 1, q.K, 32, CODEBOOKS["mxfp4"], q.scales.data_ptr())
         _run("e4b_dequantize_nf4", dev, ctypes.byref(c), _DTYPES[dtype], out.data_ptr())
     return out
 

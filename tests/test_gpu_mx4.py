@@ -208,6 +208,22 @@ def test_gated_gradient_by_differences():
 # ---- the product ----
 
 
+@pytest.mark.parametrize("is_gated", [False, True])
+def test_rows_beyond_32_bits(is_gated):
+    """More than 2^32 values: the last rows have the bits that they have alone."""
+    announce(f"mx rows beyond 32 bits gated={is_gated}")
+    n, K = 4200007, 1088
+    x = torch.empty(n, K * (1 + is_gated), device=DEV, dtype=torch.bfloat16).normal_()
+    q = e4b.mx4_rows(x, gated=is_gated)
+    alone = e4b.mx4_rows(x[-24:].clone(), gated=is_gated)
+    assert torch.equal(q.codes[-24:], alone.codes) and torch.equal(q.scales[-24:], alone.scales)
+    v = e4b.mx4_values(q)
+    assert torch.equal(bits(v[-24:]), bits(e4b.mx4_values(alone)))
+    if is_gated:
+        g = e4b.mx4_rows_backward(x, v)
+        assert torch.equal(bits(g[-24:]), bits(e4b.mx4_rows_backward(x[-24:].clone(), v[-24:].clone())))
+
+
 def _stack(E, out, inn, seed, lo=118, hi=123):
     rng = np.random.default_rng(seed)
     packed = rng.integers(0, 256, (E, out * inn // 2), dtype=np.uint8)
@@ -602,3 +618,42 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for i, (p, q) in enumerate(zip(out, want)):
             assert torch.equal(bits(p), bits(q)), (rep, i)
+
+
+@pytest.mark.parametrize("E,rows,inn,out", [(1, 3, 256, 64), (6, 60, 192, 640), (3, 900, 320, 2000), (4, 5000, 128, 520),
+                                            (4, 12000, 768, 2048)])
+def test_product_captured_in_every_tiling(E, rows, inn, out):
+    """New rows and new offsets between replays; both graphs of a workspace."""
+    announce(f"mx product in a graph E={E} rows={rows} {inn}->{out}")
+    rng = np.random.default_rng(rows)
+    stack, _ = _stack(E, out, inn, 4)
+    q = e4b.mx4_rows(dev(rng.standard_normal((rows, inn)), torch.bfloat16))
+    off = torch.zeros(E + 1, device=DEV, dtype=torch.int32)
+    bias = dev(rng.standard_normal((E, out)), torch.float32)
+    ws = torch.empty(max(256, e4b.mx_linear_workspace_bytes(stack, rows)), device=DEV, dtype=torch.uint8)
+    run = lambda: e4b.mx_linear(stack, q, offsets=off, bias=bias, act="relu", save=True, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out_t = run()
+        graphs.append((graph, out_t))
+    for rep in range(4):
+        new = e4b.mx4_rows(dev(rng.standard_normal((rows, inn)), torch.bfloat16))
+        q.codes.copy_(new.codes)
+        q.scales.copy_(new.scales)
+        off.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(_counts(E, rows - rep, rng))]).astype(np.int32)))
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        for _, got in graphs:
+            for a, b in zip(got, want):
+                assert torch.equal(bits(a), bits(b)), rep
