@@ -114,22 +114,24 @@ __device__ __forceinline__ void write_losses(const BalanceArgs &g, int s, const 
   g.z[s] = float(double(t.z) * inv);
 }
 
-// One workgroup per slot (and, behind the slots, per 256 tokens that may lie outside every
-// sequence): a chunk of at most g.chunk tokens of one sequence, 256 / L of them at a time.
+// One workgroup per slot (and, behind the slots, per so many threads' tokens that may lie outside every
+// sequence): a chunk of at most g.chunk tokens of one sequence, kThreads / L of them at a time. (Half as many chunks of
+// twice the threads take the same time here, and the join half.)
+constexpr int balance_threads(bool one) { return one ? 256 : 512; }
 template <int L, int PER, int VEC, bool ONE>
-__global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
-  constexpr int kGroups = 256 / L;
-  __shared__ float s_prob[4][kMaxE];
+__global__ __launch_bounds__(balance_threads(ONE)) void balance_kernel(BalanceArgs g) {
+  constexpr int kThreads = balance_threads(ONE), kGroups = kThreads / L, kWaves = kThreads / 64;
+  __shared__ float s_prob[kWaves][kMaxE];
   __shared__ int32_t s_counts[kMaxE];
-  __shared__ float s_z[4];
-  __shared__ int32_t s_n[4];
-  __shared__ double s_dot[4];
+  __shared__ float s_z[kWaves];
+  __shared__ int32_t s_n[kWaves];
+  __shared__ double s_dot[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int s = 0;
   int32_t lo = 0, hi = int32_t(g.T);
   if (!ONE) {
     if (int64_t(blockIdx.x) >= g.slots) {
-      const int64_t t = (int64_t(blockIdx.x) - g.slots) * 256 + tid;
+      const int64_t t = (int64_t(blockIdx.x) - g.slots) * kThreads + tid;
       if (t < g.T && (t < first_token(g, 0) || t >= first_token(g, g.S))) g.lse[t] = -INFINITY;
       return;
     }
@@ -142,7 +144,7 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
     lo = int32_t(from);
     hi = int32_t(min(int64_t(hi), from + g.chunk));
   }
-  for (int e = tid; e < g.E; e += 256) s_counts[e] = 0;
+  for (int e = tid; e < g.E; e += kThreads) s_counts[e] = 0;
   __syncthreads();
   float prob[PER][VEC], z = 0.0f;
   int32_t n = 0;
@@ -200,8 +202,10 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
   }
   __syncthreads();
   double dot = 0.0;
-  for (int e = tid; e < g.E; e += 256) {
-    const float p = (s_prob[0][e] + s_prob[1][e]) + (s_prob[2][e] + s_prob[3][e]);
+  for (int e = tid; e < g.E; e += kThreads) {
+    float p = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) p += s_prob[w][e];
     if (ONE) {
       g.prob[e] = p;
       g.counts[e] = s_counts[e];
@@ -212,14 +216,23 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
       g.part_counts[at] = s_counts[e];
     }
   }
-  z = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-  n = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+  z = 0.0f;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    z += s_z[w];
+    n += s_n[w];
+  }
   if (ONE) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
     if (lane == 0) s_dot[wave] = dot;
     __syncthreads();
-    if (tid == 0) write_losses(g, 0, Total{n, z, (s_dot[0] + s_dot[1]) + (s_dot[2] + s_dot[3])});
+    if (tid == 0) {
+      dot = 0.0;
+      for (int w = 0; w < kWaves; ++w) dot += s_dot[w];
+      write_losses(g, 0, Total{n, z, dot});
+    }
   } else if (tid == 0) {
     g.part_z[blockIdx.x] = z;
     g.part_tokens[blockIdx.x] = n;
@@ -228,7 +241,7 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs g) {
 
 // One workgroup per sequence: its chunks' sums, in order. A thread takes VEC experts of every so-many-th chunk,
 // kJoinAhead chunks at a time: waiting for one row after the other took 28 us for 512 chunks of 128
-// experts (16384 tokens, whose own sums take 7), so it takes 9.
+// experts, so they take 9, and the 256 chunks of 16384 tokens (whose own sums take 7) 6.
 constexpr int kJoinThreads = 1024, kJoinAhead = 8;
 template <int VEC>
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs g, int cols) {
@@ -444,7 +457,7 @@ extern "C" e4b_status e4b_moe_balance(const e4b_balance *b, const float *logits,
   }
   if (!need) {
     E4B_TRY(by_experts(a.E, [&](auto l, auto per, auto vec) {
-      hipLaunchKernelGGL((balance_kernel<l(), per(), vec(), true>), dim3(1), dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((balance_kernel<l(), per(), vec(), true>), dim3(1), dim3(balance_threads(true)), 0, stream, a);
     }));
     return E4B_OK;
   }
@@ -454,9 +467,10 @@ extern "C" e4b_status e4b_moe_balance(const e4b_balance *b, const float *logits,
   w += (size_t(a.slots) * size_t(a.E) * 8 + 255) / 256 * 256;
   a.part_z = reinterpret_cast<float *>(w);
   a.part_tokens = reinterpret_cast<int32_t *>(w) + a.slots;
-  const int64_t grid = a.slots + (a.cu ? (a.T + 255) / 256 : 0);
+  const int64_t grid = a.slots + (a.cu ? (a.T + balance_threads(false) - 1) / balance_threads(false) : 0);
   E4B_TRY(by_experts(a.E, [&](auto l, auto per, auto vec) {
-    hipLaunchKernelGGL((balance_kernel<l(), per(), vec(), false>), dim3(uint32_t(grid)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((balance_kernel<l(), per(), vec(), false>), dim3(uint32_t(grid)),
+                       dim3(balance_threads(false)), 0, stream, a);
   }));
   const int vec = a.E % 4 == 0 ? 4 : 1;
   int cols = 1;

@@ -191,9 +191,9 @@ e4b_status plan_balance(const e4b_balance *b, BalanceArgs *a) {
   a->S = int32_t(b->sequences);
   a->cu = b->cu_tokens;
   a->mask = b->token_mask;
-  // two workgroups to a CU where there are tokens for them
-  a->chunk = int32_t((b->T + 511) / 512 + 15) / 16 * 16;
-  if (a->chunk < 16) a->chunk = 16;
+  // a workgroup of 512 threads to a CU where there are tokens for them
+  a->chunk = int32_t((b->T + 255) / 256 + 31) / 32 * 32;
+  if (a->chunk < 32) a->chunk = 32;
   if (!a->cu && b->T <= kBalanceOne) a->chunk = int32_t(kBalanceOne);
   a->slots = b->T / a->chunk + a->S;
   return E4B_OK;
