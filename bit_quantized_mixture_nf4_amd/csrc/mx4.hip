@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t magnitude(const float (&v)[8]) {
 }
 
 // e^a of full relative precision, |a| up to kFar: the product a log2 e is off by half a step of its own, which
-// the second term adds back.
+// the second term adds back. (Down to -128 the power leaves fp32's range; far beyond, the product does.)
 constexpr float kFar = 64.0f;
 __device__ __forceinline__ float exponential(float a) {
   const float t = a * 1.4426950408889634f;
@@ -180,7 +180,8 @@ __global__ __launch_bounds__(256) void mx4_gated_bwd_kernel(const T *__restrict_
       u[q] = float(double(ga[q]) * silu64(gd));
       continue;
     }
-    const float e = exponential(-fabsf(g[q])), r = __builtin_amdgcn_rcpf(1.0f + e);
+    // (an argument beyond what `exponential` takes: at -128 the power is 0 already. A NaN stays one.)
+    const float a = -fabsf(g[q]), e = exponential(a < -128.0f ? -128.0f : a), r = __builtin_amdgcn_rcpf(1.0f + e);
     const float s = neg ? e * r : r, rest = neg ? r : e * r;  // 1 - s, without a difference
     gs = g[q] * s;
     slope = e == 0.0f ? s : s * fmaf(g[q], rest, 1.0f);  // (an infinite g times 0)

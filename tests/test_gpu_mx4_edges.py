@@ -1,0 +1,69 @@
+"""GPU tests of the microscaled 4-bit operators where single factors leave fp32's range and the result does not."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_quantized_mixture_nf4_amd as e4b
+from gpu_util import DEV, announce
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def host(t):
+    return t.detach().cpu().double().numpy()
+
+
+def silu_parts(g):
+    """(derivative of silu, the magnitudes of its terms, silu) in 64 bits, with their limits at infinite g."""
+    with np.errstate(invalid="ignore"):
+        e = np.exp(-np.abs(g))
+        s, r = np.where(g < 0, e, 1.0) / (1 + e), np.where(g < 0, 1.0, e) / (1 + e)
+        gr = np.where(r == 0, 0.0, g * r)
+        slope = np.where(s == 0, 0.0, s * (1 + gr))
+        terms = np.where(s == 0, 0.0, s * (1 + np.abs(gr)))
+        return slope, terms, np.where(s == 0, -0.0, g * s)
+
+
+def check_gated_gradient(g, u, ga, dtype):
+    """One value of [g | u] and of the gradient a block, so that none has a neighbour's company. Each factor is
+    off by a few steps (24 U of the terms in all), the result by half a step of its type, or of its least subnormal one."""
+    x = torch.zeros(g.size, 128, device=DEV)
+    grad = torch.zeros(g.size, 64, device=DEV)
+    x[:, 0], x[:, 64], grad[:, 0] = (torch.from_numpy(v.astype(np.float32)).to(DEV) for v in (g, u, ga))
+    x, grad = x.to(dtype), grad.to(dtype)
+    got = host(e4b.mx4_rows_backward(x, grad))
+    g, u, ga = host(x)[:, 0], host(x)[:, 64], host(grad)[:, 0]
+    slope, terms, silu = silu_parts(g)
+    info = torch.finfo(dtype)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = np.stack([ga * u * slope, ga * silu], axis=1)
+        size = np.stack([np.abs(ga * u) * terms, np.abs(ga * silu)], axis=1)
+        err = 24 * U * size + HALF[dtype] * np.abs(want) * (1 + 2.0 ** -6) + info.smallest_normal * info.eps
+        have = got[:, [0, 64]]
+        # what lies beyond the type's largest value by more than its own error is infinite
+        far = np.isinf(want) | (np.abs(want) - err > info.max)
+        near = ~far & (np.abs(want) + err >= info.max)
+        ok = np.where(far, have == np.sign(want) * np.inf, np.abs(have - want) <= err)
+        ok |= np.isnan(want) & np.isnan(have)
+        ok |= near & (np.abs(have) >= info.max * (1 - HALF[dtype]))
+    bad = np.argwhere(~ok)
+    assert not bad.size, (f"{len(bad)} of {ok.size} off, first g={g[bad[0, 0]]} u={u[bad[0, 0]]} grad={ga[bad[0, 0]]}: "
+                          f"{have[tuple(bad[0])]} against {want[tuple(bad[0])]}")
+    assert not np.delete(got, [0, 64], axis=1).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gated_gradient_of_the_largest_gates(dt):
+    """Where silu is the identity, or constant, to the last gate that a type holds, and at infinite ones; a NaN is
+    passed on."""
+    announce(f"gated gradient of the largest gates {dt}")
+    g = np.array([80, 88, 100, 104, 127, 128, 129, 1e4, 1e30, 2.3e38, 2.35e38, 2.37e38, 2.4e38, 3.3e38, np.inf, np.nan,
+                  -1e30, -2.4e38, -3.3e38, -np.inf])
+    u, ga = np.array([1.0, -7.0, 0.375, 0.0, 1e-20, 3e20]), np.array([0.75, -2.0, 1e-30, 0.0])
+    g, u, ga = (v.reshape(-1) for v in np.meshgrid(g, u, ga, indexing="ij"))
+    check_gated_gradient(g, u, ga, DT[dt])
