@@ -185,8 +185,12 @@ __global__ __launch_bounds__(256) void mx4_gated_bwd_kernel(const T *__restrict_
     const float s = neg ? e * r : r, rest = neg ? r : e * r;  // 1 - s, without a difference
     gs = g[q] * s;
     slope = e == 0.0f ? s : s * fmaf(g[q], rest, 1.0f);  // (an infinite g times 0)
-    g[q] = ga[q] * u[q] * slope;
-    u[q] = ga[q] * gs;
+    // The factors in an order that stays in range where the result does: ga u is infinite with a slope down to 2^-92
+    // to follow (|ga| and |u| are above 1 then, and the slope below 1.1), and half of a subnormal g loses its last bit.
+    const float p = ga[q] * u[q];
+    const float dg = fabsf(p) == INFINITY ? ga[q] * slope * u[q] : p * slope;
+    u[q] = fabsf(g[q]) < 0x1p-100f ? ga[q] * g[q] * s : ga[q] * gs;
+    g[q] = dg;
   }
   store_row<8>(out + at, g);
   store_row<8>(out + at + half, u);

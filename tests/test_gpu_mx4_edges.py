@@ -67,3 +67,30 @@ def test_gated_gradient_of_the_largest_gates(dt):
     u, ga = np.array([1.0, -7.0, 0.375, 0.0, 1e-20, 3e20]), np.array([0.75, -2.0, 1e-30, 0.0])
     g, u, ga = (v.reshape(-1) for v in np.meshgrid(g, u, ga, indexing="ij"))
     check_gated_gradient(g, u, ga, DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gated_gradient_of_factors_that_leave_the_range(dt):
+    """grad u, or silu of a least gate, beyond fp32's range or with few bits left in it, and the result within it."""
+    announce(f"gated gradient of factors that leave the range {dt}")
+    g = np.array([-90, -64.5, -64, -63.5, -50, -40, -30, -10, -1.2784645, -1, -0.25, -1e-30, -2e-31, -1e-36, -1e-39, -1e-42,
+                  0.0, -0.0, 1.4e-45, 7e-45, 1e-41, 1e-38, 1e-20, 0.5, 1, 20, 60, 90, 2e38])
+    far = np.array([0.0, 1e-45, 1e-42, 3e-39, 1e-37, 1e-30, 1e-20, 1e-15, 1.0, 1e15, 1e20, 1e30, 3e38])
+    g, u, ga = (v.reshape(-1) for v in np.meshgrid(g, np.concatenate([far, -far]), far, indexing="ij"))
+    check_gated_gradient(g, u, ga, DT[dt])
+
+
+def test_gated_gradient_next_to_such_factors():
+    """The values beside one that takes the way in 64 bits keep their bits."""
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(64, 512, device=DEV, generator=gen)
+    grad = torch.randn(64, 256, device=DEV, generator=gen)
+    want = e4b.mx4_rows_backward(x, grad)
+    at = torch.arange(64, device=DEV)
+    x2, grad2 = x.clone(), grad.clone()
+    x2[at, 3 * at], x2[at, 256 + 3 * at], grad2[at, 3 * at] = -40.0, 1e20, 1e20
+    got = e4b.mx4_rows_backward(x2, grad2)
+    assert got[at, 3 * at].isfinite().all() and got[at, 3 * at].lt(-1e23).all()
+    other = torch.ones_like(got, dtype=torch.bool)
+    other[at, 3 * at] = other[at, 256 + 3 * at] = False
+    assert torch.equal(got[other].view(torch.int32), want[other].view(torch.int32))
