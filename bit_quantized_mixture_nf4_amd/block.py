@@ -130,8 +130,13 @@ class Balance:
     top_k: int
 
 
+def _aligned(t):
+    """``t``, or a copy where a view begins off the library's 16 bytes."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _balance_args(logits, top_k, cu_tokens, token_mask):
-    """(the C descriptor, sequences); what it points to stays the caller's"""
+    """(the C descriptor, sequences, the tensors that it points to)"""
     _need(logits, "logits", torch.float32)
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
@@ -145,8 +150,9 @@ def _balance_args(logits, top_k, cu_tokens, token_mask):
         S = cu_tokens.shape[0] - 1
     if token_mask is not None:
         _need(token_mask, "token_mask", torch.bool, dev, (T,))
-    return E4bBalance(T, E, S, int(top_k), None if cu_tokens is None else cu_tokens.data_ptr(),
-                      None if token_mask is None else token_mask.data_ptr()), S
+    # a batch's part of longer bounds or of a longer mask, mask[a:b], begins anywhere
+    held = _aligned(cu_tokens), _aligned(token_mask)
+    return E4bBalance(T, E, S, int(top_k), *map(_vp, held)), S, held
 
 
 def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=None):
@@ -157,6 +163,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
     [S + 1]: sequence s has tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 and losses of its
     own (None: one sequence of all tokens). ``token_mask`` bool [T], False for tokens that
     are not counted, as padding; nor are those of no sequence and those with logits of -inf throughout.
+    Both may be parts of longer tensors (one that begins off 16 bytes is copied first).
     With N counted tokens and p the softmax of all logits,
     loss = E / (k N^2) sum_e counts_e prob_e (1 for an even use) and
     z_loss = 1 / N sum_t (log sum_e exp l_te)^2; both are 0 for a sequence without a token.
@@ -167,7 +174,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
     if topk_idx.dim() != 2:
         raise ValueError("topk_idx must be [T, k]")
     k = topk_idx.shape[1]
-    b, S = _balance_args(logits, k, cu_tokens, token_mask)
+    b, S, _held = _balance_args(logits, k, cu_tokens, token_mask)
     T, E = logits.shape
     if topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx must have {T} rows, got {topk_idx.shape[0]}")
@@ -185,7 +192,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
 
 def moe_balance_workspace_bytes(logits, top_k, cu_tokens=None):
     """Bytes of ``moe_balance``'s workspace for these arguments."""
-    b, _ = _balance_args(logits, top_k, cu_tokens, None)
+    b, _, _held = _balance_args(logits, top_k, cu_tokens, None)
     return int(load().e4b_moe_balance_workspace_bytes(ctypes.byref(b)))
 
 
@@ -199,7 +206,7 @@ def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=Non
     get ``add`` alone. With ``fwd.counts`` and ``fwd.tokens`` summed over ranks first, the
     gradient is that of the loss over all ranks' tokens.
     """
-    b, S = _balance_args(logits, fwd.top_k, cu_tokens, None)
+    b, S, _held = _balance_args(logits, fwd.top_k, cu_tokens, None)
     T, E = logits.shape
     dev = logits.device
     _need(fwd.counts, "counts", torch.int32, dev, (S, E))
