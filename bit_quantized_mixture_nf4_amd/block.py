@@ -163,7 +163,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
     [S + 1]: sequence s has tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 and losses of its
     own (None: one sequence of all tokens). ``token_mask`` bool [T], False for tokens that
     are not counted, as padding; nor are those of no sequence and those with logits of -inf throughout.
-    Both may be parts of longer tensors (one that begins off 16 bytes is copied first).
+    Both, and ``topk_idx``, may be parts of longer tensors (one that begins off 16 bytes is copied first).
     With N counted tokens and p the softmax of all logits,
     loss = E / (k N^2) sum_e counts_e prob_e (1 for an even use) and
     z_loss = 1 / N sum_t (log sum_e exp l_te)^2; both are 0 for a sequence without a token.
@@ -175,6 +175,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
         raise ValueError("topk_idx must be [T, k]")
     k = topk_idx.shape[1]
     b, S, _held = _balance_args(logits, k, cu_tokens, token_mask)
+    topk_idx = _aligned(topk_idx)
     T, E = logits.shape
     if topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx must have {T} rows, got {topk_idx.shape[0]}")
@@ -201,9 +202,9 @@ def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=Non
     selection held fixed, plus ``add``.
 
     ``fwd`` is ``moe_balance``'s result and ``cu_tokens`` its argument; ``grad_loss`` and
-    ``grad_z`` float32 [S] (None: zeros); ``add`` float32 [T, E], as ``moe_route_backward``
-    gives it; ``out`` the result's place, which may be ``add``. Tokens that are not counted
-    get ``add`` alone. With ``fwd.counts`` and ``fwd.tokens`` summed over ranks first, the
+    ``grad_z`` float32 [S], which may be parts of longer tensors (None: zeros); ``add``
+    float32 [T, E], as ``moe_route_backward`` gives it; ``out`` the result's place, which may
+    be ``add``. Tokens that are not counted get ``add`` alone. With ``fwd.counts`` and ``fwd.tokens`` summed over ranks first, the
     gradient is that of the loss over all ranks' tokens.
     """
     b, S, _held = _balance_args(logits, fwd.top_k, cu_tokens, None)
@@ -216,6 +217,7 @@ def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=Non
                            (out, "out", (T, E))):
         if t is not None:
             _need(t, name, torch.float32, dev, shape)
+    grad_loss, grad_z = _aligned(grad_loss), _aligned(grad_z)
     if out is None:
         out = torch.empty(T, E, dtype=torch.float32, device=dev)
     elif _overlap(out, logits) or (add is not None and _overlap(out, add) and out.data_ptr() != add.data_ptr()):

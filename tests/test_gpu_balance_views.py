@@ -1,4 +1,4 @@
-"""GPU tests of the router's balance on bounds and masks that are parts of longer tensors."""
+"""GPU tests of the router's balance on arguments that are parts of longer tensors."""
 
 import numpy as np
 import pytest
@@ -62,3 +62,17 @@ def test_a_captured_call_reads_the_views_again():
         graph.replay()
         torch.cuda.synchronize()
         assert _same(out, _both(lg2, idx2, cu2[10:].clone(), mask2[5:5 + T].clone())), rep
+
+
+@pytest.mark.parametrize("first", [1, 2, 4, 7])
+def test_parts_of_longer_selections_and_gradients(first):
+    announce(f"balance of selections that begin at {first}")
+    lg, idx, _, cu = _batch(T=203, k=2, seed=3)
+    cu = cu[9:].clamp(max=200)
+    lg, idx = lg[first:first + 196], idx[first:first + 196]
+    f, want = e4b.moe_balance(lg, idx, cu_tokens=cu), e4b.moe_balance(lg, idx.clone(), cu_tokens=cu)
+    assert _same([f.counts, f.prob, f.loss, f.lse], [want.counts, want.prob, want.loss, want.lse])
+    g = torch.randn(2, 16, device=DEV)
+    gl, gz = g[0, first:first + 6], g[1, first:first + 6]
+    assert _same([e4b.moe_balance_backward(f, lg, gl, gz, cu_tokens=cu)],
+                 [e4b.moe_balance_backward(f, lg, gl.clone(), gz.clone(), cu_tokens=cu)])
