@@ -15,14 +15,15 @@ import torch
 
 from . import CODEBOOKS, _need, _vp
 from ._lib import E4bStack, load
-from .block import ACTS, _DTYPES, _linear_args, _overlap, _rows, _run, _workspace
+from .block import ACTS, _DTYPES, _aligned, _linear_args, _overlap, _rows, _run, _workspace
 
 
 @dataclass
 class MxRows:
     """n rows of K values in microscaled 4-bit floats, in the layout of a stored MXFP4
     stack: ``codes`` uint8 [n, K/2] (even element in the high nibble), ``scales`` uint8
-    [n, K/32] (E8M0)."""
+    [n, K/32] (E8M0). Parts of longer rows, codes[a:b] and scales[a:b], are rows too (scales
+    that begin off 16 bytes are copied by each call)."""
 
     codes: torch.Tensor
     scales: torch.Tensor
@@ -88,7 +89,8 @@ def mx4_values(q, dtype=torch.bfloat16):
         raise ValueError("dtype must be float32 or bfloat16")
     out = torch.empty(q.rows, q.K, dtype=dtype, device=dev)
     if q.rows:  # (as a stack of so many experts of one row, of which there may be as many as rows)
-        c = E4bStack(q.codes.data_ptr(), None, q.rows, 1, q.K, 32, CODEBOOKS["mxfp4"], q.scales.data_ptr())
+        scales = _aligned(q.scales)
+        c = E4bStack(q.codes.data_ptr(), None, q.rows, 1, q.K, 32, CODEBOOKS["mxfp4"], scales.data_ptr())
         _run("e4b_dequantize_nf4", dev, ctypes.byref(c), _DTYPES[dtype], out.data_ptr())
     return out
 
@@ -142,9 +144,10 @@ def mx_linear(stack, q, offsets=None, perm=None, bias=None, act="none", residual
             raise ValueError("out must not overlap the rows, nor the residual unless it is the residual")
         y = out
     pre = torch.empty(rows, stack.out, dtype=torch.float32, device=dev) if save else None
+    scales = _aligned(q.scales)
     c = stack.as_c()
     st = ctypes.byref(c)
     ws, at, nbytes = _workspace(workspace, int(load().e4b_mx_linear_workspace_bytes(st, rows)), dev)
-    _run("e4b_mx_linear", dev, st, rows, _vp(offsets), _vp(order), top_k, q.codes.data_ptr(), q.scales.data_ptr(),
+    _run("e4b_mx_linear", dev, st, rows, _vp(offsets), _vp(order), top_k, q.codes.data_ptr(), scales.data_ptr(),
          _vp(bias), ACTS[act], _vp(residual), _DTYPES[out_dtype], y.data_ptr(), _vp(pre), at, nbytes)
     return y, pre

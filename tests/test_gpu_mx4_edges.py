@@ -1,4 +1,5 @@
-"""GPU tests of the microscaled 4-bit operators where single factors leave fp32's range and the result does not."""
+"""GPU tests of the microscaled 4-bit operators at their edges: factors that leave fp32's range where the result
+does not, parts of longer rows."""
 
 import numpy as np
 import pytest
@@ -94,3 +95,21 @@ def test_gated_gradient_next_to_such_factors():
     other = torch.ones_like(got, dtype=torch.bool)
     other[at, 3 * at] = other[at, 256 + 3 * at] = False
     assert torch.equal(got[other].view(torch.int32), want[other].view(torch.int32))
+
+
+@pytest.mark.parametrize("K", [64, 192, 512])
+def test_parts_of_longer_rows(K):
+    """Rows from any one on, with the bits of a copy."""
+    announce(f"mx rows in parts K={K}")
+    gen = torch.Generator(device=DEV).manual_seed(K)
+    q = e4b.mx4_rows(torch.randn(120, K, device=DEV, generator=gen))
+    stack = e4b.quantize(torch.randn(1, 48, K, device=DEV, generator=gen), "mxfp4")
+    for first, n in ((1, 7), (2, 100), (5, 64), (8, 1)):
+        part = e4b.MxRows(q.codes[first:first + n], q.scales[first:first + n])
+        copy = e4b.MxRows(part.codes.clone(), part.scales.clone())
+        assert torch.equal(e4b.mx4_values(part).view(torch.int16), e4b.mx4_values(copy).view(torch.int16))
+        y, want = e4b.mx_linear(stack, part)[0], e4b.mx_linear(stack, copy)[0]
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+        ids = torch.zeros(n, 1, dtype=torch.int32, device=DEV)
+        y = e4b.mx_linear(stack, part, perm=e4b.moe_permute(ids, 1)[1])[0]
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
