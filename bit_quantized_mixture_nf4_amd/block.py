@@ -217,11 +217,13 @@ def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=Non
                            (out, "out", (T, E))):
         if t is not None:
             _need(t, name, torch.float32, dev, shape)
-    grad_loss, grad_z = _aligned(grad_loss), _aligned(grad_z)
     if out is None:
         out = torch.empty(T, E, dtype=torch.float32, device=dev)
-    elif _overlap(out, logits) or (add is not None and _overlap(out, add) and out.data_ptr() != add.data_ptr()):
-        raise ValueError("out must not overlap logits, nor add unless it is add")
+    elif any(t is not None and _overlap(out, t)
+             for t in (logits, fwd.counts, fwd.tokens, fwd.lse, grad_loss, grad_z, cu_tokens)) or (
+            add is not None and _overlap(out, add) and out.data_ptr() != add.data_ptr()):
+        raise ValueError("out must not overlap what the call reads, but that it may be add")
+    grad_loss, grad_z = _aligned(grad_loss), _aligned(grad_z)
     _run("e4b_moe_balance_backward", dev, ctypes.byref(b), logits.data_ptr(), fwd.counts.data_ptr(),
          fwd.tokens.data_ptr(), fwd.lse.data_ptr(), _vp(grad_loss), _vp(grad_z), _vp(add), out.data_ptr())
     return out

@@ -638,7 +638,8 @@ size_t e4b_moe_balance_workspace_bytes(const e4b_balance *b);
  *               call, counts and tokens give the gradient of the loss over the tokens of all
  *   grad_loss, grad_z : device fp32 [sequences], or NULL for zeros
  *   add       : device fp32 [T, E] (the gradient through the routing weights), or NULL
- *   grad_logits : device fp32 [T, E] (written whole); may be add itself, in place
+ *   grad_logits : device fp32 [T, E] (written whole); may be add itself, in place, and must not
+ *               overlap anything else that is read
  * Errors: as e4b_moe_balance. */
 e4b_status e4b_moe_balance_backward(const e4b_balance *b, const float *logits, const int32_t *counts,
                                     const int32_t *tokens, const float *lse, const float *grad_loss,

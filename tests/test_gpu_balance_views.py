@@ -76,3 +76,22 @@ def test_parts_of_longer_selections_and_gradients(first):
     gl, gz = g[0, first:first + 6], g[1, first:first + 6]
     assert _same([e4b.moe_balance_backward(f, lg, gl, gz, cu_tokens=cu)],
                  [e4b.moe_balance_backward(f, lg, gl.clone(), gz.clone(), cu_tokens=cu)])
+
+
+def test_no_place_among_what_is_read():
+    lg, idx, _, _ = _batch(T=40, E=8, k=2)
+    f = e4b.moe_balance(lg, idx)
+    one = torch.ones(1, device=DEV)
+    place = torch.zeros(2, 40, 8, device=DEV)
+    lse = place[0].view(-1)[100:140].copy_(f.lse)
+    inside = e4b.Balance(f.counts, f.tokens, f.prob, f.loss, f.z_loss, lse, f.top_k)
+    counts = e4b.Balance(place[0].view(torch.int32)[3:4].copy_(f.counts), f.tokens, f.prob, f.loss, f.z_loss, f.lse, f.top_k)
+    for call in (lambda: e4b.moe_balance_backward(inside, lg, one, out=place[0]),
+                 lambda: e4b.moe_balance_backward(counts, lg, one, out=place[0]),
+                 lambda: e4b.moe_balance_backward(f, lg, place[0, 5, :1], out=place[0]),
+                 lambda: e4b.moe_balance_backward(f, lg, one, place[0, 39, 7:], out=place[0]),
+                 lambda: e4b.moe_balance_backward(f, lg, one, add=place.view(-1)[8:328].view(40, 8), out=place[0])):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    want = e4b.moe_balance_backward(f, lg, one)
+    assert _same([e4b.moe_balance_backward(f, lg, one, out=place[1])], [want])  # next to them is a place
