@@ -491,7 +491,7 @@ __device__ __forceinline__ void load_to_lds(buffer_t b, uint32_t offset, uint32_
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
                : "v"(offset), "s"(b), "s"(step), "s"(lds)
-               : "memory");
+               : "memory", "m0");
 }
 // The same if `go`, without a branch that the compiler sees: the step around it stays one basic block (behind
 // a branch the compiler gathered the matrix instructions, and copied the fragments).
@@ -502,7 +502,7 @@ __device__ __forceinline__ void load_to_lds_if(int go, buffer_t b, uint32_t offs
       ".Lmx_no_load%=:"
       :
       : "v"(offset), "s"(b), "s"(lds), "s"(go)
-      : "memory", "scc");
+      : "memory", "m0", "scc");
 }
 
 // the lane's number, counted where it is needed: no register holds it meanwhile
