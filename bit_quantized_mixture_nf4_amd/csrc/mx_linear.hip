@@ -344,7 +344,7 @@ __global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxLinearArgs m, const i
   };
   load_scales(0);
   load_step(0, 0);
-  if constexpr (D == 2) load_step(1, min(1, last));
+  load_step(1, min(1, last));
 #pragma unroll
   for (int i = 0; i < R; ++i) store(0, i);
   store_scales(0);
