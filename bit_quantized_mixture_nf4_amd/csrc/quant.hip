@@ -118,7 +118,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t *__restr
   if (g >= ngroups) return;
   const uint32_t d = packed[g];
   // 8 groups of 8 elements per 64-block; 4 per 32-element MX block
-  const float a = scales ? e8m0_value(scales[g >> 2]) : absmax[g >> 3];
+  float a = scales ? e8m0_value(scales[g >> 2]) : absmax[g >> 3];
+  if (scales && scales[g >> 2] == 255) a = NAN;  // (not the infinity that its bits would be)
   float v[8];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {

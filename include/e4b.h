@@ -189,7 +189,7 @@ e4b_status e4b_mx8_rows(const void *x_bf16, int64_t rows, int64_t K, uint8_t *co
  * rounding of the exact product), or its round-to-nearest-even bf16 when
  * dtype == E4B_BF16. [sdist] Experts4bit._dequantize_expert. A BF16 stack
  * gives its stored values (exact in fp32); an MXFP4 stack gives code *
- * 2^(s-127) (exact in both dtypes).
+ * 2^(s-127) (exact in both dtypes), and NaN for a scale of 255.
  *   st    : host descriptor of device buffers
  *   w_out : device [E, out, in] fp32 or bf16 (written)
  * Errors: NULL, SHAPE, BLOCKSIZE, CODEBOOK, DTYPE, ALIGN, HIP. */

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import bit_quantized_mixture_nf4_amd as e4b
+from oracle import mx
 from gpu_util import DEV, announce
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +114,20 @@ def test_parts_of_longer_rows(K):
         ids = torch.zeros(n, 1, dtype=torch.int32, device=DEV)
         y = e4b.mx_linear(stack, part, perm=e4b.moe_permute(ids, 1)[1])[0]
         assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_values_of_every_code_and_scale(dt):
+    """All 16 codes under all 256 scales; 255 is NaN whatever the codes are."""
+    announce(f"mx values of every code and scale {dt}")
+    codes = np.resize(np.arange(256, dtype=np.uint8), (256, 32))  # a row holds 64 values, two blocks
+    codes = np.stack([np.roll(codes[0], s) for s in range(256)])
+    codes[:, :16] = (np.arange(16) * 17)[None, :] ^ (np.arange(256) % 2 * 15)[:, None]
+    scales = np.stack([np.arange(256), np.arange(256)[::-1]], axis=1).astype(np.uint8)
+    q = e4b.MxRows(torch.from_numpy(codes).to(DEV), torch.from_numpy(np.ascontiguousarray(scales)).to(DEV))
+    with np.errstate(over="ignore"):  # 2 to 6 times 2^127, and 4 and 6 times 2^126, are infinite in either type
+        want = mx.mx_rows_values(codes, scales).astype(np.float32)
+    got = host(e4b.mx4_values(q, DT[dt]))
+    bad = np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))
+    assert not bad.size, (f"{len(bad)} of {got.size} off, first under scale {scales[bad[0, 0], bad[0, 1] // 32]}: "
+                          f"{got[tuple(bad[0])]} against {want[tuple(bad[0])]}")
