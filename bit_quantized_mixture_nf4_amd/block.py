@@ -131,8 +131,14 @@ class Balance:
 
 
 def _aligned(t):
-    """``t``, or a copy where a view begins off the library's 16 bytes."""
-    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+    """(``t``, its address), or a copy's where a view begins off the library's 16 bytes"""
+    if t is None:
+        return None, None
+    at = t.data_ptr()
+    if at % 16:
+        t = t.clone()
+        at = t.data_ptr()
+    return t, at
 
 
 def _balance_args(logits, top_k, cu_tokens, token_mask):
@@ -151,8 +157,9 @@ def _balance_args(logits, top_k, cu_tokens, token_mask):
     if token_mask is not None:
         _need(token_mask, "token_mask", torch.bool, dev, (T,))
     # a batch's part of longer bounds or of a longer mask, mask[a:b], begins anywhere
-    held = _aligned(cu_tokens), _aligned(token_mask)
-    return E4bBalance(T, E, S, int(top_k), *map(_vp, held)), S, held
+    cu_tokens, cu = _aligned(cu_tokens)
+    token_mask, mask = _aligned(token_mask)
+    return E4bBalance(T, E, S, int(top_k), cu, mask), S, (cu_tokens, token_mask)
 
 
 def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=None):
@@ -175,7 +182,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
         raise ValueError("topk_idx must be [T, k]")
     k = topk_idx.shape[1]
     b, S, _held = _balance_args(logits, k, cu_tokens, token_mask)
-    topk_idx = _aligned(topk_idx)
+    topk_idx, idx = _aligned(topk_idx)
     T, E = logits.shape
     if topk_idx.shape[0] != T:
         raise ValueError(f"topk_idx must have {T} rows, got {topk_idx.shape[0]}")
@@ -186,7 +193,7 @@ def moe_balance(logits, topk_idx, cu_tokens=None, token_mask=None, workspace=Non
     z = torch.empty(S, dtype=torch.float32, device=dev)
     lse = torch.empty(T, dtype=torch.float32, device=dev)
     ws, at, nbytes = _workspace(workspace, int(load().e4b_moe_balance_workspace_bytes(ctypes.byref(b))), dev)
-    _run("e4b_moe_balance", dev, ctypes.byref(b), logits.data_ptr(), topk_idx.data_ptr(), counts.data_ptr(),
+    _run("e4b_moe_balance", dev, ctypes.byref(b), logits.data_ptr(), idx, counts.data_ptr(),
          tokens.data_ptr(), prob.data_ptr(), loss.data_ptr(), z.data_ptr(), lse.data_ptr(), at, nbytes)
     return Balance(counts, tokens, prob, loss, z, lse, k)
 
@@ -223,9 +230,10 @@ def moe_balance_backward(fwd, logits, grad_loss=None, grad_z=None, cu_tokens=Non
              for t in (logits, fwd.counts, fwd.tokens, fwd.lse, grad_loss, grad_z, cu_tokens)) or (
             add is not None and _overlap(out, add) and out.data_ptr() != add.data_ptr()):
         raise ValueError("out must not overlap what the call reads, but that it may be add")
-    grad_loss, grad_z = _aligned(grad_loss), _aligned(grad_z)
+    grad_loss, gl = _aligned(grad_loss)
+    grad_z, gz = _aligned(grad_z)
     _run("e4b_moe_balance_backward", dev, ctypes.byref(b), logits.data_ptr(), fwd.counts.data_ptr(),
-         fwd.tokens.data_ptr(), fwd.lse.data_ptr(), _vp(grad_loss), _vp(grad_z), _vp(add), out.data_ptr())
+         fwd.tokens.data_ptr(), fwd.lse.data_ptr(), gl, gz, None if add is None else add.data_ptr(), out.data_ptr())
     return out
 
 

@@ -89,8 +89,8 @@ def mx4_values(q, dtype=torch.bfloat16):
         raise ValueError("dtype must be float32 or bfloat16")
     out = torch.empty(q.rows, q.K, dtype=dtype, device=dev)
     if q.rows:  # (as a stack of so many experts of one row, of which there may be as many as rows)
-        scales = _aligned(q.scales)
-        c = E4bStack(q.codes.data_ptr(), None, q.rows, 1, q.K, 32, CODEBOOKS["mxfp4"], scales.data_ptr())
+        _held, scales = _aligned(q.scales)
+        c = E4bStack(q.codes.data_ptr(), None, q.rows, 1, q.K, 32, CODEBOOKS["mxfp4"], scales)
         _run("e4b_dequantize_nf4", dev, ctypes.byref(c), _DTYPES[dtype], out.data_ptr())
     return out
 
@@ -144,10 +144,10 @@ def mx_linear(stack, q, offsets=None, perm=None, bias=None, act="none", residual
             raise ValueError("out must not overlap the rows, nor the residual unless it is the residual")
         y = out
     pre = torch.empty(rows, stack.out, dtype=torch.float32, device=dev) if save else None
-    scales = _aligned(q.scales)
+    _held, scales = _aligned(q.scales)
     c = stack.as_c()
     st = ctypes.byref(c)
     ws, at, nbytes = _workspace(workspace, int(load().e4b_mx_linear_workspace_bytes(st, rows)), dev)
-    _run("e4b_mx_linear", dev, st, rows, _vp(offsets), _vp(order), top_k, q.codes.data_ptr(), scales.data_ptr(),
+    _run("e4b_mx_linear", dev, st, rows, _vp(offsets), _vp(order), top_k, q.codes.data_ptr(), scales,
          _vp(bias), ACTS[act], _vp(residual), _DTYPES[out_dtype], y.data_ptr(), _vp(pre), at, nbytes)
     return y, pre
