@@ -663,7 +663,8 @@ e4b_status e4b_mx4_rows(const void *x, int32_t dtype, int64_t rows, int64_t K, i
                         uint8_t *codes, uint8_t *scales, hipStream_t stream);
 
 /* Gradient of the gated rows, straight through their rounding: of [g | u] from that of
- * silu(g) u. (Rows that are not gated pass their gradient on.)
+ * silu(g) u. (Rows that are not gated pass their gradient on.) At an infinite g the
+ * derivative of silu is its limit, 1 or 0.
  *   x      : device [rows, 2 K] (dtype)
  *   grad   : device [rows, K], bf16 or fp32 (grad_dtype)
  *   grad_x : device [rows, 2 K] (dtype)  (written; must not overlap x or grad)
