@@ -131,3 +131,26 @@ def test_values_of_every_code_and_scale(dt):
     bad = np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))
     assert not bad.size, (f"{len(bad)} of {got.size} off, first under scale {scales[bad[0, 0], bad[0, 1] // 32]}: "
                           f"{got[tuple(bad[0])]} against {want[tuple(bad[0])]}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gated_rows_of_the_largest_gates(dt):
+    """Their codes: silu is the identity there, or nothing; what leaves fp32's range is infinite and its block NaN."""
+    announce(f"gated rows of the largest gates {dt}")
+    g = np.array([100, 127, 128, 129, 1e30, 2.3e38, 2.37e38, 3.3e38, np.inf, np.nan, -100, -128, -1e30, -2.4e38, -np.inf])
+    u = np.array([0.0, 1.0, -0.5, 1.4e-45, 1e-38, 1e-10, 3e20, -3.3e38])
+    g, u = (v.reshape(-1) for v in np.meshgrid(g, u, indexing="ij"))
+    x = np.zeros((g.size, 128), np.float32)
+    x[:, 0], x[:, 64] = g, u  # alone in its block
+    x[:, 32:64], x[:, 96:] = 3.0, np.arange(32)  # and beside others
+    x[:, 37], x[:, 101] = g, u
+    x_d = torch.from_numpy(x).to(DEV).to(DT[dt])
+    xh = host(x_d)
+    with np.errstate(invalid="ignore", over="ignore"):
+        v = silu_parts(xh[:, :64])[2] * xh[:, 64:]
+        v = np.where(np.abs(v) > np.finfo(np.float32).max, np.inf, v)
+    codes, scales = mx.quantize_mx_rows(v)
+    q = e4b.mx4_rows(x_d, gated=True)
+    for got, want, name in ((q.scales, scales, "scales"), (q.codes, codes, "codes")):
+        bad = np.argwhere(got.cpu().numpy() != want)
+        assert not bad.size, (name, g[bad[0, 0]], u[bad[0, 0]], got[tuple(bad[0])].item(), want[tuple(bad[0])])
